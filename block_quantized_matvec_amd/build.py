@@ -22,7 +22,8 @@ ARCH = "gfx950"
 
 SOURCES = ["ft_mmvq_kq.hip", "ft_mmvq_kq_b.hip", "ft_mmvq_kq_c.hip", "ft_mmvq_kq_d.hip", "ft_mmvq_q8k.hip", "ft_mmvq.hip",
            "ft_api.cpp", "ft_quant.hip", "ft_mmvq_mfma.hip", "ft_moe.hip", "ft_moe_fused.hip", "ft_moe_fp4.hip", "ft_grouped.hip",
-           "ft_probe.hip"]
+           "ft_probe.hip", "ft_kv.hip", "ft_attn.hip", "ft_attn_d64.hip", "ft_attn_d96.hip", "ft_attn_d128.hip",
+           "ft_attn_d256.hip", "ft_route.hip"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -10,8 +10,10 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
+#include <map>
 #include <mutex>
-#include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "ft.h"
@@ -26,6 +28,9 @@ constexpr int kBytes[kTypes] = {18, 34, 144, 176, 210, 17, 36, 292, 84, 110, 20,
 bool is_weight(int t) { return (t >= FT_Q4_0 && t <= FT_MXFP4) || (t >= FT_Q2_K && t <= FT_Q5_1); }
 // Q8_0 is a weight format and, with the same block layout, an activation format
 bool is_act(int t) { return t == FT_Q8_1 || t == FT_Q8_K || t == FT_Q8_0; }
+bool is_kv_type(int t) { return t == FT_Q8_0 || t == FT_Q4_0; }
+bool is_float(int t) { return t == FT_F32 || t == FT_F16 || t == FT_BF16; }
+bool float_aligned(const void* p, int t) { return ((uintptr_t)p & (t == FT_F32 ? 3 : 1)) == 0; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 int64_t row_bytes_of(int type, int64_t k) { return k / kElems[type] * kBytes[type]; }
 
@@ -42,11 +47,14 @@ struct Pool {
   std::vector<void*> retired;
 };
 std::mutex g_pool_mu;
-std::unordered_map<hipStream_t, Pool> g_pools;
+// by device too: every device has the null stream
+std::map<std::pair<int, hipStream_t>, Pool> g_pools;
 
 ft_status pool_get(hipStream_t st, size_t bytes, void** out) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return FT_ERR_HIP;
   std::lock_guard<std::mutex> lk(g_pool_mu);
-  Pool& p = g_pools[st];
+  Pool& p = g_pools[{dev, st}];
   if (p.size >= bytes) {
     *out = p.ptr;
     return FT_OK;
@@ -135,6 +143,79 @@ bool grouped_pair(int w, int a) {
   return a == FT_Q8_K && (w == FT_Q4_K || w == FT_Q5_K || w == FT_Q6_K || w == FT_MXFP4);
 }
 
+bool kv_sizes(int64_t page, int64_t heads, int64_t dim) {
+  return (page == 16 || page == 32 || page == 64 || page == 128 || page == 256) && heads >= 1 && heads <= 1024 &&
+         (dim == 64 || dim == 96 || dim == 128 || dim == 256);
+}
+// the cache itself: types, sizes, pools
+ft_status kv_check(const ft_kv_cache* c) {
+  if (!c) return FT_ERR_INVALID_ARG;
+  if (!is_kv_type(c->k_type) || !is_kv_type(c->v_type)) return FT_ERR_UNSUPPORTED;
+  if (!kv_sizes(c->page_size, c->n_kv_head, c->head_dim)) return FT_ERR_SHAPE;
+  if (c->n_pages < 1 || c->n_pages > INT32_MAX) return FT_ERR_SHAPE;
+  if (!c->k_pages || !c->v_pages) return FT_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return FT_ERR_ALIGNMENT;
+  return FT_OK;
+}
+// strides of a [rows][heads][dim] tensor whose rows may not run into each other
+bool strides_ok(int64_t rows, int64_t heads, int64_t dim, int64_t token, int64_t head) {
+  if ((rows > 1 && token < dim) || (heads > 1 && head < dim) || token < 0 || head < 0) return false;
+  const int64_t lim = (int64_t)1 << 40;   // offsets stay far from 63 bits
+  return token <= lim && head <= lim;
+}
+
+KvArgs kv_args(const ft_kv_cache* c, ft_float type, void* k, int64_t k_token, int64_t k_head, void* v,
+               int64_t v_token, int64_t v_head, const int64_t* slots, int64_t t) {
+  KvArgs a = {};
+  a.k_type = c->k_type;
+  a.v_type = c->v_type;
+  a.k_pages = c->k_pages;
+  a.v_pages = c->v_pages;
+  a.n_pages = c->n_pages;
+  a.page = (int)c->page_size;
+  a.heads = (int)c->n_kv_head;
+  a.dim = (int)c->head_dim;
+  a.ftype = type;
+  a.k = k;
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v = v;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.slots = slots;
+  a.t = t;
+  return a;
+}
+
+// Sizes and options of ft_attn_kv into the arguments that the planner needs.
+ft_status attn_sizes(const ft_kv_cache* c, int64_t n_tok, int64_t n_head, int64_t n_seq, int64_t max_kv,
+                     const ft_attn_opts& o, AttnArgs* a) {
+  if (!kv_sizes(c->page_size, c->n_kv_head, c->head_dim)) return FT_ERR_SHAPE;
+  if (n_tok < 0 || n_seq < 0 || max_kv < 0 || o.window < 0 || o.n_shared < 0) return FT_ERR_INVALID_ARG;
+  if (!(o.softcap >= 0.0f) || std::isinf(o.softcap) || !std::isfinite(o.scale)) return FT_ERR_INVALID_ARG;
+  if (o.bidirectional != 0 && o.bidirectional != 1) return FT_ERR_INVALID_ARG;
+  if (n_head < 1 || n_head > 1024 || n_head % c->n_kv_head) return FT_ERR_SHAPE;
+  if (n_tok > (1 << 24) || n_seq > (1 << 20) || max_kv > (1 << 30)) return FT_ERR_SHAPE;
+  if (o.n_shared % c->page_size || o.n_shared > max_kv) return FT_ERR_SHAPE;
+  a->page = (int)c->page_size;
+  a->page_shift = __builtin_ctz((unsigned)a->page);
+  a->n_kv_head = (int)c->n_kv_head;
+  a->dim = (int)c->head_dim;
+  a->n_head = (int)n_head;
+  a->group = (int)(n_head / c->n_kv_head);
+  a->n_tok = (int)n_tok;
+  a->n_seq = (int)n_seq;
+  a->max_kv = (int)max_kv;
+  a->scale = o.scale != 0.0f ? o.scale : 1.0f / std::sqrt((float)c->head_dim);
+  a->softcap = o.softcap;
+  a->causal = !o.bidirectional;
+  a->window = std::min<int64_t>(o.window, 1 << 30);
+  a->slopes = o.slopes;
+  a->prefix_len = o.prefix_len;
+  a->n_shared = (int)o.n_shared;
+  return FT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,6 +233,7 @@ int ft_supported(ft_op op, ft_type w, ft_type act) {
     case FT_OP_MOE_VEC: return moe_pair(w, act);
     case FT_OP_GROUPED: return grouped_pair(w, act);
     case FT_OP_BLOCK_DOTS: return is_weight(w) && is_act(act);
+    case FT_OP_KV_CACHE: return is_kv_type(w) && is_kv_type(act);
   }
   return 0;
 }
@@ -163,7 +245,7 @@ const char* ft_status_str(ft_status s) {
     case FT_ERR_UNSUPPORTED: return "unsupported format combination";
     case FT_ERR_SHAPE: return "shape not supported (block multiple, topk or size limit)";
     case FT_ERR_ALIGNMENT: return "pointer not 16-byte aligned";
-    case FT_ERR_NO_SCRATCH: return "scratch pool too small while capturing";
+    case FT_ERR_NO_SCRATCH: return "scratch too small (pool while capturing, or the given workspace)";
     case FT_ERR_HIP: return "HIP runtime error";
   }
   return "unknown status";
@@ -236,6 +318,142 @@ ft_status ft_moe_route(const float* logits, int64_t t, int64_t n_expert, int top
   if (t == 0) return FT_OK;
   if (!logits || !ids || !w) return FT_ERR_INVALID_ARG;
   return hip_status(ftk_launch_route(logits, t, n_expert, topk, ids, w, hs(stream)));
+}
+
+ft_status ft_moe_route_ex(const void* logits, ft_float type, int64_t t, int64_t n_expert, int64_t ld, int topk,
+                          const ft_route_opts* opts, int32_t* ids, float* w, ft_stream_t stream) {
+  ft_route_opts o = {};
+  if (opts) o = *opts;
+  if (!is_float(type)) return FT_ERR_UNSUPPORTED;
+  if (t < 0 || n_expert < 1 || n_expert > 1024 || t > ((int64_t)1 << 32)) return FT_ERR_SHAPE;
+  if ((o.sigmoid != 0 && o.sigmoid != 1) || (o.no_renorm != 0 && o.no_renorm != 1) || !std::isfinite(o.scale) ||
+      o.group_top < 0 || o.group_top > 2 || (ld < n_expert && t > 1) || ld < 0 || ld > ((int64_t)1 << 30))
+    return FT_ERR_INVALID_ARG;
+  const int64_t groups = o.n_group ? o.n_group : 1;
+  const int64_t keep = o.topk_group ? o.topk_group : groups;
+  if (groups < 1 || groups > 64 || n_expert % groups || keep < 1 || keep > groups) return FT_ERR_SHAPE;
+  if (topk < 1 || topk > 32 || topk > keep * (n_expert / groups)) return FT_ERR_SHAPE;
+  if (t == 0) return FT_OK;
+  if (!logits || !ids || !w) return FT_ERR_INVALID_ARG;
+  if (!float_aligned(logits, type)) return FT_ERR_ALIGNMENT;
+  RouteArgs a = {};
+  a.logits = logits;
+  a.ftype = type;
+  a.ld = ld;
+  a.t = t;
+  a.n_expert = (int)n_expert;
+  a.topk = topk;
+  a.sigmoid = o.sigmoid;
+  a.bias = o.bias;
+  a.n_group = (int)groups;
+  a.topk_group = (int)keep;
+  a.group_top = o.group_top ? o.group_top : 1;
+  a.renorm = !o.no_renorm;
+  a.scale = o.scale != 0.0 ? o.scale : 1.0;
+  a.ids = ids;
+  a.w = w;
+  return hip_status(ftk_launch_route_ex(a, hs(stream)));
+}
+
+size_t ft_kv_page_bytes(ft_type type, int64_t page_size, int64_t n_kv_head, int64_t head_dim) {
+  if (!is_kv_type(type) || !kv_sizes(page_size, n_kv_head, head_dim)) return 0;
+  return (size_t)(page_size * n_kv_head * row_bytes_of(type, head_dim));
+}
+
+ft_status ft_kv_store(const ft_kv_cache* cache, ft_float type, const void* k, int64_t k_token, int64_t k_head,
+                      const void* v, int64_t v_token, int64_t v_head, const int64_t* slots, int64_t t,
+                      ft_stream_t stream) {
+  const ft_status s = kv_check(cache);
+  if (s != FT_OK) return s;
+  if (!is_float(type)) return FT_ERR_UNSUPPORTED;
+  const int64_t H = cache->n_kv_head, D = cache->head_dim;
+  if (t < 0 || !strides_ok(t, H, D, k_token, k_head) || !strides_ok(t, H, D, v_token, v_head))
+    return FT_ERR_INVALID_ARG;
+  if (t > ((int64_t)1 << 24)) return FT_ERR_SHAPE;
+  if (t == 0) return FT_OK;
+  if (!k || !v || !slots) return FT_ERR_INVALID_ARG;
+  if (!float_aligned(k, type) || !float_aligned(v, type) || ((uintptr_t)slots & 7)) return FT_ERR_ALIGNMENT;
+  const KvArgs a = kv_args(cache, type, (void*)k, k_token, k_head, (void*)v, v_token, v_head, slots, t);
+  return hip_status(ftk_launch_kv(a, false, hs(stream)));
+}
+
+ft_status ft_kv_load(const ft_kv_cache* cache, const int64_t* slots, int64_t t, ft_float type, void* k,
+                     int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head, ft_stream_t stream) {
+  const ft_status s = kv_check(cache);
+  if (s != FT_OK) return s;
+  if (!is_float(type)) return FT_ERR_UNSUPPORTED;
+  const int64_t H = cache->n_kv_head, D = cache->head_dim;
+  if (t < 0 || (k && !strides_ok(t, H, D, k_token, k_head)) || (v && !strides_ok(t, H, D, v_token, v_head)))
+    return FT_ERR_INVALID_ARG;
+  if (t > ((int64_t)1 << 24)) return FT_ERR_SHAPE;
+  if (t == 0 || (!k && !v)) return FT_OK;
+  if (!slots) return FT_ERR_INVALID_ARG;
+  if (!float_aligned(k, type) || !float_aligned(v, type) || ((uintptr_t)slots & 7)) return FT_ERR_ALIGNMENT;
+  const KvArgs a = kv_args(cache, type, k, k_token, k_head, v, v_token, v_head, slots, t);
+  return hip_status(ftk_launch_kv(a, true, hs(stream)));
+}
+
+size_t ft_attn_kv_scratch_bytes(const ft_kv_cache* cache, int64_t n_tok, int64_t n_head, int64_t n_seq, int64_t max_kv,
+                                const ft_attn_opts* opts) {
+  ft_attn_opts o = {};
+  if (opts) o = *opts;
+  AttnArgs a = {};
+  if (!cache || attn_sizes(cache, n_tok, n_head, n_seq, max_kv, o, &a) != FT_OK || n_tok == 0 || n_seq == 0) return 0;
+  return align256(ftk_attn_plan(a).scratch);
+}
+
+ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int64_t q_token, int64_t q_head,
+                     int64_t n_tok, int64_t n_head, const int32_t* q_start, const int32_t* kv_len,
+                     const int32_t* table, int64_t table_ld, int64_t n_col, int64_t n_seq, int64_t max_kv, void* out,
+                     int64_t out_token, int64_t out_head, const ft_attn_opts* opts, ft_stream_t stream) {
+  ft_attn_opts o = {};
+  if (opts) o = *opts;
+  ft_status s = kv_check(cache);
+  if (s != FT_OK) return s;
+  if (!is_float(type)) return FT_ERR_UNSUPPORTED;
+  if (n_col < 1 || n_col > INT32_MAX || (n_seq > 1 && table_ld < n_col) || table_ld < 0) return FT_ERR_INVALID_ARG;
+  AttnArgs a = {};
+  // no key lies past the table
+  const int64_t room = std::min<int64_t>(n_col * cache->page_size, 1 << 30);
+  s = attn_sizes(cache, n_tok, n_head, n_seq, std::min(max_kv, room), o, &a);
+  if (s != FT_OK) return s;
+  const int64_t D = cache->head_dim;
+  if (!strides_ok(n_tok, n_head, D, q_token, q_head) || !strides_ok(n_tok, n_head, D, out_token, out_head))
+    return FT_ERR_INVALID_ARG;
+  if (n_tok == 0 || n_seq == 0) return FT_OK;
+  if (!q || !q_start || !kv_len || !table || !out) return FT_ERR_INVALID_ARG;
+  if (!float_aligned(q, type) || !float_aligned(out, type) || (((uintptr_t)q_start | (uintptr_t)kv_len |
+      (uintptr_t)table | (uintptr_t)o.slopes | (uintptr_t)o.prefix_len) & 3) || !aligned16(o.workspace))
+    return FT_ERR_ALIGNMENT;
+  a.k_type = cache->k_type;
+  a.v_type = cache->v_type;
+  a.k_pages = (const uint8_t*)cache->k_pages;
+  a.v_pages = (const uint8_t*)cache->v_pages;
+  a.n_pages = (int)cache->n_pages;
+  a.ftype = type;
+  const int64_t step = type == FT_F32 ? 4 : 8;   // elements in 16 bytes
+  a.q = q;
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.q_vec = aligned16(q) && q_token % step == 0 && q_head % step == 0;
+  a.out = out;
+  a.out_token = out_token;
+  a.out_head = out_head;
+  a.out_vec = aligned16(out) && out_token % step == 0 && out_head % step == 0;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.table = table;
+  a.table_ld = table_ld;
+  a.cols = (int)n_col;
+  const AttnPlan p = ftk_attn_plan(a);
+  if (std::max(p.tiles * p.n_split, p.shared_tiles * p.shared_splits) * a.n_kv_head > INT32_MAX) return FT_ERR_SHAPE;
+  void* base = o.workspace;
+  if (p.scratch && base && o.workspace_bytes < p.scratch) return FT_ERR_NO_SCRATCH;
+  if (p.scratch && !base) {
+    s = pool_get(hs(stream), align256(p.scratch), &base);
+    if (s != FT_OK) return s;
+  }
+  return hip_status(ftk_launch_attn(a, p, base, hs(stream)));
 }
 
 ft_status ft_moe_sort(const int32_t* ids, int64_t t, int topk, int64_t n_expert, int32_t* counts, int32_t* offsets,

@@ -1,0 +1,507 @@
+// ft_attn_kernels.h -- attention over the paged, block-quantized cache: device code
+// and launch templates, instantiated per head dimension in ft_attn_d*.hip.
+//
+// For query row (token i, head h) over the keys j of its sequence:
+//   s_j = scale * q . k_j, then cap * tanh(s_j / cap), then - slope_h |pos_i - j|,
+//   o = sum_j exp(s_j) v_j / sum_j exp(s_j) over the visible keys, 0 if there is none.
+#pragma once
+
+#include "ft_device.h"
+#include "ft_internal.h"
+#include "ft_kv.h"
+
+namespace ftk {
+
+constexpr float LOG2E = 1.44269504088896340736f;
+constexpr int ATTN_STEP = 64;    // keys per step of a wave
+constexpr float NO_MAX = -1e30f; // below every score
+
+// a value of the four lane groups (lanes l, l^16, l^32, l^48) met in all of them
+__device__ __forceinline__ float groups_max(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ uint32_t groups_umax(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max((uint32_t)a[0], (uint32_t)a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max((uint32_t)b[0], (uint32_t)b[1]);
+}
+// over the 16 lanes of a row of the wave
+__device__ __forceinline__ int row_min(int v) {
+  v = min(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, false));
+  v = min(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, false));
+  v = min(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, false));
+  return min(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, false));
+}
+__device__ __forceinline__ int row_max(int v) { return -row_min(-v); }
+
+// ---- codes to fp16 (exact) -------------------------------------------------
+// 0x6400 | u is the fp16 number 1024 + u
+__device__ __forceinline__ h16x2 code_pair(uint32_t biased, float off) {
+  const h16x2 o = {(_Float16)off, (_Float16)off};
+  return __builtin_bit_cast(h16x2, biased) - o;
+}
+__device__ __forceinline__ h16x8 codes8_q8(u32x2 w) {   // eight bytes, code + 128
+  h16x2 p[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    p[2 * i] = code_pair(__builtin_amdgcn_perm(0x64646464u, w[i], 0x04010400u), 1152.0f);
+    p[2 * i + 1] = code_pair(__builtin_amdgcn_perm(0x64646464u, w[i], 0x04030402u), 1152.0f);
+  }
+  return __builtin_bit_cast(h16x8, *(const u32x4*)p);
+}
+__device__ __forceinline__ h16x8 codes8_q4(uint32_t w) {   // eight nibbles, code + 8: nibbles (0, 4), (1, 5), ...
+  h16x2 p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = code_pair(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 1032.0f);
+  return __builtin_bit_cast(h16x8, *(const u32x4*)p);
+}
+// the low (H = 0) or high nibbles of eight bytes: keys 0, 2, 1, 3, 4, 6, 5, 7
+template <int H>
+__device__ __forceinline__ h16x8 codes8_q4_half(u32x2 w) {
+  h16x2 p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    p[i] = code_pair(((w[i >> 1] >> (4 * H + 8 * (i & 1))) & 0x000F000Fu) | 0x64006400u, 1032.0f);
+  return __builtin_bit_cast(h16x8, *(const u32x4*)p);
+}
+
+// Eight numbers as fp16, and (LO) what the rounding left as fp16 too.  The first part
+// passes through a register the compiler cannot look into: it would otherwise round
+// some uses of it from the product's exact value and others from the product's fp32
+// one, and the remainder would belong to the other.
+template <bool LO>
+__device__ __forceinline__ void split8(const float (&p)[8], h16x8& hi, h16x8& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = __builtin_bit_cast(uint32_t, h16x2{(_Float16)p[2 * i], (_Float16)p[2 * i + 1]});
+    if constexpr (LO) {
+      asm("" : "+v"(h[i]));
+      const h16x2 x = __builtin_bit_cast(h16x2, h[i]);
+      l[i] = __builtin_bit_cast(uint32_t, h16x2{(_Float16)(p[2 * i] - (float)x[0]), (_Float16)(p[2 * i + 1] - (float)x[1])});
+    }
+  }
+  hi = __builtin_bit_cast(h16x8, *(const u32x4*)h);
+  if constexpr (LO) lo = __builtin_bit_cast(h16x8, *(const u32x4*)l);
+}
+
+// 2, 3 or 4 words, as aligned as their number allows (unrolled: `words` is known)
+__device__ __forceinline__ void load_words(const uint8_t* p, int words, uint32_t* w) {
+  if (words == 4) {
+    const u32x4 x = *(const u32x4*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = x[i];
+  } else if (words == 2) {
+    const u32x2 x = *(const u32x2*)p;
+    w[0] = x[0];
+    w[1] = x[1];
+  } else {
+    for (int i = 0; i < words; ++i) w[i] = ((const uint32_t*)p)[i];
+  }
+}
+
+// Key blocks (of 64 keys) that some row of a tile can see, in the part [lo, hi) of
+// the keys: a first run [a, b) and a second [c, d); step i is block i + a, then on
+// from c.
+struct AttnSteps {
+  int a, n1, c, total;
+  __device__ __forceinline__ int block(int i) const { return i < n1 ? a + i : c + i - n1; }
+};
+
+__device__ __forceinline__ AttnSteps attn_steps(const AttnArgs& A, int part_lo, int part_hi, int min_pos, int max_pos,
+                                                int max_len, int max_pfx) {
+  AttnSteps s;
+  const int end = min(part_hi, max_len);
+  int hi = A.causal ? min(end, max_pos + 1) : end;
+  int lo = A.window > 0 ? max(part_lo, min_pos - (int)A.window + 1) : part_lo;
+  lo = max(lo, part_lo);
+  const int pfx = min(end, max_pfx);
+  s.a = part_lo / ATTN_STEP;
+  const int b = pfx > part_lo ? (pfx + ATTN_STEP - 1) / ATTN_STEP : s.a;
+  s.n1 = b - s.a;
+  s.c = max(lo / ATTN_STEP, b);
+  const int d = hi > part_lo ? (hi + ATTN_STEP - 1) / ATTN_STEP : s.c;
+  s.total = s.n1 + max(0, d - s.c);
+  return s;
+}
+
+// The sequence whose tiles include tile `tile` when sequence i's tiles start at
+// q_start[i] * G / ROWS + i (64-bit product, floor): a wave counts the starts at or
+// below it.  The starts grow by at least one per sequence and leave room for every
+// sequence's last, partly filled tile.
+__device__ __forceinline__ int seq_of_tile(const AttnArgs& A, int64_t tile, int rows, int lane) {
+  int n = 0;
+  for (int i0 = 0; i0 < A.n_seq; i0 += 64) {
+    const int i = i0 + lane;
+    bool at = false;
+    if (i < A.n_seq) {
+      const int64_t q = min(max(A.q_start[i], 0), A.n_tok);
+      at = q * A.group / rows + i <= tile;
+    }
+    const int c = __popcll(__ballot(at));
+    n += c;
+    if (c < 64) break;
+  }
+  return max(n - 1, 0);
+}
+// the sequence that token `tok` belongs to (shared part: every lane its own)
+__device__ __forceinline__ int seq_of_token(const AttnArgs& A, int tok) {
+  int lo = 0, hi = A.n_seq - 1;   // the last i with q_start[i] <= tok
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (A.q_start[mid] <= tok) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// What one row (of a lane, or of an output) is: its token and head, its position and
+// how many keys it has.
+struct AttnRow {
+  int tok, head;      // head within the KV head's group
+  int pos, len, pfx;
+  bool real;
+};
+__device__ __forceinline__ void row_facts(const AttnArgs& A, int seq, AttnRow& r) {
+  const int q0 = min(max(A.q_start[seq], 0), A.n_tok), q1 = min(max(A.q_start[seq + 1], q0), A.n_tok);
+  r.len = min(max(A.kv_len[seq], 0), A.max_kv);
+  r.pos = r.len - (q1 - q0) + (r.tok - q0);
+  r.pfx = A.prefix_len ? min(max(A.prefix_len[seq], 0), r.len) : 0;
+}
+// Row `at` (0 ..) of a tile that starts at row `first` of sequence `seq`, or of the
+// whole batch in the shared part (seq < 0).  Rows past the end repeat the last one and
+// are not real.
+__device__ __forceinline__ AttnRow attn_row(const AttnArgs& A, int seq, int64_t first, int at) {
+  AttnRow r;
+  int64_t q0 = 0, n = (int64_t)min(max(A.q_start[A.n_seq], 0), A.n_tok) * A.group;
+  if (seq >= 0) {
+    const int s0 = min(max(A.q_start[seq], 0), A.n_tok), s1 = min(max(A.q_start[seq + 1], s0), A.n_tok);
+    q0 = s0;
+    n = (int64_t)(s1 - s0) * A.group;
+  }
+  int64_t i = first + at;
+  r.real = i >= 0 && i < n;
+  i = max((int64_t)0, min(i, n - 1));
+  r.tok = (int)(q0 + i / A.group);
+  r.head = (int)(i % A.group);
+  return r;
+}
+
+__device__ __forceinline__ int page_at(const int32_t* row, int col, int cols, int n_pages) {
+  const int p = row[min(col, cols - 1)];
+  return min(max(p, 0), n_pages - 1);   // ids outside the pool are clamped, never followed
+}
+
+// ---------------------------------------------------------------------------
+// up to 16 query rows per workgroup, its waves splitting the keys
+// ---------------------------------------------------------------------------
+template <int TK, int TV, int NB, bool LO>
+__global__ void __launch_bounds__(256, NB <= 4 ? 2 : 1)
+attn_step_kernel(AttnArgs A) {
+  constexpr int D = NB * 32;
+  constexpr int NW = 4;
+  using C = KvCodes<TK>;
+  constexpr int NG = (NB + C::GROUP - 1) / C::GROUP;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int col = lane & 15, g = lane >> 4;
+  const int hk = blockIdx.x % A.n_kv_head;
+  const int split = (blockIdx.x / A.n_kv_head) % A.n_split;
+  const int64_t tile = blockIdx.x / A.n_kv_head / A.n_split;
+
+  int seq = -1;
+  int64_t first = tile * 16;
+  if (!A.shared_part) {
+    seq = seq_of_tile(A, tile, 16, lane);
+    const int64_t q0 = min(max(A.q_start[seq], 0), A.n_tok);
+    first = (tile - (q0 * A.group / 16 + seq)) * 16;
+  }
+  AttnRow row = attn_row(A, seq, first, col);
+  if (!__ballot(row.real)) return;   // a tile past its sequence's rows
+  row_facts(A, A.shared_part ? seq_of_token(A, row.tok) : seq, row);
+
+  const int min_pos = row_min(row.pos), max_pos = row_max(row.pos);
+  const int min_len = row_min(row.len), max_len = row_max(row.len);
+  const int min_pfx = row_min(row.pfx), max_pfx = row_max(row.pfx);
+  const int part_lo = A.shared_part ? 0 : A.n_shared, part_hi = A.shared_part ? A.n_shared : A.max_kv;
+  const AttnSteps steps = attn_steps(A, part_lo, part_hi, min_pos, max_pos, max_len, max_pfx);
+  const int s_end = min(steps.total, (split + 1) * A.split_steps);
+  const int32_t* pages = A.table + (int64_t)max(seq, 0) * A.table_ld;
+
+  // the rows' q: a power of two brings the largest element of a row to [2^10, 2^11), so
+  // that an fp16 (and, for fp32, a second one of the remainder) holds every element to
+  // 2^-24 of the largest; the power returns with the score's factor
+  const int head = hk * A.group + row.head;
+  h16x8 qh[NB], ql[LO ? NB : 1];
+  float c1;
+  {
+    float x[NB][8], amax = 0.0f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      kv_load8(A.ftype, A.q, row.tok * A.q_token + head * A.q_head + 32 * b + 8 * g, A.q_vec, x[b]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
+    }
+    amax = groups_max(amax);
+    const int ex = amax > 0.0f && amax < INFINITY ? min(max(11 - __builtin_amdgcn_frexp_expf(amax), -120), 120) : 0;
+    const float up = __builtin_ldexpf(1.0f, ex);
+    c1 = A.scale * __builtin_ldexpf(1.0f, -ex);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[b][e] *= up;
+      split8<LO>(x[b], qh[b], ql[LO ? b : 0]);
+    }
+  }
+  const float slope = A.slopes ? A.slopes[head] * LOG2E : 0.0f;
+  const bool capped = A.softcap > 0.0f;
+  const float c0 = capped ? c1 / A.softcap : c1 * LOG2E, cap = A.softcap * LOG2E;
+
+  float m = NO_MAX, l = 0.0f;
+  f32x4 o[2 * NB];
+#pragma unroll
+  for (int i = 0; i < 2 * NB; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int page_mask = A.page - 1;
+  const int hb_k = kv_head_bytes(TK, D, A.page), hb_v = kv_head_bytes(TV, D, A.page);
+  const int cb_k = kv_code_bytes(TK, D, A.page), cb_v = kv_code_bytes(TV, D, A.page);
+  const int64_t pb_k = (int64_t)A.n_kv_head * hb_k, pb_v = (int64_t)A.n_kv_head * hb_v;
+
+  for (int i = split * A.split_steps + wave; i < s_end; i += NW) {
+    const int key0 = steps.block(i) * ATTN_STEP;
+    // lane row r = col holds key (r/4)*16 + 4t + r%4 of score tile t, so that the four
+    // scores a lane group gets of every tile are its own 16 keys 16g .. 16g+15
+    const int kk = key0 + (col >> 2) * 16 + (col & 3), kg = key0 + 16 * g;
+    const int pk = page_at(pages, kk >> A.page_shift, A.cols, A.n_pages);
+    const int pg = page_at(pages, kg >> A.page_shift, A.cols, A.n_pages);
+    const uint8_t* kc = A.k_pages + pk * pb_k + (int64_t)hk * hb_k;
+    const uint8_t* ks = A.k_pages + pg * pb_k + (int64_t)hk * hb_k + cb_k + 2 * (kg & page_mask);
+    const uint8_t* vc = A.v_pages + pg * pb_v + (int64_t)hk * hb_v + (kg & page_mask);
+    const uint8_t* vs = A.v_pages + pg * pb_v + (int64_t)hk * hb_v + cb_v + 2 * (kg & page_mask);
+
+    // scores: s[t][i] of key kg + 4t + i
+    f32x4 s[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t kcode[4][NB * C::CB / 4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int j = (kk + 4 * t) & page_mask;
+#pragma unroll
+      for (int p = 0; p < NG; ++p) {
+        constexpr int W = C::GROUP * C::CB / 4;
+        const int words = (NB - p * C::GROUP < C::GROUP ? NB - p * C::GROUP : C::GROUP) * C::CB / 4;
+        load_words(kc + kv_k_at<TK, NB>(A.page, j, p * C::GROUP, g), words, &kcode[t][p * W]);
+      }
+    }
+    uint32_t kd[NB][8], vd[NB][8];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      *(u32x4*)&kd[b][0] = *(const u32x4*)(ks + 2 * b * A.page);
+      *(u32x4*)&kd[b][4] = *(const u32x4*)(ks + 2 * b * A.page + 16);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      *(u32x4*)&vd[b][0] = *(const u32x4*)(vs + 2 * b * A.page);
+      *(u32x4*)&vd[b][4] = *(const u32x4*)(vs + 2 * b * A.page + 16);
+    }
+    constexpr int VT = TV == FT_Q8_0 ? 2 * NB : NB;
+    u32x4 vcode[VT];
+#pragma unroll
+    for (int d = 0; d < VT; ++d) vcode[d] = *(const u32x4*)(vc + (16 * d + col) * A.page);
+
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        h16x8 a;
+        if constexpr (TK == FT_Q8_0) a = codes8_q8(u32x2{kcode[t][2 * b], kcode[t][2 * b + 1]});
+        else a = codes8_q4(kcode[t][b]);
+        f32x4 x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[b], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+        if constexpr (LO) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[b], x, 0, 0, 0);
+        const h16x2 d0 = __builtin_bit_cast(h16x2, kd[b][2 * t]), d1 = __builtin_bit_cast(h16x2, kd[b][2 * t + 1]);
+        s[t][0] = fmaf((float)d0[0], x[0], s[t][0]);
+        s[t][1] = fmaf((float)d0[1], x[1], s[t][1]);
+        s[t][2] = fmaf((float)d1[0], x[2], s[t][2]);
+        s[t][3] = fmaf((float)d1[1], x[3], s[t][3]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] *= c0;
+    if (capped) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = cap * tanhf(s[t][e]);
+    }
+    if (A.slopes) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] -= slope * fabsf((float)(row.pos - (kg + 4 * t + e)));
+    }
+    const int last = key0 + ATTN_STEP - 1;
+    const bool all = key0 >= part_lo && last < min(min_len, part_hi) &&
+                     (((!A.causal || last <= min_pos) && (!A.window || key0 > max_pos - (int)A.window)) || last < min_pfx);
+    if (!all) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = kg + 4 * t + e;
+          const bool in = key >= part_lo && key < part_hi && key < row.len &&
+                          (((!A.causal || key <= row.pos) && (!A.window || key > row.pos - (int)A.window)) || key < row.pfx);
+          if (!in) s[t][e] = -INFINITY;
+        }
+      // slots past the sequence may hold anything: their scales count as zero
+      const int end = min(max_len, part_hi);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t keep = (kg + 2 * k < end ? 0xFFFFu : 0u) | (kg + 2 * k + 1 < end ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vd[b][k] &= keep;
+      }
+    }
+    // the step's largest V scale: with C = 29 - its fp16 exponent, exp2(s - m) * d stays
+    // below 2^15 where m is at least the largest score minus C
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 big = {0, 0};
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, vd[b][k] & 0x7FFF7FFFu));
+    const uint32_t vmax = groups_umax(max((uint32_t)big[0], (uint32_t)big[1]));
+    const float lift = (float)(29 - (int)(vmax >> 10));
+    float top = s[0][0];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, s[t][e]);
+    top = groups_max(top);
+    const float mn = fmaxf(m, top - lift);
+    if (__ballot(mn != m)) {
+      const float al = __builtin_amdgcn_exp2f(m - mn);
+      l *= al;
+#pragma unroll
+      for (int i2 = 0; i2 < 2 * NB; ++i2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i2][e] *= al;
+      m = mn;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[t][e] = __builtin_amdgcn_exp2f(s[t][e] - m);
+        l += s[t][e];
+      }
+    // o += V^T p: p times V's scale of (key, block) as fp16 (fp32 rows: and its remainder)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {   // keys 16g + 8h .. + 7
+        float p[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const h16x2 d = __builtin_bit_cast(h16x2, vd[b][4 * h + k]);
+          p[2 * k] = s[2 * h + (k >> 1)][2 * (k & 1)] * (float)d[0];
+          p[2 * k + 1] = s[2 * h + (k >> 1)][2 * (k & 1) + 1] * (float)d[1];
+        }
+        if constexpr (TV == FT_Q4_0) {   // its codes come as keys 0, 2, 1, 3
+          float x = p[1]; p[1] = p[2]; p[2] = x;
+          x = p[5]; p[5] = p[6]; p[6] = x;
+        }
+        h16x8 ph, pl;
+        split8<LO>(p, ph, pl);
+#pragma unroll
+        for (int d2 = 0; d2 < 2; ++d2) {
+          h16x8 a;
+          if constexpr (TV == FT_Q8_0) a = codes8_q8(u32x2{vcode[2 * b + d2][2 * h], vcode[2 * b + d2][2 * h + 1]});
+          else if (d2 == 0) a = codes8_q4_half<0>(u32x2{vcode[b][2 * h], vcode[b][2 * h + 1]});
+          else a = codes8_q4_half<1>(u32x2{vcode[b][2 * h], vcode[b][2 * h + 1]});
+          o[2 * b + d2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph, o[2 * b + d2], 0, 0, 0);
+          if constexpr (LO) o[2 * b + d2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl, o[2 * b + d2], 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  // the waves' states meet in LDS: rows of D floats per wave, and (m, l) per wave and row
+  __shared__ __align__(16) float s_o[NW][16][D + 4];
+  __shared__ float s_m[NW][16], s_l[NW][16];
+  l = groups_sum(l);
+  if (g == 0) {
+    s_m[wave][col] = m;
+    s_l[wave][col] = l;
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * NB; ++i) *(f32x4*)&s_o[wave][col][16 * i + 4 * g] = o[i];
+  __syncthreads();
+  // 16 threads per row, four consecutive elements each at a time
+  const int r = threadIdx.x >> 4, e0 = (threadIdx.x & 15) * 4;
+  float M = s_m[0][r];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) M = fmaxf(M, s_m[w][r]);
+  float f[NW], L = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    f[w] = __builtin_amdgcn_exp2f(s_m[w][r] - M);
+    L += f[w] * s_l[w][r];
+  }
+  const AttnRow out = attn_row(A, seq, first, r);
+  if (!out.real) return;
+  const int oh = hk * A.group + out.head;
+  const int64_t at = (int64_t)out.tok * A.n_head + oh;
+  if (A.part_o) {
+    const int64_t ps = (int64_t)(A.split0 + split) * A.n_tok * A.n_head + at;
+    if ((threadIdx.x & 15) == 0) {
+      A.part_ml[2 * ps] = L > 0.0f ? M : NO_MAX;
+      A.part_ml[2 * ps + 1] = L;
+    }
+    if (!(L > 0.0f)) return;   // the join skips it
+    for (int e = e0; e < D; e += 64) {
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) x += f[w] * *(const f32x4*)&s_o[w][r][e];
+      *(f32x4*)(A.part_o + ps * D + e) = x;
+    }
+    return;
+  }
+  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  for (int e = e0; e < D; e += 64) {
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) x += f[w] * *(const f32x4*)&s_o[w][r][e];
+    const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+    kv_store_n<4>(A.ftype, A.out, out.tok * A.out_token + oh * A.out_head + e, A.out_vec, y);
+  }
+}
+
+template <int TK, int TV, int NB>
+static hipError_t attn_launch(const AttnArgs& a, hipStream_t st) {
+  const unsigned grid = (unsigned)(a.tiles * a.n_split * a.n_kv_head);
+  if (a.ftype == FT_F32) attn_step_kernel<TK, TV, NB, true><<<grid, 256, 0, st>>>(a);
+  else attn_step_kernel<TK, TV, NB, false><<<grid, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int NB>
+static hipError_t attn_pick(const AttnArgs& a, hipStream_t st) {
+  if (a.k_type == FT_Q8_0)
+    return a.v_type == FT_Q8_0 ? attn_launch<FT_Q8_0, FT_Q8_0, NB>(a, st) : attn_launch<FT_Q8_0, FT_Q4_0, NB>(a, st);
+  return a.v_type == FT_Q8_0 ? attn_launch<FT_Q4_0, FT_Q8_0, NB>(a, st) : attn_launch<FT_Q4_0, FT_Q4_0, NB>(a, st);
+}
+
+}  // namespace ftk

@@ -127,3 +127,79 @@ struct GroupedArgs {
   float* y;                // [t*topk][n]
 };
 hipError_t ftk_launch_grouped(const GroupedArgs& a, hipStream_t st);
+
+// paged key/value cache (ft_kv.hip): rows in (load = false) or out; k or v null on a
+// load: that side is not read
+struct KvArgs {
+  int k_type, v_type;
+  void *k_pages, *v_pages;
+  int64_t n_pages;
+  int page, heads, dim;
+  int ftype;               // ft_float of x
+  void *k, *v;
+  int64_t k_token, k_head, v_token, v_head;   // strides in elements
+  const int64_t* slots;
+  int64_t t;
+};
+hipError_t ftk_launch_kv(const KvArgs& a, bool load, hipStream_t st);
+
+// attention over the cache (ft_attn_kernels.h, ft_attn.hip)
+struct AttnArgs {
+  int k_type, v_type;
+  const uint8_t *k_pages, *v_pages;
+  int n_pages, page, page_shift, n_kv_head, dim;
+  int ftype;               // ft_float of q and out
+  const void* q;
+  int64_t q_token, q_head; // strides in elements
+  int q_vec;               // q rows are 16-byte aligned
+  void* out;
+  int64_t out_token, out_head;
+  int out_vec;
+  int n_head, group;       // group = n_head / n_kv_head
+  int n_tok, n_seq;
+  const int32_t* q_start;  // [n_seq + 1]
+  const int32_t* kv_len;   // [n_seq]
+  const int32_t* table;    // [n_seq][table_ld]
+  int64_t table_ld;
+  int cols;
+  int max_kv;              // no key past it is read
+  float scale, softcap;
+  int causal;
+  int64_t window;          // 0: none
+  const float* slopes;     // nullable [n_head]
+  const int32_t* prefix_len;  // nullable [n_seq]
+  int n_shared;            // leading keys that all sequences share; 0: none
+  // set by the planner, per launch
+  int shared_part;         // 1: the rows of all sequences over the shared keys
+  int64_t tiles;
+  int n_split, split_steps, split0;   // splits of the keys; this launch's first partial
+  float* part_o;           // null: results go to out.  [splits][n_tok * n_head][dim]
+  float* part_ml;          // [splits][n_tok * n_head][2]
+};
+struct AttnPlan {
+  int64_t tiles, shared_tiles;
+  int n_split, split_steps, shared_splits, shared_steps;
+  size_t scratch;          // bytes of partial results; 0: none
+};
+AttnPlan ftk_attn_plan(const AttnArgs& a);
+hipError_t ftk_launch_attn(AttnArgs a, const AttnPlan& p, void* scratch, hipStream_t st);
+hipError_t ftk_attn_d64(const AttnArgs& a, hipStream_t st);
+hipError_t ftk_attn_d96(const AttnArgs& a, hipStream_t st);
+hipError_t ftk_attn_d128(const AttnArgs& a, hipStream_t st);
+hipError_t ftk_attn_d256(const AttnArgs& a, hipStream_t st);
+
+// router with scores, bias and groups (ft_route.hip)
+struct RouteArgs {
+  const void* logits;
+  int ftype;
+  int64_t ld, t;
+  int n_expert, topk;
+  int sigmoid;             // 0: softmax over all experts
+  const float* bias;       // nullable [n_expert]
+  int n_group, topk_group, group_top;
+  int renorm;
+  double scale;
+  int32_t* ids;
+  float* w;
+};
+hipError_t ftk_launch_route_ex(const RouteArgs& a, hipStream_t st);

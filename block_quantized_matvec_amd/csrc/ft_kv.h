@@ -1,0 +1,134 @@
+// ft_kv.h -- the paged key/value cache's page layout (include/ft.h defines it) and
+// the element types of the tensors around it, shared by the store, load and
+// attention kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ft.h"
+
+namespace ftk {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+
+// One page head: the codes of `page` keys (D elements each), then the fp16 scales
+// [D/32][page].
+__host__ __device__ constexpr int kv_code_bytes(int type, int dim, int page) {
+  return type == FT_Q8_0 ? dim * page : dim * page / 2;
+}
+__host__ __device__ constexpr int kv_head_bytes(int type, int dim, int page) {
+  return kv_code_bytes(type, dim, page) + dim / 32 * page * 2;
+}
+
+// K codes: the blocks of a key are taken in groups (two of Q8_0, four of Q4_0, the
+// last group may hold fewer); a group's keys lie one after the other, and within a
+// key its four 8-element eighths-of-a-pair lie one after the other with the group's
+// blocks side by side.  Lane group g of a matrix operand (k = 8g .. 8g+7 of a
+// 32-element block) so finds its codes of the whole group in one load.
+template <int T> struct KvCodes;
+template <> struct KvCodes<FT_Q8_0> { static constexpr int GROUP = 2, CB = 8; };   // blocks per group, bytes per 8 codes
+template <> struct KvCodes<FT_Q4_0> { static constexpr int GROUP = 4, CB = 4; };
+template <int T, int NB>
+__host__ __device__ constexpr int kv_group_blocks(int p) {
+  return NB - p * KvCodes<T>::GROUP < KvCodes<T>::GROUP ? NB - p * KvCodes<T>::GROUP : KvCodes<T>::GROUP;
+}
+// byte of the first of codes 8g .. 8g+7 of block b of key j
+template <int T, int NB>
+__host__ __device__ inline int kv_k_at(int page, int j, int b, int g) {
+  constexpr int G = KvCodes<T>::GROUP, CB = KvCodes<T>::CB;
+  const int p = b / G, left = NB - p * G, m = left < G ? left : G;
+  return page * 64 * p + j * 4 * m * CB + g * m * CB + (b - p * G) * CB;
+}
+
+// Eight codes as the cache holds them (each plus 128, or plus 8): Q8_0 in element
+// order; Q4_0 with element e in nibble e/2 + 4*(e%2), so that (w >> 4i) & 0x000F000F
+// is the pair of elements 2i, 2i+1 in the two halves of a register.
+__device__ __forceinline__ u32x2 kv_pack8(const int (&q)[8]) {
+  u32x2 w = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(q[i] + 128) << (8 * (i & 3));
+  return w;
+}
+__device__ __forceinline__ uint32_t kv_pack4(const int (&q)[8]) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w |= (uint32_t)(q[i] + 8) << (4 * ((i >> 1) + 4 * (i & 1)));
+  return w;
+}
+
+// eight consecutive elements of a float tensor; vec: 16-byte aligned
+__device__ __forceinline__ float bf16_value(uint32_t h) { return __uint_as_float(h << 16); }
+__device__ __forceinline__ void kv_load8(int type, const void* base, int64_t at, bool vec, float (&v)[8]) {
+  if (type == FT_F32) {
+    const float* p = (const float*)base + at;
+    if (vec) {
+      const f32x4 a = ((const f32x4*)p)[0], b = ((const f32x4*)p)[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p[i];
+    }
+    return;
+  }
+  const uint16_t* p = (const uint16_t*)base + at;
+  uint32_t h[8];
+  if (vec) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    const u4 a = *(const u4*)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (a[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = p[i];
+  }
+  if (type == FT_BF16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = bf16_value(h[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)h[i]);
+  }
+}
+
+// round to nearest even; a NaN keeps its top bits and stays a NaN
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+  const uint32_t u = __float_as_uint(f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
+  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+__device__ __forceinline__ uint32_t float_bits16(int type, float f) {
+  return type == FT_BF16 ? bf16_bits(f) : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f);
+}
+template <int N>   // N consecutive elements (4 or 8)
+__device__ __forceinline__ void kv_store_n(int type, void* base, int64_t at, bool vec, const float (&v)[N]) {
+  if (type == FT_F32) {
+    float* p = (float*)base + at;
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *(f32x4*)(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) p[i] = v[i];
+    }
+    return;
+  }
+  uint16_t* p = (uint16_t*)base + at;
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = float_bits16(type, v[2 * i]) | (float_bits16(type, v[2 * i + 1]) << 16);
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 2) *(u32x2*)(p + 2 * i) = u32x2{w[i], w[i + 1]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+}  // namespace ftk

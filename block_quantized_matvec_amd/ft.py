@@ -17,7 +17,8 @@ LIB_PATH = os.path.join(_PKG, "libft.so")
 
 TYPES = {"Q4_0": 0, "Q8_0": 1, "Q4_K": 2, "Q5_K": 3, "Q6_K": 4, "MXFP4": 5, "Q8_1": 6, "Q8_K": 7,
          "Q2_K": 8, "Q3_K": 9, "Q4_1": 10, "Q5_0": 11, "Q5_1": 12}
-OPS = {"quantize": 0, "dequant": 1, "mmvq": 2, "moe_vec": 3, "grouped": 4, "block_dots": 5}
+OPS = {"quantize": 0, "dequant": 1, "mmvq": 2, "moe_vec": 3, "grouped": 4, "block_dots": 5, "kv_cache": 6}
+FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 STATUS = {0: "FT_OK", 1: "FT_ERR_INVALID_ARG", 2: "FT_ERR_UNSUPPORTED", 3: "FT_ERR_SHAPE",
           4: "FT_ERR_ALIGNMENT", 5: "FT_ERR_NO_SCRATCH", 6: "FT_ERR_HIP"}
 
@@ -34,6 +35,26 @@ class _MoeOpts(ctypes.Structure):
                 ("tap_hq", ctypes.c_void_p), ("tap_down", ctypes.c_void_p), ("in_hq", ctypes.c_void_p),
                 ("logits", ctypes.c_void_p), ("ids_out", ctypes.c_void_p), ("w_out", ctypes.c_void_p)]
 
+
+class _RouteOpts(ctypes.Structure):
+    _fields_ = [("sigmoid", ctypes.c_int), ("bias", ctypes.c_void_p), ("n_group", ctypes.c_int),
+                ("topk_group", ctypes.c_int), ("group_top", ctypes.c_int), ("no_renorm", ctypes.c_int),
+                ("scale", ctypes.c_double)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k_type", ctypes.c_int), ("v_type", ctypes.c_int), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("n_kv_head", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
+
+
+class _AttnOpts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("bidirectional", ctypes.c_int),
+                ("window", ctypes.c_int64), ("slopes", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+                ("n_shared", ctypes.c_int64), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+_P, _I64 = ctypes.c_void_p, ctypes.c_int64
 
 EXPORTS = {
     "ft_block_elems": (ctypes.c_int, [ctypes.c_int]),
@@ -70,6 +91,17 @@ EXPORTS = {
                                            ctypes.c_void_p]),
     "ft_debug_ceiling": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                         ctypes.c_void_p, ctypes.c_void_p]),
+    "ft_moe_route_ex": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_int, ctypes.POINTER(_RouteOpts),
+                                       _P, _P, _P]),
+    "ft_kv_page_bytes": (ctypes.c_size_t, [ctypes.c_int, _I64, _I64, _I64]),
+    "ft_kv_store": (ctypes.c_int, [ctypes.POINTER(_KvCache), ctypes.c_int, _P, _I64, _I64, _P, _I64, _I64, _P, _I64,
+                                   _P]),
+    "ft_kv_load": (ctypes.c_int, [ctypes.POINTER(_KvCache), _P, _I64, ctypes.c_int, _P, _I64, _I64, _P, _I64, _I64,
+                                  _P]),
+    "ft_attn_kv": (ctypes.c_int, [ctypes.POINTER(_KvCache), ctypes.c_int, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64,
+                                  _I64, _I64, _I64, _P, _I64, _I64, ctypes.POINTER(_AttnOpts), _P]),
+    "ft_attn_kv_scratch_bytes": (ctypes.c_size_t, [ctypes.POINTER(_KvCache), _I64, _I64, _I64, _I64,
+                                                   ctypes.POINTER(_AttnOpts)]),
     "ft_scratch_reserve": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t]),
     "ft_moe_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                                                ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
@@ -184,6 +216,88 @@ def moe_route(logits: torch.Tensor, topk: int, ids: torch.Tensor | None = None, 
     return ids, w
 
 
+def _float_type(t: torch.Tensor, name: str) -> int:
+    try:
+        return FLOATS[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}") from None
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, not {t.device}")
+
+
+def _ints(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+class _on:
+    """The stream for a call on `device`: the caller's, or the current one of that device (which the library
+    then sees as its current device)."""
+
+    def __init__(self, device, stream):
+        self.guard = None
+        if device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        if s.device != self.device:
+            self.__exit__()
+            raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
+        return s.cuda_stream
+
+    def __exit__(self, *_):
+        if self.guard is not None:
+            self.guard.__exit__(None, None, None)
+
+
+def moe_route_ex(logits: torch.Tensor, topk: int, score: str = "softmax", bias: torch.Tensor | None = None,
+                 n_group: int = 1, topk_group: int | None = None, group_top: int = 1, renorm: bool = True,
+                 scale: float = 1.0, ids: torch.Tensor | None = None, w: torch.Tensor | None = None, stream=None):
+    """ids, w of the topk experts per row of logits ((t, n_expert), rows may be strided): score "softmax" (over all
+    experts) or "sigmoid"; the choice by score + bias among the topk_group best of n_group groups (a group's value:
+    the sum of its group_top largest choices); w the scores, over their sum with renorm, times scale."""
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    ty = _float_type(logits, "logits")
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score must be softmax or sigmoid, not {score}")
+    t, e = logits.shape
+    if e > 1 and logits.stride(1) != 1 or (t > 1 and logits.stride(0) < e):
+        raise ValueError("logits must have unit element stride and rows at least n_expert apart")
+    dev = logits.device
+    _same_device(dev, bias=bias, ids=ids, w=w)
+    if bias is not None:
+        _ints(bias, "bias", torch.float32, (e,))
+    if ids is None:
+        ids = torch.empty((t, topk), dtype=torch.int32, device=dev)
+    else:
+        _ints(ids, "ids", torch.int32, (t, topk))
+    if w is None:
+        w = torch.empty((t, topk), dtype=torch.float32, device=dev)
+    else:
+        _ints(w, "w", torch.float32, (t, topk))
+    if not scale:
+        raise ValueError("scale must not be 0")
+    if n_group < 1 or topk_group is not None and topk_group < 1 or group_top < 1:
+        raise ValueError("n_group, topk_group and group_top start at 1")
+    o = _RouteOpts(score == "sigmoid", None if bias is None else bias.data_ptr(), n_group, topk_group or 0, group_top,
+                   not renorm, scale)
+    with _on(dev, stream) as s:
+        _check(lib().ft_moe_route_ex(logits.data_ptr(), ty, t, e, logits.stride(0) if t > 1 else e, topk,
+                                     ctypes.byref(o), ids.data_ptr(), w.data_ptr(), s), "ft_moe_route_ex")
+    return ids, w
+
+
 def moe_sort(ids: torch.Tensor, n_expert: int, stream=None):
     _dev(ids, "ids")
     t, topk = ids.shape
@@ -286,3 +400,152 @@ def scratch_reserve(nbytes: int, stream=None) -> None:
 
 def moe_scratch_bytes(w: str, act: str, n_expert: int, hidden: int, inter: int, t: int, topk: int) -> int:
     return lib().ft_moe_scratch_bytes(TYPES[w], TYPES[act], n_expert, hidden, inter, t, topk)
+
+
+# ---------------------------------------------------------------------------
+# paged, block-quantized key/value cache and the attention over it
+# ---------------------------------------------------------------------------
+def kv_page_bytes(ty: str, page_size: int, n_kv_head: int, head_dim: int) -> int:
+    """Bytes of one page of one side (keys or values) of a cache."""
+    n = lib().ft_kv_page_bytes(TYPES[ty], page_size, n_kv_head, head_dim)
+    if not n:
+        raise FtError(3, f"no cache pages of {ty}, {page_size} tokens, {n_kv_head} heads of {head_dim}")
+    return n
+
+
+class KvCache:
+    """A paged key/value cache: the caller's two page pools (uint8, n_pages * kv_page_bytes each, any shape) and what
+    they hold.  Slot s is token s % page_size of page s // page_size."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_size: int, n_kv_head: int, head_dim: int,
+                 k: str = "Q8_0", v: str = "Q8_0"):
+        kb, vb = (kv_page_bytes(ty, page_size, n_kv_head, head_dim) for ty in (k, v))
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            _dev(t, name)
+            if t.dtype != torch.uint8:
+                raise ValueError(f"{name} must be uint8")
+        n = k_pages.numel() // kb
+        if not n or k_pages.numel() != n * kb or v_pages.numel() != n * vb:
+            raise ValueError(f"the pools hold {k_pages.numel()} and {v_pages.numel()} bytes: want a whole number of "
+                             f"pages, the same for both, of {kb} and {vb} bytes")
+        _same_device(k_pages.device, v_pages=v_pages)
+        self.k_pages, self.v_pages, self.device = k_pages, v_pages, k_pages.device
+        self.k, self.v = k, v
+        self.n_pages, self.page_size, self.n_kv_head, self.head_dim = n, page_size, n_kv_head, head_dim
+        self._c = _KvCache(TYPES[k], TYPES[v], k_pages.data_ptr(), v_pages.data_ptr(), n, page_size, n_kv_head, head_dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_head: int, head_dim: int, k: str = "Q8_0", v: str = "Q8_0",
+              device="cuda") -> "KvCache":
+        """A cache with pools of its own (not cleared: a slot is read only after it was written)."""
+        pools = [torch.empty((n_pages, kv_page_bytes(ty, page_size, n_kv_head, head_dim)), dtype=torch.uint8,
+                             device=device) for ty in (k, v)]
+        return cls(*pools, page_size, n_kv_head, head_dim, k, v)
+
+
+def _rows(t: torch.Tensor, name: str, shape, device, ty: int):
+    """Token and head strides of a (tokens, heads, dim) tensor."""
+    if t.device != device or tuple(t.shape) != tuple(shape) or FLOATS.get(t.dtype) != ty:
+        raise ValueError(f"{name} must be {tuple(shape)} of one float type on {device}, "
+                         f"not {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit element stride")
+    return t.stride(0), t.stride(1)
+
+
+def kv_store(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Quantize k, v ((t, n_kv_head, head_dim), float32, float16 or bfloat16, strided tokens and heads) into the slots
+    (int64 (t,), distinct; a negative one is skipped)."""
+    t = k.shape[0]
+    ty = _float_type(k, "k")
+    dev, shape = cache.device, (t, cache.n_kv_head, cache.head_dim)
+    kt, kh = _rows(k, "k", shape, dev, ty)
+    vt, vh = _rows(v, "v", shape, dev, ty)
+    _same_device(dev, slots=slots)
+    _ints(slots, "slots", torch.int64, (t,))
+    with _on(dev, stream) as s:
+        _check(lib().ft_kv_store(cache._ref, ty, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), t, s),
+               "ft_kv_store")
+
+
+def kv_load(cache: KvCache, slots: torch.Tensor, dtype=torch.float32, k: torch.Tensor | None = None,
+            v: torch.Tensor | None = None, stream=None):
+    """The slots' rows as plain numbers: (k, v), each (t, n_kv_head, head_dim) of dtype, into the given tensors where
+    there are any (whose type then counts).  A negative slot gives zeros."""
+    t = slots.shape[0]
+    dev, shape = cache.device, (t, cache.n_kv_head, cache.head_dim)
+    if k is not None or v is not None:
+        dtype = (k if k is not None else v).dtype
+    if dtype not in FLOATS:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
+    ty = FLOATS[dtype]
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=dev)
+    kt, kh = _rows(k, "k", shape, dev, ty)
+    vt, vh = _rows(v, "v", shape, dev, ty)
+    _same_device(dev, slots=slots)
+    _ints(slots, "slots", torch.int64, (t,))
+    with _on(dev, stream) as s:
+        _check(lib().ft_kv_load(cache._ref, slots.data_ptr(), t, ty, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, s),
+               "ft_kv_load")
+    return k, v
+
+
+def attn_kv_scratch_bytes(cache: KvCache, n_tok: int, n_head: int, n_seq: int, max_kv: int, causal: bool = True,
+                          window: int = 0, prefix: bool = False, n_shared: int = 0) -> int:
+    """Bytes of a workspace for attn_kv at these sizes (prefix: a prefix_len will be given)."""
+    o = _AttnOpts(0.0, 0.0, not causal, window, None, 1 if prefix else None, n_shared, None, 0)
+    return lib().ft_attn_kv_scratch_bytes(cache._ref, n_tok, n_head, n_seq, max_kv, ctypes.byref(o))
+
+
+def attn_kv(cache: KvCache, q: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor,
+            max_kv: int | None = None, out: torch.Tensor | None = None, scale: float | None = None,
+            causal: bool = True, window: int = 0, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+            prefix_len: torch.Tensor | None = None, n_shared: int = 0, workspace: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """Attention of q ((n_tok, n_head, head_dim), strided tokens and heads) over the cache.  table: int32 (n_seq,
+    pages) page ids; kv_len: int32 (n_seq,); q_start: int32 (n_seq + 1,), sequence i's query tokens are
+    q_start[i] .. q_start[i+1] - 1, the newest of its kv_len keys.  max_kv: a bound of kv_len (default: what the table
+    holds).  window: a token sees its last `window` keys; prefix_len (int32 (n_seq,)): leading keys that all tokens
+    see; slopes (float32 (n_head,)): a bias of -slope * distance; n_shared: leading keys that all sequences share
+    (pages of table row 0).  workspace: uint8, attn_kv_scratch_bytes (default: the stream's pool)."""
+    if q.dim() != 3:
+        raise ValueError("q must be (n_tok, n_head, head_dim)")
+    ty = _float_type(q, "q")
+    n_tok, n_head, dim = q.shape
+    dev = cache.device
+    qt, qh = _rows(q, "q", (n_tok, n_head, cache.head_dim), dev, ty)
+    n_seq = kv_len.shape[0]
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_seq or \
+            (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be int32 (n_seq, pages) with unit element stride")
+    cols = table.shape[1]
+    table_ld = table.stride(0) if n_seq > 1 else cols
+    _ints(kv_len, "kv_len", torch.int32, (n_seq,))
+    _ints(q_start, "q_start", torch.int32, (n_seq + 1,))
+    _same_device(dev, table=table, kv_len=kv_len, q_start=q_start, slopes=slopes, prefix_len=prefix_len,
+                 workspace=workspace)
+    if slopes is not None:
+        _ints(slopes, "slopes", torch.float32, (n_head,))
+    if prefix_len is not None:
+        _ints(prefix_len, "prefix_len", torch.int32, (n_seq,))
+    if scale is not None and not scale:
+        raise ValueError("scale must not be 0")
+    if out is None:
+        out = torch.empty((n_tok, n_head, dim), dtype=q.dtype, device=dev)
+    ot, oh = _rows(out, "out", (n_tok, n_head, dim), dev, ty)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    o = _AttnOpts(scale or 0.0, softcap, not causal, window, None if slopes is None else slopes.data_ptr(),
+                  None if prefix_len is None else prefix_len.data_ptr(), n_shared, ws, ws_bytes)
+    with _on(dev, stream) as s:
+        _check(lib().ft_attn_kv(cache._ref, ty, q.data_ptr(), qt, qh, n_tok, n_head, q_start.data_ptr(),
+                                kv_len.data_ptr(), table.data_ptr(), table_ld, cols, n_seq,
+                                cols * cache.page_size if max_kv is None else max_kv, out.data_ptr(), ot, oh,
+                                ctypes.byref(o), s), "ft_attn_kv")
+    return out

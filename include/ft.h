@@ -79,14 +79,20 @@ typedef enum {
   FT_ERR_UNSUPPORTED = 2, /* (op, weight, activation) combination not provided */
   FT_ERR_SHAPE = 3,       /* k not a multiple of the block sizes, topk out of range */
   FT_ERR_ALIGNMENT = 4,   /* a base pointer is not 16-byte aligned */
-  FT_ERR_NO_SCRATCH = 5,  /* the pool is too small and the stream is capturing */
+  FT_ERR_NO_SCRATCH = 5,  /* the pool is too small and the stream is capturing, or the
+                             caller's workspace is too small */
   FT_ERR_HIP = 6          /* a HIP runtime call or kernel launch failed */
 } ft_status;
 
 typedef enum {
   FT_OP_QUANTIZE = 0, FT_OP_DEQUANT = 1, FT_OP_MMVQ = 2, FT_OP_MOE_VEC = 3,
-  FT_OP_GROUPED = 4, FT_OP_BLOCK_DOTS = 5
+  FT_OP_GROUPED = 4, FT_OP_BLOCK_DOTS = 5,
+  FT_OP_KV_CACHE = 6 /* w: the keys' block type, act: the values' */
 } ft_op;
+
+/* element types of the plain tensors around the key/value cache and the scored
+   router (every other call's plain tensors are fp32) */
+typedef enum { FT_F32 = 0, FT_F16 = 1, FT_BF16 = 2 } ft_float;
 
 /* Elements per block (32 or 256) and bytes per block; 0 for an unknown type. */
 int ft_block_elems(ft_type type);
@@ -258,6 +264,117 @@ ft_status ft_debug_block_dots(ft_type w, const void* W, int64_t n, int64_t k,
    the work live).  The caller times the call. */
 ft_status ft_debug_ceiling(int which, const void* buf, int64_t bytes, int64_t iters, void* out,
                            ft_stream_t stream);
+
+/* Router with scores over all experts, a bias for balance and expert groups.
+   logits: [t][n_expert] of `type`, rows ld (elements) apart.  Per token:
+     score_e  = softmax over all experts, or with `sigmoid` 1 / (1 + exp(-x_e));
+     choice_e = score_e + bias_e;
+     with n_group > 1 the experts are n_group consecutive groups of equal size; a
+     group's value is its largest choice (group_top 1) or the sum of its two largest
+     (group_top 2), and only the topk_group groups of largest value stay;
+     ids [t][topk] = the topk largest choices left, slot 0 the largest;
+     w   [t][topk] = score of ids (without the bias), divided by their sum with
+     `renorm`, times scale.
+   Every tie goes to the lower index.  Scores, choices and sums are held in 64 bits,
+   w is rounded to fp32 once.  A logit of -inf has score 0; NaN logits count as -inf
+   when experts are chosen.  1 <= topk <= min(32, topk_group * n_expert / n_group),
+   n_expert <= 1024, n_group <= 64 and a divisor of n_expert, 1 <= topk_group <=
+   n_group.  opts NULL: softmax, no bias, one group, renorm, scale 1. */
+typedef struct {
+  int sigmoid;        /* 0 softmax, 1 sigmoid */
+  const float* bias;  /* nullable [n_expert] */
+  int n_group;        /* 0 = 1 */
+  int topk_group;     /* 0 = n_group */
+  int group_top;      /* 1 or 2 (0 = 1) */
+  int no_renorm;      /* 1: the weights are not divided by their sum */
+  double scale;       /* 0 = 1 */
+} ft_route_opts;
+ft_status ft_moe_route_ex(const void* logits, ft_float type, int64_t t, int64_t n_expert, int64_t ld, int topk,
+                          const ft_route_opts* opts, int32_t* ids, float* w, ft_stream_t stream);
+
+/* Paged key/value cache, its rows quantized in blocks of 32 along head_dim as they
+   are written.  A pool of pages per side; a page holds page_size tokens of every KV
+   head and is [n_kv_head] page heads; slot s is token s % page_size of page
+   s / page_size.  Types FT_Q8_0 and FT_Q4_0 (each side its own), page_size 16, 32,
+   64, 128 or 256, head_dim 64, 96, 128 or 256.  A page takes as many bytes as the
+   same rows in GGUF blocks, in another order.  With P = page_size, NB = head_dim / 32
+   and element e = 32 b + i of token j, a page head is its codes, then the scales, fp16
+   [NB][P]; the code is
+     K, FT_Q8_0: the byte (code + 128) at P*64*(b/2) + j*32*m + (i/8)*8*m + (b%2)*8 + i%8,
+       m the number of blocks in the group b/2 (2; 1 in a last odd group);
+     K, FT_Q4_0: nibble (i%8)/2 + 4*(i%2) (code + 8) of the 32-bit word at P*64*(b/4) +
+       j*16*m + (i/8)*4*m + (b%4)*4, m the number of blocks in the group b/4;
+     V, FT_Q8_0: the byte (code + 128) at e*P + j;
+     V, FT_Q4_0: in the byte at (16*b + i%16)*P + j, low nibble for i < 16, high above.
+   k_pages, v_pages: 16-byte aligned, n_pages * ft_kv_page_bytes each. */
+typedef struct {
+  ft_type k_type, v_type;
+  void* k_pages;
+  void* v_pages;
+  int64_t n_pages;
+  int64_t page_size, n_kv_head, head_dim;
+} ft_kv_cache;
+/* bytes of one page of one side; 0 for a type or size that is not provided */
+size_t ft_kv_page_bytes(ft_type type, int64_t page_size, int64_t n_kv_head, int64_t head_dim);
+
+/* Quantize t tokens' keys and values into the cache.  k, v: [t][n_kv_head][head_dim] of
+   `type`, element stride 1, token and head strides in elements.  slots [t] int64: a
+   negative slot, or one past the pool, writes nothing.  Per block of 32:
+     FT_Q8_0: d = fp16(amax / 127), q = clamp(round_half_away(x / d), -127, 127);
+     FT_Q4_0: d = fp16(m / -8) with m the first element of largest magnitude,
+              q = clamp(round_half_away(x / d), -8, 7);
+   against the stored d (q = 0 where it is 0); d is limited to +-65504.  The slots of
+   one call must be distinct: of two tokens with one slot, each code and scale is one or
+   the other's. */
+ft_status ft_kv_store(const ft_kv_cache* cache, ft_float type, const void* k, int64_t k_token, int64_t k_head,
+                      const void* v, int64_t v_token, int64_t v_head, const int64_t* slots, int64_t t,
+                      ft_stream_t stream);
+/* The rows of t slots as plain numbers d * q, rounded once to `type`.  k or v may be
+   NULL: that side is not read.  A negative slot, or one past the pool, gives zeros. */
+ft_status ft_kv_load(const ft_kv_cache* cache, const int64_t* slots, int64_t t, ft_float type, void* k,
+                     int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head, ft_stream_t stream);
+
+/* Attention of n_tok query tokens over the cache.
+   q, out: [n_tok][n_head][head_dim] of `type`, element stride 1, token and head strides
+   in elements; n_head a multiple of the cache's n_kv_head, KV head h serves query heads
+   h*G .. h*G + G-1.  Sequence i has the query tokens q_start[i] .. q_start[i+1]-1 (its
+   newest, already stored) and kv_len[i] keys; its key j lies in slot j % page_size of page
+   table[i][j / page_size], table rows table_ld apart, n_col pages each.  q_start is
+   [n_seq+1], ascending; kv_len and table are int32.  All of it is on the device: max_kv
+   is the host's bound of kv_len (lengths past it or past the table are cut to it).
+   The query token at position p = kv_len - (number of query tokens) + its index sees key j
+     if j < kv_len and (j <= p, unless `bidirectional`) and (j > p - window, with a window),
+     or if j < kv_len and j < prefix_len[i] (a prefix that all see: prompt or sink tokens).
+   score = scale * q.k; with softcap c, c * tanh(score / c); with slopes, - slopes[head] *
+   |p - j|; out = softmax over the visible keys times v, zeros where there is none.
+   Tokens of no sequence (before q_start[0], from q_start[n_seq] on) are left as they were.
+   n_shared > 0: the first n_shared keys (a multiple of page_size) of every sequence are
+   the pages of table row 0, read once for all sequences; the result is the same up to
+   fp32 rounding.
+   fp32: products of fp16 pairs summed in fp32, about fp32 accuracy; fp16 and bf16: the
+   probabilities times V's scales are rounded to fp16, everything else as for fp32.
+   Page ids outside the pool are clamped.  opts NULL: causal, scale 1/sqrt(head_dim).
+   Scratch (parts of split keys): the stream's pool, or the caller's `workspace` (16-byte
+   aligned, ft_attn_kv_scratch_bytes).  Graphs captured on one stream share its pool: give
+   those that may replay at the same time a workspace each. */
+typedef struct {
+  float scale;               /* 0 = 1/sqrt(head_dim) */
+  float softcap;             /* 0 = none */
+  int bidirectional;         /* 1: keys after the token are seen too */
+  int64_t window;            /* 0 = none */
+  const float* slopes;       /* nullable [n_head] */
+  const int32_t* prefix_len; /* nullable [n_seq] */
+  int64_t n_shared;          /* 0 = none */
+  void* workspace;           /* nullable */
+  size_t workspace_bytes;
+} ft_attn_opts;
+ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int64_t q_token, int64_t q_head,
+                     int64_t n_tok, int64_t n_head, const int32_t* q_start, const int32_t* kv_len,
+                     const int32_t* table, int64_t table_ld, int64_t n_col, int64_t n_seq, int64_t max_kv, void* out,
+                     int64_t out_token, int64_t out_head, const ft_attn_opts* opts, ft_stream_t stream);
+/* scratch bytes ft_attn_kv needs for these sizes and options */
+size_t ft_attn_kv_scratch_bytes(const ft_kv_cache* cache, int64_t n_tok, int64_t n_head, int64_t n_seq, int64_t max_kv,
+                                const ft_attn_opts* opts);
 
 /* Grow the stream's scratch pool to at least `bytes` [P3 review: grow-only
    per-stream pool].  Call before capturing a graph.  The pool is never shrunk;
