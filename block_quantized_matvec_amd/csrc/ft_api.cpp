@@ -446,7 +446,8 @@ ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int
   a.table_ld = table_ld;
   a.cols = (int)n_col;
   const AttnPlan p = ftk_attn_plan(a);
-  if (std::max(p.tiles * p.n_split, p.shared_tiles * p.shared_splits) * a.n_kv_head > INT32_MAX) return FT_ERR_SHAPE;
+  for (const AttnSplit& x : {p.shared, p.tile, p.step})
+    if (x.tiles * x.n_split * a.n_kv_head > INT32_MAX) return FT_ERR_SHAPE;
   void* base = o.workspace;
   if (p.scratch && base && o.workspace_bytes < p.scratch) return FT_ERR_NO_SCRATCH;
   if (p.scratch && !base) {

@@ -44,6 +44,35 @@ __device__ __forceinline__ int row_min(int v) {
 }
 __device__ __forceinline__ int row_max(int v) { return -row_min(-v); }
 
+// c * tanh(x / c) in the units of `cap`; x comes divided by c.
+// EXACT: an odd series below 0.35 (its next term is under 2^-26 of the result), else
+// 1 - 2 / (exp(2x) + 1), within 2^-22.6 absolute; without EXACT the latter throughout
+// (its absolute error is what matters to a score, and 2^-22 * c is far below the
+// rounding of 16-bit probabilities).
+template <bool EXACT>
+__device__ __forceinline__ float capped_score(float x, float cap) {
+  const float t = __builtin_amdgcn_exp2f(x * (2.0f * LOG2E));
+  float y = fmaf(-2.0f, __builtin_amdgcn_rcpf(t + 1.0f), 1.0f);
+  if constexpr (EXACT) {
+    const float q = x * x;
+    float p = fmaf(q, -1382.0f / 155925.0f, 62.0f / 2835.0f);
+    p = fmaf(q, p, -17.0f / 315.0f);
+    p = fmaf(q, p, 2.0f / 15.0f);
+    p = fmaf(q, p, -1.0f / 3.0f);
+    p = fmaf(x * q, p, x);
+    y = fabsf(x) < 0.35f ? p : y;
+  }
+  return cap * y;
+}
+
+// two fp16 numbers of a word (by value: a bit cast of a vector's element would read the
+// vector's first)
+__device__ __forceinline__ h16x2 halves(uint32_t w) { return __builtin_bit_cast(h16x2, w); }
+__device__ __forceinline__ h16x8 join8(const h16x2 (&p)[4]) {
+  return __builtin_shufflevector(__builtin_shufflevector(p[0], p[1], 0, 1, 2, 3), __builtin_shufflevector(p[2], p[3], 0, 1, 2, 3),
+                                 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 // ---- codes to fp16 (exact) -------------------------------------------------
 // 0x6400 | u is the fp16 number 1024 + u
 __device__ __forceinline__ h16x2 code_pair(uint32_t biased, float off) {
@@ -57,13 +86,13 @@ __device__ __forceinline__ h16x8 codes8_q8(u32x2 w) {   // eight bytes, code + 1
     p[2 * i] = code_pair(__builtin_amdgcn_perm(0x64646464u, w[i], 0x04010400u), 1152.0f);
     p[2 * i + 1] = code_pair(__builtin_amdgcn_perm(0x64646464u, w[i], 0x04030402u), 1152.0f);
   }
-  return __builtin_bit_cast(h16x8, *(const u32x4*)p);
+  return join8(p);
 }
 __device__ __forceinline__ h16x8 codes8_q4(uint32_t w) {   // eight nibbles, code + 8: nibbles (0, 4), (1, 5), ...
   h16x2 p[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) p[i] = code_pair(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 1032.0f);
-  return __builtin_bit_cast(h16x8, *(const u32x4*)p);
+  return join8(p);
 }
 // the low (H = 0) or high nibbles of eight bytes: keys 0, 2, 1, 3, 4, 6, 5, 7
 template <int H>
@@ -72,7 +101,7 @@ __device__ __forceinline__ h16x8 codes8_q4_half(u32x2 w) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     p[i] = code_pair(((w[i >> 1] >> (4 * H + 8 * (i & 1))) & 0x000F000Fu) | 0x64006400u, 1032.0f);
-  return __builtin_bit_cast(h16x8, *(const u32x4*)p);
+  return join8(p);
 }
 
 // Eight numbers as fp16, and (LO) what the rounding left as fp16 too.  The first part
@@ -91,8 +120,8 @@ __device__ __forceinline__ void split8(const float (&p)[8], h16x8& hi, h16x8& lo
       l[i] = __builtin_bit_cast(uint32_t, h16x2{(_Float16)(p[2 * i] - (float)x[0]), (_Float16)(p[2 * i + 1] - (float)x[1])});
     }
   }
-  hi = __builtin_bit_cast(h16x8, *(const u32x4*)h);
-  if constexpr (LO) lo = __builtin_bit_cast(h16x8, *(const u32x4*)l);
+  hi = __builtin_bit_cast(h16x8, u32x4{h[0], h[1], h[2], h[3]});
+  if constexpr (LO) lo = __builtin_bit_cast(h16x8, u32x4{l[0], l[1], l[2], l[3]});
 }
 
 // 2, 3 or 4 words, as aligned as their number allows (unrolled: `words` is known)
@@ -165,6 +194,12 @@ __device__ __forceinline__ int seq_of_token(const AttnArgs& A, int tok) {
   return lo;
 }
 
+// query rows of a sequence
+__device__ __forceinline__ int64_t seq_rows(const AttnArgs& A, int seq) {
+  const int q0 = min(max(A.q_start[seq], 0), A.n_tok), q1 = min(max(A.q_start[seq + 1], q0), A.n_tok);
+  return (int64_t)(q1 - q0) * A.group;
+}
+
 // What one row (of a lane, or of an output) is: its token and head, its position and
 // how many keys it has.
 struct AttnRow {
@@ -197,6 +232,24 @@ __device__ __forceinline__ AttnRow attn_row(const AttnArgs& A, int seq, int64_t 
   return r;
 }
 
+// The keys a row sees of the part [lo, hi): key >= lo, and either above < key < below
+// or key < pfx.
+struct AttnSeen {
+  int above, below, pfx;
+};
+__device__ __forceinline__ AttnSeen seen_by(const AttnArgs& A, const AttnRow& r, int part_hi) {
+  AttnSeen s;
+  s.below = min(r.len, part_hi);
+  s.pfx = min(r.pfx, part_hi);
+  if (A.causal) s.below = min(s.below, r.pos + 1);
+  s.above = A.window > 0 ? r.pos - (int)A.window : -1;
+  return s;
+}
+// by bits, not by branches: a select per score
+__device__ __forceinline__ bool sees(const AttnSeen& s, int part_lo, int key) {
+  return (key >= part_lo) & (((key > s.above) & (key < s.below)) | (key < s.pfx));
+}
+
 __device__ __forceinline__ int page_at(const int32_t* row, int col, int cols, int n_pages) {
   const int p = row[min(col, cols - 1)];
   return min(max(p, 0), n_pages - 1);   // ids outside the pool are clamped, never followed
@@ -220,7 +273,11 @@ attn_step_kernel(AttnArgs A) {
 
   int seq = -1;
   int64_t first = tile * 16;
-  if (!A.shared_part) {
+  if (A.step_rows) {   // beside the tile kernel: the sequences of at most step_rows rows
+    seq = (int)(tile / (A.step_rows / 16));
+    first = (tile % (A.step_rows / 16)) * 16;
+    if (seq_rows(A, seq) > A.step_rows) return;
+  } else if (!A.shared_part) {
     seq = seq_of_tile(A, tile, 16, lane);
     const int64_t q0 = min(max(A.q_start[seq], 0), A.n_tok);
     first = (tile - (q0 * A.group / 16 + seq)) * 16;
@@ -233,6 +290,7 @@ attn_step_kernel(AttnArgs A) {
   const int min_len = row_min(row.len), max_len = row_max(row.len);
   const int min_pfx = row_min(row.pfx), max_pfx = row_max(row.pfx);
   const int part_lo = A.shared_part ? 0 : A.n_shared, part_hi = A.shared_part ? A.n_shared : A.max_kv;
+  const AttnSeen seen = seen_by(A, row, part_hi);
   const AttnSteps steps = attn_steps(A, part_lo, part_hi, min_pos, max_pos, max_len, max_pfx);
   const int s_end = min(steps.total, (split + 1) * A.split_steps);
   const int32_t* pages = A.table + (int64_t)max(seq, 0) * A.table_ld;
@@ -245,9 +303,9 @@ attn_step_kernel(AttnArgs A) {
   float c1;
   {
     float x[NB][8], amax = 0.0f;
+    kv_load_row<NB>(A.ftype, A.q, row.tok * A.q_token + head * A.q_head + 8 * g, A.q_vec, x);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      kv_load8(A.ftype, A.q, row.tok * A.q_token + head * A.q_head + 32 * b + 8 * g, A.q_vec, x[b]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
     }
@@ -328,7 +386,7 @@ attn_step_kernel(AttnArgs A) {
         else a = codes8_q4(kcode[t][b]);
         f32x4 x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[b], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
         if constexpr (LO) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[b], x, 0, 0, 0);
-        const h16x2 d0 = __builtin_bit_cast(h16x2, kd[b][2 * t]), d1 = __builtin_bit_cast(h16x2, kd[b][2 * t + 1]);
+        const h16x2 d0 = halves(kd[b][2 * t]), d1 = halves(kd[b][2 * t + 1]);
         s[t][0] = fmaf((float)d0[0], x[0], s[t][0]);
         s[t][1] = fmaf((float)d0[1], x[1], s[t][1]);
         s[t][2] = fmaf((float)d1[0], x[2], s[t][2]);
@@ -343,13 +401,13 @@ attn_step_kernel(AttnArgs A) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] = cap * tanhf(s[t][e]);
+        for (int e = 0; e < 4; ++e) s[t][e] = capped_score<LO>(s[t][e], cap);
     }
     if (A.slopes) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] -= slope * fabsf((float)(row.pos - (kg + 4 * t + e)));
+        for (int e = 0; e < 4; ++e) s[t][e] -= slope * fabsf((float)(row.pos - kg) - (float)(4 * t + e));
     }
     const int last = key0 + ATTN_STEP - 1;
     const bool all = key0 >= part_lo && last < min(min_len, part_hi) &&
@@ -358,12 +416,7 @@ attn_step_kernel(AttnArgs A) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = kg + 4 * t + e;
-          const bool in = key >= part_lo && key < part_hi && key < row.len &&
-                          (((!A.causal || key <= row.pos) && (!A.window || key > row.pos - (int)A.window)) || key < row.pfx);
-          if (!in) s[t][e] = -INFINITY;
-        }
+        for (int e = 0; e < 4; ++e) s[t][e] = sees(seen, part_lo, kg + 4 * t + e) ? s[t][e] : -INFINITY;
       // slots past the sequence may hold anything: their scales count as zero
       const int end = min(max_len, part_hi);
 #pragma unroll
@@ -415,7 +468,7 @@ attn_step_kernel(AttnArgs A) {
         float p[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const h16x2 d = __builtin_bit_cast(h16x2, vd[b][4 * h + k]);
+          const h16x2 d = halves(vd[b][4 * h + k]);
           p[2 * k] = s[2 * h + (k >> 1)][2 * (k & 1)] * (float)d[0];
           p[2 * k + 1] = s[2 * h + (k >> 1)][2 * (k & 1) + 1] * (float)d[1];
         }
@@ -463,9 +516,9 @@ attn_step_kernel(AttnArgs A) {
   const AttnRow out = attn_row(A, seq, first, r);
   if (!out.real) return;
   const int oh = hk * A.group + out.head;
-  const int64_t at = (int64_t)out.tok * A.n_head + oh;
   if (A.part_o) {
-    const int64_t ps = (int64_t)(A.split0 + split) * A.n_tok * A.n_head + at;
+    const int64_t at = A.step_rows ? ((int64_t)seq * A.step_rows + first + r) * A.n_kv_head + hk : (int64_t)out.tok * A.n_head + oh;
+    const int64_t ps = (A.split0 + split) * A.part_rows + at;
     if ((threadIdx.x & 15) == 0) {
       A.part_ml[2 * ps] = L > 0.0f ? M : NO_MAX;
       A.part_ml[2 * ps + 1] = L;
@@ -489,8 +542,497 @@ attn_step_kernel(AttnArgs A) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// many query rows: NW waves of 16 * CT rows each over the same keys
+// ---------------------------------------------------------------------------
+// natural key order: the low (H = 0) or high nibbles of eight bytes
+template <int H>
+__device__ __forceinline__ h16x8 codes8_q4_bytes(u32x2 w) {
+  h16x2 p[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = (w[i] >> (4 * H)) & 0x0F0F0F0Fu;
+    p[2 * i] = code_pair(__builtin_amdgcn_perm(0x64646464u, x, 0x04010400u), 1032.0f);
+    p[2 * i + 1] = code_pair(__builtin_amdgcn_perm(0x64646464u, x, 0x04030402u), 1032.0f);
+  }
+  return join8(p);
+}
+// 2^n as fp16, -15 <= n <= 15, in both halves
+__device__ __forceinline__ h16x2 pow2_pair(int n) {
+  const uint32_t h = n >= -14 ? (uint32_t)(n + 15) << 10 : 0x0200u;
+  return __builtin_bit_cast(h16x2, h | (h << 16));
+}
+__device__ __forceinline__ h16x8 times(h16x8 a, h16x2 f) {   // by pairs
+  return a * __builtin_shufflevector(f, f, 0, 1, 0, 1, 0, 1, 0, 1);
+}
+
+constexpr int PREC_BF16 = 0, PREC_F16 = 1, PREC_F32 = 2;
+
+// Where lane (g, r) of an operand lies in its 1 KB.  LDS serves a 16-byte access in
+// groups of 16 lanes that take quads 0, 3 of lane group 0 with quads 1, 2 of group 1
+// (and so on): turning the quads of group g by 0, 3, 2, 1 keeps such reads on different
+// banks, and puts the four lane groups of one row or key, which one write holds side by
+// side, on different banks too (in order they would meet on one).
+__device__ __forceinline__ int operand_slot(int g, int r) { return g * 16 + (r ^ (((-g) & 3) * 4)); }
+
+template <int NB>
+struct TileLds {
+  u32x4 k[2][4][NB][64];          // K operands: [key tile][block][lane]
+  u32x4 v[2][2 * NB][2][64];      // V operands: [16 rows of V^T][key half][lane]
+  uint16_t vd[2][NB][64];         // V's scales
+  uint16_t kd[2][NB][64];         // K's scales (fp16, fp32 rows)
+  float kf[2][64];                // K's power of two per key (bf16 rows)
+  uint32_t vmax[2];               // largest |scale| of V in the step
+};
+
+template <int TK, int TV, int NB, int NW, int CT, int PREC>
+__global__ void __launch_bounds__(64 * NW, NB <= 3 || (NB == 4 && PREC != PREC_F32) ? 4 : 2)
+attn_tile_kernel(AttnArgs A) {
+  constexpr int D = NB * 32, T = 64 * NW, ROWS = NW * 16 * CT;
+  constexpr bool LO = PREC == PREC_F32;
+  using C = KvCodes<TK>;
+  constexpr int NG = (NB + C::GROUP - 1) / C::GROUP;
+  constexpr int KU = (NG * 256 + T - 1) / T;                       // K units per thread
+  constexpr int VR = TV == FT_Q8_0 ? D : D / 2;
+  constexpr int VU = (VR * 4 + T - 1) / T;                         // V units per thread
+  __shared__ TileLds<NB> L;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  const int col = lane & 15, g = lane >> 4;
+  const int hk = blockIdx.x % A.n_kv_head;
+  const int split = (blockIdx.x / A.n_kv_head) % A.n_split;
+  // the last tiles first: under the causal mask they have the most keys
+  const int64_t tile = A.tiles - 1 - blockIdx.x / A.n_kv_head / A.n_split;
+
+  int seq = -1;
+  int64_t first = tile * ROWS;
+  if (!A.shared_part) {
+    seq = seq_of_tile(A, tile, ROWS, lane);
+    const int64_t q0 = min(max(A.q_start[seq], 0), A.n_tok);
+    first = (tile - (q0 * A.group / ROWS + seq)) * ROWS;
+    if (A.step_rows && seq_rows(A, seq) <= A.step_rows) return;    // the other kernel's
+  }
+  if (!attn_row(A, seq, first, 0).real) return;
+  // what the whole workgroup's rows can see (row 0 and the last are the extremes of a
+  // sequence; rows of many sequences are looked at one by one)
+  AttnRow row[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    row[c] = attn_row(A, seq, first, (wave * CT + c) * 16 + col);
+    row_facts(A, A.shared_part ? seq_of_token(A, row[c].tok) : seq, row[c]);
+  }
+  int lo_pos = row[0].pos, hi_pos = row[0].pos, lo_len = row[0].len, hi_len = row[0].len, lo_pfx = row[0].pfx, hi_pfx = row[0].pfx;
+#pragma unroll
+  for (int c = 1; c < CT; ++c) {
+    lo_pos = min(lo_pos, row[c].pos);
+    hi_pos = max(hi_pos, row[c].pos);
+    lo_len = min(lo_len, row[c].len);
+    hi_len = max(hi_len, row[c].len);
+    lo_pfx = min(lo_pfx, row[c].pfx);
+    hi_pfx = max(hi_pfx, row[c].pfx);
+  }
+  const int min_pos = row_min(lo_pos), max_pos = row_max(hi_pos), min_len = row_min(lo_len), max_len = row_max(hi_len);
+  const int min_pfx = row_min(lo_pfx), max_pfx = row_max(hi_pfx);
+  __shared__ int s_ext[4][NW];
+  if (lane == 0) {
+    s_ext[0][wave] = min_pos;
+    s_ext[1][wave] = max_pos;
+    s_ext[2][wave] = max_len;
+    s_ext[3][wave] = max_pfx;
+  }
+  __syncthreads();
+  int w_min_pos = s_ext[0][0], w_max_pos = s_ext[1][0], w_max_len = s_ext[2][0], w_max_pfx = s_ext[3][0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) {
+    w_min_pos = min(w_min_pos, s_ext[0][w]);
+    w_max_pos = max(w_max_pos, s_ext[1][w]);
+    w_max_len = max(w_max_len, s_ext[2][w]);
+    w_max_pfx = max(w_max_pfx, s_ext[3][w]);
+  }
+  const int part_lo = A.shared_part ? 0 : A.n_shared, part_hi = A.shared_part ? A.n_shared : A.max_kv;
+  AttnSeen seen[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) seen[c] = seen_by(A, row[c], part_hi);
+  int pos[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) pos[c] = row[c].pos;
+  const AttnSteps steps = attn_steps(A, part_lo, part_hi, w_min_pos, w_max_pos, w_max_len, w_max_pfx);
+  const int s0 = split * A.split_steps, s_end = min(steps.total, s0 + A.split_steps);
+  const int32_t* pages = A.table + (int64_t)max(seq, 0) * A.table_ld;
+
+  // q as the step kernel holds it; a negative scale turns q's sign, so that the factor
+  // of the scores is positive and their maximum can be taken before it
+  h16x8 qh[CT][NB];
+  h16x8 ql[LO ? CT : 1][LO ? NB : 1];
+  float c0[CT];
+  __shared__ int s_tok[NW][CT][16], s_head[NW][CT][16];   // where the rows go; -1: nowhere
+  __shared__ float s_slope[NW][CT][16];
+  const bool capped = A.softcap > 0.0f;
+  const float cap = A.softcap * LOG2E;
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int head = hk * A.group + row[c].head;
+    float x[NB][8], amax = 0.0f;
+    kv_load_row<NB>(A.ftype, A.q, row[c].tok * A.q_token + head * A.q_head + 8 * g, A.q_vec, x);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
+    }
+    amax = groups_max(amax);
+    const int ex = amax > 0.0f && amax < INFINITY ? min(max(11 - __builtin_amdgcn_frexp_expf(amax), -120), 120) : 0;
+    const float up = __builtin_ldexpf(A.scale < 0.0f ? -1.0f : 1.0f, ex);
+    const float c1 = fabsf(A.scale) * __builtin_ldexpf(1.0f, -ex);
+    c0[c] = capped ? c1 / A.softcap : c1 * LOG2E;
+    if (g == 0) {
+      s_tok[wave][c][col] = row[c].real ? row[c].tok : -1;
+      s_head[wave][c][col] = head;
+      s_slope[wave][c][col] = A.slopes ? A.slopes[head] * LOG2E : 0.0f;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[b][e] *= up;
+      split8<LO>(x[b], qh[c][b], ql[LO ? c : 0][LO ? b : 0]);
+    }
+  }
+
+  float m[CT], l[CT];
+  f32x4 o[CT][2 * NB];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    m[c] = NO_MAX;
+    l[c] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2 * NB; ++i) o[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  const int page_mask = A.page - 1;
+  const int hb_k = kv_head_bytes(TK, D, A.page), hb_v = kv_head_bytes(TV, D, A.page);
+  const int cb_k = kv_code_bytes(TK, D, A.page), cb_v = kv_code_bytes(TV, D, A.page);
+  const uint32_t pb_k = (uint32_t)A.n_kv_head * hb_k, pb_v = (uint32_t)A.n_kv_head * hb_v;   // under 2^30
+  const uint8_t *k_head = A.k_pages + (uint32_t)hk * hb_k, *v_head = A.v_pages + (uint32_t)hk * hb_v;
+  const auto page_of = [&](int key) { return (uint32_t)page_at(pages, key >> A.page_shift, A.cols, A.n_pages); };
+
+  const int slot = operand_slot(g, col);
+  // this thread's part of a step: K units (group p of blocks, key j, lane group kg_) and V
+  // units (row of V^T, 16 keys 16 * vg_ ..)
+  const int j = (tid >> 2) & 63, kg_ = tid & 3;
+  const int vg_ = tid & 3;
+  uint32_t kw[KU][4];
+  uint16_t ksc[PREC == PREC_BF16 ? NB : 1];
+  u32x4 vw[VU], sc;
+  const auto fetch = [&](int key0) {
+    const int key = key0 + j, keyv = key0 + 16 * vg_;
+    const uint8_t* kc = k_head + (uint64_t)page_of(key) * pb_k;
+    const uint8_t* vc = v_head + (uint64_t)page_of(keyv) * pb_v;
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      const int p = (tid + i * T) >> 8;   // uniform over a wave
+      if (p < NG) {
+        const uint8_t* src = kc + A.page * 64 * p;
+        if (NB % C::GROUP == 0 || p < NG - 1) {
+          constexpr int W = (NB < C::GROUP ? NB : C::GROUP) * C::CB / 4;
+          load_words(src + ((key & page_mask) * 4 + kg_) * W * 4, W, kw[i]);
+        } else {
+          constexpr int W = (NB % C::GROUP) * C::CB / 4;
+          load_words(src + ((key & page_mask) * 4 + kg_) * W * 4, W, kw[i]);
+        }
+      }
+    }
+    if constexpr (PREC == PREC_BF16) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) ksc[b] = *(const uint16_t*)(kc + cb_k + 2 * (b * A.page + (key & page_mask)));
+    }
+#pragma unroll
+    for (int i = 0; i < VU; ++i) {
+      const int r = (tid + i * T) >> 2;
+      if (VR * 4 % T == 0 || r < VR) vw[i] = *(const u32x4*)(vc + r * A.page + (keyv & page_mask));
+    }
+    if (wave < (PREC == PREC_BF16 ? 1 : 2) && lane < NB * 8) {   // the scales, eight keys per lane: V's, and K's
+      const int kk = key0 + 8 * (lane & 7), b = lane >> 3;
+      const uint64_t pg = page_of(kk);
+      const uint8_t* src = wave == 0 ? v_head + pg * pb_v + cb_v : k_head + pg * pb_k + cb_k;
+      sc = *(const u32x4*)(src + 2 * (b * A.page + (kk & page_mask)));
+    }
+  };
+  const int end = min(w_max_len, part_hi);   // slots from here on may hold anything
+  const auto commit = [&](int buf, int key0) {
+    const int r = (j >> 4) * 4 + (j & 3), t = (j >> 2) & 3;   // key j's row and tile
+    h16x2 df[PREC == PREC_BF16 ? NB : 1];
+    if constexpr (PREC == PREC_BF16) {
+      // the key's scales as multiples of a power of two that takes the largest to [1, 2)
+      uint32_t top = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) top = max(top, (uint32_t)ksc[b] & 0x7FFFu);
+      const int e = min((int)(top >> 10), 30);
+      const h16x2 f = pow2_pair(15 - e);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) df[b] = __builtin_bit_cast(h16x2, (uint32_t)ksc[b] * 0x00010001u) * f;
+      if (tid < 256 && kg_ == 0) L.kf[buf][j] = __uint_as_float((uint32_t)(e - 15 + 127) << 23);
+    }
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      const int p = (tid + i * T) >> 8;
+      if (p < NG) {
+#pragma unroll
+        for (int q = 0; q < C::GROUP; ++q) {
+          const int b = p * C::GROUP + q;
+          if (b < NB) {
+            h16x8 a;
+            if constexpr (TK == FT_Q8_0) a = codes8_q8(u32x2{kw[i][2 * q], kw[i][2 * q + 1]});
+            else a = codes8_q4(kw[i][q]);
+            if constexpr (PREC == PREC_BF16) {
+              h16x2 d = df[q];
+#pragma unroll
+              for (int pp = 1; pp < NG; ++pp)
+                if (p == pp && pp * C::GROUP + q < NB) d = df[pp * C::GROUP + q < NB ? pp * C::GROUP + q : 0];
+              a = times(a, d);
+            }
+            L.k[buf][t][b][operand_slot(kg_, r)] = __builtin_bit_cast(u32x4, a);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VU; ++i) {
+      const int vr = (tid + i * T) >> 2;
+      if (VR * 4 % T == 0 || vr < VR) {
+        const u32x2 w0 = {vw[i][0], vw[i][1]}, w1 = {vw[i][2], vw[i][3]};
+        if constexpr (TV == FT_Q8_0) {
+          const int at = operand_slot(vg_, vr & 15);
+          L.v[buf][vr >> 4][0][at] = __builtin_bit_cast(u32x4, codes8_q8(w0));
+          L.v[buf][vr >> 4][1][at] = __builtin_bit_cast(u32x4, codes8_q8(w1));
+        } else {
+          const int at = operand_slot(vg_, vr & 15), b = vr >> 4;
+          L.v[buf][2 * b][0][at] = __builtin_bit_cast(u32x4, codes8_q4_bytes<0>(w0));
+          L.v[buf][2 * b][1][at] = __builtin_bit_cast(u32x4, codes8_q4_bytes<0>(w1));
+          L.v[buf][2 * b + 1][0][at] = __builtin_bit_cast(u32x4, codes8_q4_bytes<1>(w0));
+          L.v[buf][2 * b + 1][1][at] = __builtin_bit_cast(u32x4, codes8_q4_bytes<1>(w1));
+        }
+      }
+    }
+    if (wave == 0) {
+      const int kk = key0 + 8 * (lane & 7), b = lane >> 3;
+      uint32_t top = 0;
+      if (lane < NB * 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sc[k] &= (kk + 2 * k < end ? 0xFFFFu : 0u) | (kk + 2 * k + 1 < end ? 0xFFFF0000u : 0u);
+          top = max(top, max(sc[k] & 0x7FFFu, (sc[k] >> 16) & 0x7FFFu));
+        }
+      }
+      top = wave_umax(top);
+      if (lane == 0) L.vmax[buf] = top;
+      if constexpr (PREC == PREC_BF16)   // as multiples of a power of two: the largest is in [1, 2)
+        sc = __builtin_bit_cast(u32x4, times(__builtin_bit_cast(h16x8, sc), pow2_pair(15 - min((int)(top >> 10), 30))));
+      if (lane < NB * 8) *(u32x4*)&L.vd[buf][b][8 * (lane & 7)] = sc;
+    } else if (PREC != PREC_BF16 && wave == 1) {
+      if (lane < NB * 8) *(u32x4*)&L.kd[buf][lane >> 3][8 * (lane & 7)] = sc;
+    }
+  };
+
+  if (s0 < s_end) {
+    const int key0 = steps.block(s0) * ATTN_STEP;
+    fetch(key0);
+    commit(0, key0);
+  }
+  for (int i = s0; i < s_end; ++i) {
+    const int buf = (i - s0) & 1;
+    const int key0 = steps.block(i) * ATTN_STEP;
+    int key1 = 0;
+    __syncthreads();
+    if (i + 1 < s_end) {
+      key1 = steps.block(i + 1) * ATTN_STEP;
+      fetch(key1);
+    }
+    const int last = key0 + ATTN_STEP - 1;
+    {
+      const bool all = key0 >= part_lo && last < min(min_len, part_hi) &&
+                       (((!A.causal || last <= min_pos) && (!A.window || key0 > max_pos - (int)A.window)) || last < min_pfx);
+      const int kg = key0 + 16 * g;
+      f32x4 s[CT][4];
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        u32x4 kd[2];
+        if constexpr (PREC != PREC_BF16) {
+          kd[0] = *(const u32x4*)&L.kd[buf][b][16 * g];
+          kd[1] = *(const u32x4*)&L.kd[buf][b][16 * g + 8];
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const h16x8 a = __builtin_bit_cast(h16x8, L.k[buf][t][b][slot]);
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            if constexpr (PREC == PREC_BF16) {
+              s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[c][b], s[c][t], 0, 0, 0);
+            } else {
+              f32x4 x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[c][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+              if constexpr (LO) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[c][b], x, 0, 0, 0);
+              const h16x2 d0 = halves(kd[t >> 1][2 * (t & 1)]), d1 = halves(kd[t >> 1][2 * (t & 1) + 1]);
+              s[c][t][0] = fmaf((float)d0[0], x[0], s[c][t][0]);
+              s[c][t][1] = fmaf((float)d0[1], x[1], s[c][t][1]);
+              s[c][t][2] = fmaf((float)d1[0], x[2], s[c][t][2]);
+              s[c][t][3] = fmaf((float)d1[1], x[3], s[c][t][3]);
+            }
+          }
+        }
+        if constexpr (PREC != PREC_BF16) __builtin_amdgcn_sched_barrier(0);
+      }
+      const int ev = min((int)(L.vmax[buf] >> 10), 30);
+      const float lift = (float)(29 - ev);
+      if constexpr (PREC == PREC_BF16) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const f32x4 kf = *(const f32x4*)&L.kf[buf][16 * g + 4 * t];
+#pragma unroll
+          for (int c = 0; c < CT; ++c) s[c][t] *= kf;
+        }
+      }
+      h16x8 ph[PREC == PREC_BF16 ? CT : 1][2];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        float top = -INFINITY;
+        const bool plain = !capped && !A.slopes;   // the factor can wait for the exponent
+        if (!plain) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[c][t][e] *= c0[c];
+          if (capped) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[c][t][e] = capped_score<LO>(s[c][t][e], cap);
+          }
+          if (A.slopes) {
+            const float far = (float)(pos[c] - kg), slope = s_slope[wave][c][col];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[c][t][e] -= slope * fabsf(far - (float)(4 * t + e));
+          }
+        }
+        if (!all) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[c][t][e] = sees(seen[c], part_lo, kg + 4 * t + e) ? s[c][t][e] : -INFINITY;
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, s[c][t][e]);
+        const float k0 = plain ? c0[c] : 1.0f;
+        top = groups_max(top) * k0;
+        const float mn = fmaxf(m[c], top - lift);
+        if (__ballot(mn != m[c])) {
+          const float al = __builtin_amdgcn_exp2f(m[c] - mn);
+          l[c] *= al;
+#pragma unroll
+          for (int i2 = 0; i2 < 2 * NB; ++i2) o[c][i2] *= al;
+          m[c] = mn;
+        }
+        // bf16 rows: p in units that the scales below 2 leave under 2^15
+        const float shift = PREC == PREC_BF16 ? (float)(ev - 15) - m[c] : -m[c];
+        float sum = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[c][t][e] = __builtin_amdgcn_exp2f(fmaf(s[c][t][e], k0, shift));
+            sum += s[c][t][e];
+          }
+        if constexpr (PREC == PREC_BF16) {
+          l[c] = fmaf(sum, __uint_as_float((uint32_t)(15 - ev + 127) << 23), l[c]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ph[c][h][k] = (_Float16)s[c][2 * h + (k >> 2)][k & 3];
+        } else {
+          l[c] += sum;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x4 dw = *(const u32x4*)&L.vd[buf][b][16 * g + 8 * h];
+          h16x8 hi[CT], lo[LO ? CT : 1];
+          if constexpr (PREC == PREC_BF16) {
+            const h16x8 d = __builtin_bit_cast(h16x8, dw);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) hi[c] = ph[c][h] * d;
+          } else {
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+              float p[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const h16x2 d = halves(dw[k >> 1]);
+                p[k] = s[c][2 * h + (k >> 2)][k & 3] * (float)d[k & 1];
+              }
+              split8<LO>(p, hi[c], lo[LO ? c : 0]);
+            }
+          }
+#pragma unroll
+          for (int d2 = 0; d2 < 2; ++d2) {
+            const h16x8 a = __builtin_bit_cast(h16x8, L.v[buf][2 * b + d2][h][slot]);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+              o[c][2 * b + d2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, hi[c], o[c][2 * b + d2], 0, 0, 0);
+              if constexpr (LO) o[c][2 * b + d2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, lo[c], o[c][2 * b + d2], 0, 0, 0);
+            }
+          }
+        }
+        if constexpr (PREC != PREC_BF16) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (i + 1 < s_end) commit(buf ^ 1, key1);
+  }
+
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const float L_ = groups_sum(l[c]);
+    const int tok = s_tok[wave][c][col], oh = s_head[wave][c][col];
+    if (tok < 0) continue;
+    if (A.part_o) {
+      const int64_t ps = (A.split0 + split) * A.part_rows + (int64_t)tok * A.n_head + oh;
+      if (g == 0) *(f32x2*)(A.part_ml + 2 * ps) = f32x2{L_ > 0.0f ? m[c] : NO_MAX, L_};
+      if (!(L_ > 0.0f)) continue;
+#pragma unroll
+      for (int i = 0; i < 2 * NB; ++i) *(f32x4*)(A.part_o + ps * D + 16 * i + 4 * g) = o[c][i];
+    } else {
+      const float inv = L_ > 0.0f ? 1.0f / L_ : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2 * NB; ++i) {
+        const float y[4] = {o[c][i][0] * inv, o[c][i][1] * inv, o[c][i][2] * inv, o[c][i][3] * inv};
+        kv_store_n<4>(A.ftype, A.out, tok * A.out_token + oh * A.out_head + 16 * i + 4 * g, A.out_vec, y);
+      }
+    }
+  }
+}
+
+// rows of a workgroup of the tile kernel
+constexpr int TILE_WAVES = 8, TILE_CT = 1, TILE_ROWS = 16 * TILE_WAVES * TILE_CT;
+
+template <int TK, int TV, int NB, int PREC>
+static hipError_t tile_launch(const AttnArgs& a, hipStream_t st) {
+  const unsigned grid = (unsigned)(a.tiles * a.n_split * a.n_kv_head);
+  attn_tile_kernel<TK, TV, NB, TILE_WAVES, TILE_CT, PREC><<<grid, 64 * TILE_WAVES, 0, st>>>(a);
+  return hipGetLastError();
+}
+
 template <int TK, int TV, int NB>
 static hipError_t attn_launch(const AttnArgs& a, hipStream_t st) {
+  if (a.tile_kernel) {
+    if (a.ftype == FT_F32) return tile_launch<TK, TV, NB, PREC_F32>(a, st);
+    if (a.ftype == FT_F16) return tile_launch<TK, TV, NB, PREC_F16>(a, st);
+    return tile_launch<TK, TV, NB, PREC_BF16>(a, st);
+  }
   const unsigned grid = (unsigned)(a.tiles * a.n_split * a.n_kv_head);
   if (a.ftype == FT_F32) attn_step_kernel<TK, TV, NB, true><<<grid, 256, 0, st>>>(a);
   else attn_step_kernel<TK, TV, NB, false><<<grid, 256, 0, st>>>(a);

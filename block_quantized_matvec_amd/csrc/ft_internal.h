@@ -171,15 +171,24 @@ struct AttnArgs {
   int n_shared;            // leading keys that all sequences share; 0: none
   // set by the planner, per launch
   int shared_part;         // 1: the rows of all sequences over the shared keys
+  int tile_kernel;         // 1: many rows per workgroup
+  int step_rows;           // both kernels run: sequences of at most this many rows go to the step kernel
   int64_t tiles;
   int n_split, split_steps, split0;   // splits of the keys; this launch's first partial
-  float* part_o;           // null: results go to out.  [splits][n_tok * n_head][dim]
-  float* part_ml;          // [splits][n_tok * n_head][2]
+  float* part_o;           // null: results go to out.  [splits][part_rows][dim]
+  float* part_ml;          // [splits][part_rows][2]
+  int64_t part_rows;       // n_tok * n_head; with step_rows, the step kernel's n_seq * step_rows * n_kv_head
+};
+struct AttnSplit {
+  int64_t tiles;
+  int n_split, split_steps;
 };
 struct AttnPlan {
-  int64_t tiles, shared_tiles;
-  int n_split, split_steps, shared_splits, shared_steps;
+  AttnSplit shared, tile, step;   // tiles 0: no such launch
+  int shared_tile;         // the shared part runs on the tile kernel
+  int step_rows;
   size_t scratch;          // bytes of partial results; 0: none
+  size_t step_at;          // byte offset of the step kernel's, with step_rows
 };
 AttnPlan ftk_attn_plan(const AttnArgs& a);
 hipError_t ftk_launch_attn(AttnArgs a, const AttnPlan& p, void* scratch, hipStream_t st);

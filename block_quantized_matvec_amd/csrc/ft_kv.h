@@ -96,6 +96,50 @@ __device__ __forceinline__ void kv_load8(int type, const void* base, int64_t at,
   }
 }
 
+// The same of N blocks, 32 elements apart: every load goes out before the first value
+// is converted.
+template <int N>
+__device__ __forceinline__ void kv_load_row(int type, const void* base, int64_t at, bool vec, float (&v)[N][8]) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  if (!vec) {
+#pragma unroll
+    for (int b = 0; b < N; ++b) kv_load8(type, base, at + 32 * b, false, v[b]);
+    return;
+  }
+  if (type == FT_F32) {
+    const f32x4* p = (const f32x4*)((const float*)base + at);
+    f32x4 r[N][2];
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+      r[b][0] = p[8 * b];
+      r[b][1] = p[8 * b + 1];
+    }
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[b][i] = r[b][i >> 2][i & 3];
+    return;
+  }
+  const u4* p = (const u4*)((const uint16_t*)base + at);
+  u4 r[N];
+#pragma unroll
+  for (int b = 0; b < N; ++b) r[b] = p[4 * b];
+  if (type == FT_BF16) {
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[b][i] = __uint_as_float(i & 1 ? r[b][i >> 1] & 0xFFFF0000u : r[b][i >> 1] << 16);
+  } else {
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = r[b][i >> 1];
+        v[b][i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? w >> 16 : w));
+      }
+  }
+}
+
 // round to nearest even; a NaN keeps its top bits and stays a NaN
 __device__ __forceinline__ uint32_t bf16_bits(float f) {
   const uint32_t u = __float_as_uint(f);

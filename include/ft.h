@@ -351,8 +351,9 @@ ft_status ft_kv_load(const ft_kv_cache* cache, const int64_t* slots, int64_t t, 
    n_shared > 0: the first n_shared keys (a multiple of page_size) of every sequence are
    the pages of table row 0, read once for all sequences; the result is the same up to
    fp32 rounding.
-   fp32: products of fp16 pairs summed in fp32, about fp32 accuracy; fp16 and bf16: the
-   probabilities times V's scales are rounded to fp16, everything else as for fp32.
+   fp32: products of fp16 pairs summed in fp32, about fp32 accuracy; fp16: the
+   probabilities times V's scales are rounded to fp16, everything else as for fp32; bf16:
+   with many query tokens the keys and the probabilities are rounded to fp16 too.
    Page ids outside the pool are clamped.  opts NULL: causal, scale 1/sqrt(head_dim).
    Scratch (parts of split keys): the stream's pool, or the caller's `workspace` (16-byte
    aligned, ft_attn_kv_scratch_bytes).  Graphs captured on one stream share its pool: give

@@ -96,22 +96,28 @@ def attention(q, k, v, count, kv_len, scale=None, causal=True, window=0, softcap
     return out, terms, bias, mass
 
 
-def attention_bound(out, terms, bias, mass, v, eps_p, eps_out, softcap=0.0):
+def attention_bound(out, terms, bias, mass, v, dtype, softcap=0.0):
     """How far an output may be off.
     score: q as a pair of fp16 (2^-22), 32 products and the blocks' scales summed in fp32 (at most 48 roundings of the
     sum of |terms|), three more factors: (4 + 48 + 3) 2^-24 of the terms; under softcap tanh is within 2^-21 of its
     result, times the cap; a bias takes three roundings of its own size.  p = exp2(score): a score off by x moves p by
     x relative, numerator and denominator both.
-    exp2 2^-23; p times V's scale: eps_p (2^-21 as an fp16 pair, 2^-11 as one), products summed in fp32: at most one
+    bf16 rows: a key's code times its scale is rounded to fp16 once, 2^-11 of each term.
+    exp2 2^-23; p times V's scale: 2^-21 as an fp16 pair (fp32 rows), 2^-11 as one fp16 (fp16 rows); bf16 rows: p rounded
+    to fp16, and its product with the scale again, 2 * 2^-11.  Products summed in fp32: at most one
     rounding per key a wave sums, keys / 4 + 64; the joins of waves and splits: 64 roundings more.
     All of it relative to sum p |v|; then the output's own rounding.
     The fp16 numbers p d (d: V's scale) end at 2^-25 absolute.  Their unit 2^-C is such that 2^14 <= 2^C d_max, d_max the
     largest scale of the step that set it, and the sum of p that divides is at least 2^C in it: a code times what is lost
     is 128 * 2^-25 / 2^C <= 2^-32 d_max = 2^-39 v_max per key for Q8_0, 8 * 2^-25 / 2^C = 2^-36 d_max = 2^-39 v_max for Q4_0
-    (v_max of all the sequence's keys; d_max = v_max / 127 or / 8 but for the rounding of d: twice that here)."""
+    (v_max of all the sequence's keys; d_max = v_max / 127 or / 8 but for the rounding of d: twice that here).
+    bf16 rows lose 2^-25 in p (times a scale below 2) and in the product: three times that, under 2^-37 v_max per key; and
+    scales are held to 2^-25 of the step's largest, 2^-25 v_max over all keys together."""
     keys = len(v)
-    lost = keys * 2.0 ** -38 * (np.abs(v).max() if keys else 0.0)
-    score = 55 * 2.0 ** -24 * terms + 3 * 2.0 ** -24 * bias + softcap * 2.0 ** -21
+    lost = (keys * 2.0 ** -37 + 2.0 ** -25 * (dtype == "bf16")) * (np.abs(v).max() if keys else 0.0)
+    eps_k, eps_p, eps_out = {"f32": (0, 2.0 ** -21, 2.0 ** -24), "f16": (0, 2.0 ** -11, 2.0 ** -11),
+                             "bf16": (2.0 ** -11, 2 * 2.0 ** -11, 2.0 ** -8)}[dtype]
+    score = (eps_k + 55 * 2.0 ** -24) * terms + 3 * 2.0 ** -24 * bias + softcap * 2.0 ** -21
     rel = 2 * np.expm1(score) + 2.0 ** -22 + eps_p + (keys / 2 + 256) * 2.0 ** -24
     return rel[..., None] * mass + eps_out * np.abs(out) + lost + 1e-30
 

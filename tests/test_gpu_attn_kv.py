@@ -76,8 +76,7 @@ def check(kv, new, heads, heads_kv, dim, page=16, k="Q8_0", v="Q8_0", dtype="f32
     for i, (n, c) in enumerate(zip(kv, new)):
         a = slice(start[i], start[i + 1])
         o, terms, bias, mass = kv_ref.attention(x[a], *refs[i], c, n, slopes=sl, prefix=0 if prefix is None else min(prefix[i], n), **ref_kw)
-        eps = torch.finfo(TYPES[dtype]).eps / 2
-        bound = kv_ref.attention_bound(o, terms, bias, mass, refs[i][1], 2.0 ** -21 if dtype == "f32" else 2.0 ** -11, eps, kw.get("softcap", 0.0))
+        bound = kv_ref.attention_bound(o, terms, bias, mass, refs[i][1], dtype, kw.get("softcap", 0.0))
         off = np.abs(got[a] - o)
         fine = bool(np.all(np.isfinite(got[a])) and np.all(off <= bound))
         worst = np.unravel_index(np.argmax(np.nan_to_num(off / bound, nan=np.inf)), off.shape)
@@ -111,6 +110,30 @@ def test_head_groups(heads, heads_kv):
 @pytest.mark.parametrize("kv,new", [([33], [33]), ([200], [130]), ([5, 130, 64, 1], [5, 70, 1, 1])])
 def test_prompts(kv, new, k, v, dtype):
     check(kv, new, 4, 2, 128, page=32, k=k, v=v, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("kv,new,heads,heads_kv,kw", [
+    ([700], [600], 4, 1, dict()), ([257], [257], 8, 1, dict(page=64, k="Q4_0")), ([600, 9, 400, 30], [300, 9, 200, 1], 6, 2, dict(v="Q4_0")),
+    ([1500], [100], 4, 1, dict(page=128)), ([500, 300], [260, 300], 2, 1, dict(window=70)), ([400], [200], 4, 1, dict(window=33, prefix=[5])),
+    ([300, 280], [299, 130], 2, 2, dict(causal=False)), ([350], [350], 2, 1, dict(prefix=[200], softcap=3.0, slopes=[0.25, 0.01])),
+    ([90, 64], [90, 64], 40, 1, dict(scale=-0.2)), ([30, 250], [60, 250], 2, 1, dict())])
+def test_many_rows(kv, new, heads, heads_kv, kw, dtype):
+    """Tiles of many rows, next to sequences of few; more new tokens than keys in the last."""
+    check(kv, new, heads, heads_kv, 128, dtype=dtype, **kw)
+
+
+@pytest.mark.parametrize("k,v", PAIRS)
+@pytest.mark.parametrize("dim", [64, 96, 256])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_many_rows_dims(k, v, dim, dtype):
+    check([330], [290], 3, 1, dim, k=k, v=v, dtype=dtype)
+
+
+def test_prompts_and_steps_together():
+    """One prompt among single tokens with long contexts (their keys are split)."""
+    check([900, 2500, 800, 1300], [700, 1, 1, 2], 4, 2, 64, page=32)
+    check([2600, 2500, 10], [90, 1, 1], 4, 2, 64, page=32, dtype="bf16")
 
 
 @pytest.mark.parametrize("dim", [64, 96, 256])
@@ -149,7 +172,7 @@ def test_rows_that_see_nothing():
     assert (got[1:3] == 0).all()                      # no keys at all
     assert (got[3:5] == 0).all() and (got[5:8] != 0).any()   # five tokens, three keys: the first two see none
     o, terms, bias, mass = kv_ref.attention(host(q)[5:8].astype(np.float64), *refs[1], 3, 3)
-    assert np.all(np.abs(got[5:8] - o) <= kv_ref.attention_bound(o, terms, bias, mass, refs[1][1], 2.0 ** -21, 2.0 ** -24))
+    assert np.all(np.abs(got[5:8] - o) <= kv_ref.attention_bound(o, terms, bias, mass, refs[1][1], "f32"))
 
 
 def test_long_cache_splits():
@@ -164,6 +187,7 @@ def test_long_cache_splits():
 def test_shared_prefix(kv, new, page, shared, dtype):
     """The last: sequences shorter than the prefix that the others share."""
     check(kv, new, 8, 2, 64, page=page, shared=shared, dtype=dtype)
+    check([n + 130 for n in kv], [c + 120 for c in new], 4, 2, 64, page=page, shared=shared, dtype=dtype)   # prompts behind a shared prefix
     check(kv, new, 6, 1, 128, page=page, shared=shared, dtype=dtype, k="Q4_0", v="Q4_0", softcap=20.0, window=90, prefix=[4] * len(kv))
 
 
@@ -188,7 +212,7 @@ def test_uneven_scales():
         got = host(ft.attn_kv(cache, q.cuda(), table, ints([n]), ints([0, 1]))).astype(np.float64)
         kk, vv = kv_ref.values(*kv_ref.quantize(x.numpy(), "Q8_0")), kv_ref.values(*kv_ref.quantize(y.numpy(), "Q8_0"))
         o, terms, bias, mass = kv_ref.attention(q.double().numpy(), kk, vv, 1, n)
-        bound = kv_ref.attention_bound(o, terms, bias, mass, vv, 2.0 ** -21, 2.0 ** -24)
+        bound = kv_ref.attention_bound(o, terms, bias, mass, vv, "f32")
         assert np.all(np.isfinite(got)) and np.all(np.abs(got - o) <= bound), size
 
 

@@ -45,7 +45,7 @@ def test_layer():
         keys["v"].append(kv_ref.values(*kv_ref.quantize(host(v), "Q4_0")))
         kk, vv = np.concatenate(keys["k"]), np.concatenate(keys["v"])
         ro, terms, zero, mass = kv_ref.attention(host(q).astype(np.float64), kk, vv, t, done)
-        bound = kv_ref.attention_bound(ro, terms, zero, mass, vv, 2.0 ** -21, 2.0 ** -24)
+        bound = kv_ref.attention_bound(ro, terms, zero, mass, vv, "f32")
         off = np.abs(host(o) - ro)
         at = np.unravel_index(np.argmax(off / bound), off.shape)
         assert off[at] <= bound[at], f"{t} of {done} tokens, {at}: {host(o)[at]} for {ro[at]}, bound {bound[at]}, terms {terms[at[:2]]}"
