@@ -210,5 +210,6 @@ struct RouteArgs {
   double scale;
   int32_t* ids;
   float* w;
+  int vec, vec_bias;       // set by the launcher: rows (the bias) in aligned quads
 };
 hipError_t ftk_launch_route_ex(const RouteArgs& a, hipStream_t st);

@@ -88,6 +88,19 @@ def test_neighbours():
         check(x, 16, score=score, bias=bias)
 
 
+def test_many_from_one_lane():
+    """The best experts side by side: one lane of the kernel gives up all of its own, more than once."""
+    for e, first in ((256, 0), (256, 64), (512, 128), (1024, 256), (64, 0), (128, 4)):
+        x = torch.randn(2100, e, generator=torch.Generator().manual_seed(e + first)) * 0.1
+        for i in range(12):                            # quads 64 (128, 256) apart are one lane's
+            at = (first + i // 4 * (64 if e <= 256 else 128 if e <= 512 else 256) + i % 4) % e
+            x[:, at] += 5 + i
+        check(x[:40], 10)
+        check(x, 10, score="sigmoid", bias=torch.zeros(e))
+    x = -torch.arange(256.0).repeat(3000, 1)           # expert 0 first, its lane's others next
+    check(x, 14)
+
+
 def test_strided_rows_and_outputs():
     x = torch.randn(10, 300)
     wide = x.cuda()
