@@ -203,6 +203,8 @@ ft_status attn_sizes(const ft_kv_cache* c, int64_t n_tok, int64_t n_head, int64_
   a->dim = (int)c->head_dim;
   a->n_head = (int)n_head;
   a->group = (int)(n_head / c->n_kv_head);
+  a->group_mul = ((1ull << 40) + (unsigned)a->group - 1) / (unsigned)a->group;
+  if (n_tok * a->group >= (1 << 30)) return FT_ERR_SHAPE;
   a->n_tok = (int)n_tok;
   a->n_seq = (int)n_seq;
   a->max_kv = (int)max_kv;
@@ -447,7 +449,7 @@ ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int
   a.cols = (int)n_col;
   const AttnPlan p = ftk_attn_plan(a);
   for (const AttnSplit& x : {p.shared, p.tile, p.step})
-    if (x.tiles * x.n_split * a.n_kv_head > INT32_MAX) return FT_ERR_SHAPE;
+    if (x.tiles * a.n_kv_head > INT32_MAX || x.n_split > 65535) return FT_ERR_SHAPE;
   void* base = o.workspace;
   if (p.scratch && base && o.workspace_bytes < p.scratch) return FT_ERR_NO_SCRATCH;
   if (p.scratch && !base) {

@@ -20,7 +20,7 @@ attn_join_kernel(AttnArgs A, int parts) {
   if (A.step_rows && !A.tile_kernel) {   // the step kernel's rows: [seq][step_rows][n_kv_head]
     const int64_t i = row / A.n_kv_head;
     const int seq = (int)(i / A.step_rows), r = (int)(i % A.step_rows);
-    const int64_t n = seq_rows(A, seq);
+    const int n = seq_rows(A, seq);
     if (n > A.step_rows || r >= n) return;
     tok = min(max(A.q_start[seq], 0), A.n_tok) + r / A.group;
     head = (int)(row % A.n_kv_head) * A.group + r % A.group;

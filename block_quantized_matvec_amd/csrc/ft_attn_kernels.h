@@ -16,6 +16,13 @@ constexpr float LOG2E = 1.44269504088896340736f;
 constexpr int ATTN_STEP = 64;    // keys per step of a wave
 constexpr float NO_MAX = -1e30f; // below every score
 
+// what this wave's lanes wrote to LDS is there for all of them (LDS serves a wave in
+// order; the fence keeps the compiler from moving accesses across)
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // a value of the four lane groups (lanes l, l^16, l^32, l^48) met in all of them
 __device__ __forceinline__ float groups_max(float v) {
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -164,28 +171,48 @@ __device__ __forceinline__ AttnSteps attn_steps(const AttnArgs& A, int part_lo, 
   return s;
 }
 
-// The sequence whose tiles include tile `tile` when sequence i's tiles start at
-// q_start[i] * G / ROWS + i (64-bit product, floor): a wave counts the starts at or
-// below it.  The starts grow by at least one per sequence and leave room for every
-// sequence's last, partly filled tile.
-__device__ __forceinline__ int seq_of_tile(const AttnArgs& A, int64_t tile, int rows, int lane) {
-  int n = 0;
+// What a workgroup's tile belongs to: its sequence (-1: the rows of all, shared part) and
+// that sequence's query tokens [q0, q1), keys and prefix.
+struct AttnSeq {
+  int seq, q0, q1, len, pfx;
+};
+__device__ __forceinline__ AttnSeq seq_facts(const AttnArgs& A, int seq) {
+  AttnSeq s;
+  s.seq = seq;
+  s.q0 = min(max(A.q_start[seq], 0), A.n_tok);
+  s.q1 = min(max(A.q_start[seq + 1], s.q0), A.n_tok);
+  s.len = min(max(A.kv_len[seq], 0), A.max_kv);
+  s.pfx = A.prefix_len ? min(max(A.prefix_len[seq], 0), s.len) : 0;
+  return s;
+}
+// Sequence i's tiles start at tile q_start[i] * group / ROWS + i (floor): the starts grow
+// by at least one per sequence and leave room for every sequence's last, partly filled
+// tile.  A wave counts the starts at or below `tile`, 64 sequences at a time, with all
+// that is to be known of them loaded at once.
+template <int ROWS>
+__device__ __forceinline__ AttnSeq seq_of_tile(const AttnArgs& A, int tile, int lane) {
+  AttnSeq s = {0, 0, 0, 0, 0};
   for (int i0 = 0; i0 < A.n_seq; i0 += 64) {
-    const int i = i0 + lane;
-    bool at = false;
-    if (i < A.n_seq) {
-      const int64_t q = min(max(A.q_start[i], 0), A.n_tok);
-      at = q * A.group / rows + i <= tile;
+    const int i = min(i0 + lane, A.n_seq - 1);
+    const int a = A.q_start[i], b = A.q_start[i + 1], n = A.kv_len[i], p = A.prefix_len ? A.prefix_len[i] : 0;
+    const int q0 = min(max(a, 0), A.n_tok);
+    const uint64_t at = __ballot(i0 + lane < A.n_seq && q0 * A.group / ROWS + i <= tile);
+    const int c = __popcll(at);
+    if (c > 0 || i0 == 0) {
+      const int w = max(c - 1, 0);
+      s.seq = i0 + w;
+      s.q0 = __builtin_amdgcn_readlane(q0, w);
+      s.q1 = min(max(__builtin_amdgcn_readlane(b, w), s.q0), A.n_tok);
+      s.len = min(max(__builtin_amdgcn_readlane(n, w), 0), A.max_kv);
+      s.pfx = min(max(__builtin_amdgcn_readlane(p, w), 0), s.len);
     }
-    const int c = __popcll(__ballot(at));
-    n += c;
     if (c < 64) break;
   }
-  return max(n - 1, 0);
+  return s;
 }
-// the sequence that token `tok` belongs to (shared part: every lane its own)
+// the sequence that token `tok` belongs to: the last i with q_start[i] <= tok
 __device__ __forceinline__ int seq_of_token(const AttnArgs& A, int tok) {
-  int lo = 0, hi = A.n_seq - 1;   // the last i with q_start[i] <= tok
+  int lo = 0, hi = A.n_seq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (A.q_start[mid] <= tok) lo = mid;
@@ -193,43 +220,46 @@ __device__ __forceinline__ int seq_of_token(const AttnArgs& A, int tok) {
   }
   return lo;
 }
-
 // query rows of a sequence
-__device__ __forceinline__ int64_t seq_rows(const AttnArgs& A, int seq) {
+__device__ __forceinline__ int seq_rows(const AttnArgs& A, int seq) {
   const int q0 = min(max(A.q_start[seq], 0), A.n_tok), q1 = min(max(A.q_start[seq + 1], q0), A.n_tok);
-  return (int64_t)(q1 - q0) * A.group;
+  return (q1 - q0) * A.group;
 }
 
-// What one row (of a lane, or of an output) is: its token and head, its position and
-// how many keys it has.
+// One row: its token and head (within the KV head's group), its position, how many keys
+// it has and how many of them everyone sees.
 struct AttnRow {
-  int tok, head;      // head within the KV head's group
+  int tok, head;
   int pos, len, pfx;
   bool real;
 };
-__device__ __forceinline__ void row_facts(const AttnArgs& A, int seq, AttnRow& r) {
-  const int q0 = min(max(A.q_start[seq], 0), A.n_tok), q1 = min(max(A.q_start[seq + 1], q0), A.n_tok);
-  r.len = min(max(A.kv_len[seq], 0), A.max_kv);
-  r.pos = r.len - (q1 - q0) + (r.tok - q0);
-  r.pfx = A.prefix_len ? min(max(A.prefix_len[seq], 0), r.len) : 0;
-}
-// Row `at` (0 ..) of a tile that starts at row `first` of sequence `seq`, or of the
-// whole batch in the shared part (seq < 0).  Rows past the end repeat the last one and
+// n / group: the host's multiplier is right for n < 2^30
+__device__ __forceinline__ int by_group(const AttnArgs& A, int n) { return (int)(((uint64_t)(uint32_t)n * A.group_mul) >> 40); }
+// Row `at` of a tile that starts at row `first`; rows past the end repeat the last one and
 // are not real.
-__device__ __forceinline__ AttnRow attn_row(const AttnArgs& A, int seq, int64_t first, int at) {
+__device__ __forceinline__ AttnRow attn_row(const AttnArgs& A, const AttnSeq& s, int first, int at) {
   AttnRow r;
-  int64_t q0 = 0, n = (int64_t)min(max(A.q_start[A.n_seq], 0), A.n_tok) * A.group;
-  if (seq >= 0) {
-    const int s0 = min(max(A.q_start[seq], 0), A.n_tok), s1 = min(max(A.q_start[seq + 1], s0), A.n_tok);
-    q0 = s0;
-    n = (int64_t)(s1 - s0) * A.group;
-  }
-  int64_t i = first + at;
+  const int n = (s.q1 - s.q0) * A.group;
+  int i = first + at;
   r.real = i >= 0 && i < n;
-  i = max((int64_t)0, min(i, n - 1));
-  r.tok = (int)(q0 + i / A.group);
-  r.head = (int)(i % A.group);
+  i = max(0, min(i, n - 1));
+  const int t = by_group(A, i);
+  r.tok = s.q0 + t;
+  r.head = i - t * A.group;
+  r.len = s.len;
+  r.pfx = s.pfx;
+  r.pos = s.len - (s.q1 - s.q0) + t;
   return r;
+}
+// the same of the shared part's rows, which are of many sequences: every lane looks its own up
+__device__ __forceinline__ void own_seq(const AttnArgs& A, AttnRow& r) {
+  const AttnSeq s = seq_facts(A, seq_of_token(A, r.tok));
+  r.len = s.len;
+  r.pfx = s.pfx;
+  r.pos = s.len - (s.q1 - s.q0) + (r.tok - s.q0);
+}
+__device__ __forceinline__ AttnSeq all_rows(const AttnArgs& A) {
+  return {-1, 0, min(max(A.q_start[A.n_seq], 0), A.n_tok), 0, 0};
 }
 
 // The keys a row sees of the part [lo, hi): key >= lo, and either above < key < below
@@ -255,8 +285,32 @@ __device__ __forceinline__ int page_at(const int32_t* row, int col, int cols, in
   return min(max(p, 0), n_pages - 1);   // ids outside the pool are clamped, never followed
 }
 
+// q rows as matrix operands: a power of two brings the largest element of a row to [2^10,
+// 2^11), so that an fp16 (and, for fp32 rows, a second one of the remainder) holds every
+// element to 2^-24 of the largest.  A negative scale turns q's sign, so that the scores'
+// factor is positive and their maximum can be taken before it.  Returns the factor (the
+// scale and the power back).
+template <int NB, bool LO>
+__device__ __forceinline__ float q_operands(const AttnArgs& A, float (&x)[NB][8], h16x8 (&hi)[NB], h16x8 (&lo)[LO ? NB : 1]) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
+  amax = groups_max(amax);
+  const int ex = amax > 0.0f && amax < INFINITY ? min(max(11 - __builtin_amdgcn_frexp_expf(amax), -120), 120) : 0;
+  const float up = __builtin_ldexpf(A.scale < 0.0f ? -1.0f : 1.0f, ex);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[b][e] *= up;
+    split8<LO>(x[b], hi[b], lo[LO ? b : 0]);
+  }
+  return fabsf(A.scale) * __builtin_ldexpf(1.0f, -ex);
+}
+
 // ---------------------------------------------------------------------------
-// up to 16 query rows per workgroup, its waves splitting the keys
+// up to 16 query rows per workgroup, its four waves taking the 64-key blocks in turn
 // ---------------------------------------------------------------------------
 template <int TK, int TV, int NB, bool LO>
 __global__ void __launch_bounds__(256, NB <= 4 ? 2 : 1)
@@ -265,26 +319,32 @@ attn_step_kernel(AttnArgs A) {
   constexpr int NW = 4;
   using C = KvCodes<TK>;
   constexpr int NG = (NB + C::GROUP - 1) / C::GROUP;
+  constexpr int VT = TV == FT_Q8_0 ? 2 * NB : NB;            // 16-row pieces of V^T
+  constexpr int SC = 2 * NB * 8, SL = (SC + 63) / 64;        // 16-byte pieces of a step's scales, per lane
+  __shared__ __align__(16) float s_o[NW][16][D + 4];
+  __shared__ float s_m[NW][16], s_l[NW][16];
+  __shared__ u32x4 s_sc[NW][SL * 64];                        // a step's scales: K's [NB][64], V's [NB][64]
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int col = lane & 15, g = lane >> 4;
-  const int hk = blockIdx.x % A.n_kv_head;
-  const int split = (blockIdx.x / A.n_kv_head) % A.n_split;
-  const int64_t tile = blockIdx.x / A.n_kv_head / A.n_split;
+  const int tile = blockIdx.x / (unsigned)A.n_kv_head, hk = blockIdx.x - tile * A.n_kv_head;
+  const int split = blockIdx.y;
 
-  int seq = -1;
-  int64_t first = tile * 16;
+  AttnSeq sq;
+  int first = tile * 16;
   if (A.step_rows) {   // beside the tile kernel: the sequences of at most step_rows rows
-    seq = (int)(tile / (A.step_rows / 16));
-    first = (tile % (A.step_rows / 16)) * 16;
-    if (seq_rows(A, seq) > A.step_rows) return;
-  } else if (!A.shared_part) {
-    seq = seq_of_tile(A, tile, 16, lane);
-    const int64_t q0 = min(max(A.q_start[seq], 0), A.n_tok);
-    first = (tile - (q0 * A.group / 16 + seq)) * 16;
+    const unsigned per = A.step_rows / 16;
+    sq = seq_facts(A, (int)((unsigned)tile / per));
+    first = (int)((unsigned)tile % per) * 16;
+    if ((sq.q1 - sq.q0) * A.group > A.step_rows) return;
+  } else if (A.shared_part) {
+    sq = all_rows(A);
+  } else {
+    sq = seq_of_tile<16>(A, tile, lane);
+    first = (tile - (sq.q0 * A.group / 16 + sq.seq)) * 16;
   }
-  AttnRow row = attn_row(A, seq, first, col);
+  AttnRow row = attn_row(A, sq, first, col);
   if (!__ballot(row.real)) return;   // a tile past its sequence's rows
-  row_facts(A, A.shared_part ? seq_of_token(A, row.tok) : seq, row);
+  if (A.shared_part) own_seq(A, row);
 
   const int min_pos = row_min(row.pos), max_pos = row_max(row.pos);
   const int min_len = row_min(row.len), max_len = row_max(row.len);
@@ -293,171 +353,178 @@ attn_step_kernel(AttnArgs A) {
   const AttnSeen seen = seen_by(A, row, part_hi);
   const AttnSteps steps = attn_steps(A, part_lo, part_hi, min_pos, max_pos, max_len, max_pfx);
   const int s_end = min(steps.total, (split + 1) * A.split_steps);
-  const int32_t* pages = A.table + (int64_t)max(seq, 0) * A.table_ld;
+  const int s0 = split * A.split_steps + wave;
+  const int s_last = s0 + (s_end - 1 - s0) / NW * NW;   // this wave's last step (where there is one)
+  const int32_t* pages = A.table + (int64_t)max(sq.seq, 0) * A.table_ld;
 
-  // the rows' q: a power of two brings the largest element of a row to [2^10, 2^11), so
-  // that an fp16 (and, for fp32, a second one of the remainder) holds every element to
-  // 2^-24 of the largest; the power returns with the score's factor
+  const int page_mask = A.page - 1;
+  const int hb_k = kv_head_bytes(TK, D, A.page), hb_v = kv_head_bytes(TV, D, A.page);
+  const int cb_k = kv_code_bytes(TK, D, A.page), cb_v = kv_code_bytes(TV, D, A.page);
+  const uint32_t pb_k = (uint32_t)A.n_kv_head * hb_k, pb_v = (uint32_t)A.n_kv_head * hb_v;   // under 2^30
+  const uint8_t *k_head = A.k_pages + (uint32_t)hk * hb_k, *v_head = A.v_pages + (uint32_t)hk * hb_v;
+
+  // Lane row r = col holds key (r/4)*16 + 4t + r%4 of score tile t, so that the four scores
+  // a lane group gets of every tile are its own 16 keys 16g .. 16g+15.  Scales: piece
+  // lane + 64 i is eight keys of one block and side.
+  const int my_k = (col >> 2) * 16 + (col & 3), my_v = 16 * g, my_s = 8 * (lane & 7);
+  struct Ids { int k, v, s; };
+  const auto ids_of = [&](int i) {
+    const int key0 = steps.block(i) * ATTN_STEP;
+    return Ids{page_at(pages, (key0 + my_k) >> A.page_shift, A.cols, A.n_pages),
+               page_at(pages, (key0 + my_v) >> A.page_shift, A.cols, A.n_pages),
+               page_at(pages, (key0 + my_s) >> A.page_shift, A.cols, A.n_pages)};
+  };
+  uint32_t kcode[4][NB * C::CB / 4];
+  u32x4 vcode[VT], sc[SL];
+  const auto load_scales = [&](int i, const Ids& id) {
+    const int j = (steps.block(i) * ATTN_STEP + my_s) & page_mask;
+#pragma unroll
+    for (int n = 0; n < SL; ++n) {
+      const int p = min(lane + 64 * n, SC - 1);   // lanes past the pieces repeat the last
+      const int b = (p >> 3) % NB;
+      const uint8_t* src = p < NB * 8 ? k_head + (uint64_t)(uint32_t)id.s * pb_k + cb_k : v_head + (uint64_t)(uint32_t)id.s * pb_v + cb_v;
+      sc[n] = *(const u32x4*)(src + 2 * (b * A.page + j));
+    }
+  };
+  const auto load_k = [&](int i, const Ids& id) {
+    const int j = (steps.block(i) * ATTN_STEP + my_k) & page_mask;
+    const uint8_t* src = k_head + (uint64_t)(uint32_t)id.k * pb_k;
+#pragma unroll
+    for (int p = 0; p < NG; ++p) {
+      const int words = (NB - p * C::GROUP < C::GROUP ? NB - p * C::GROUP : C::GROUP) * C::CB / 4;
+      const uint8_t* at = src + A.page * 64 * p + (4 * j + g) * words * 4;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) load_words(at + 64 * t * words, words, &kcode[t][p * C::GROUP * C::CB / 4]);
+    }
+  };
+  const auto load_v = [&](int i, const Ids& id) {
+    const uint8_t* at = v_head + (uint64_t)(uint32_t)id.v * pb_v + ((steps.block(i) * ATTN_STEP + my_v) & page_mask) + col * A.page;
+#pragma unroll
+    for (int d = 0; d < VT; ++d) vcode[d] = *(const u32x4*)(at + 16 * d * A.page);
+  };
+
   const int head = hk * A.group + row.head;
-  h16x8 qh[NB], ql[LO ? NB : 1];
-  float c1;
-  {
-    float x[NB][8], amax = 0.0f;
-    kv_load_row<NB>(A.ftype, A.q, row.tok * A.q_token + head * A.q_head + 8 * g, A.q_vec, x);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
-    }
-    amax = groups_max(amax);
-    const int ex = amax > 0.0f && amax < INFINITY ? min(max(11 - __builtin_amdgcn_frexp_expf(amax), -120), 120) : 0;
-    const float up = __builtin_ldexpf(1.0f, ex);
-    c1 = A.scale * __builtin_ldexpf(1.0f, -ex);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[b][e] *= up;
-      split8<LO>(x[b], qh[b], ql[LO ? b : 0]);
-    }
-  }
+  float x[NB][8];
+  Ids id = {0, 0, 0};
+  if (s0 < s_end) id = ids_of(s0);
+  kv_load_row<NB>(A.ftype, A.q, row.tok * A.q_token + head * A.q_head + 8 * g, A.q_vec, x);
   const float slope = A.slopes ? A.slopes[head] * LOG2E : 0.0f;
-  const bool capped = A.softcap > 0.0f;
+  if (s0 < s_end) {
+    load_scales(s0, id);
+    load_k(s0, id);
+    load_v(s0, id);
+    id = ids_of(min(s0 + NW, s_last));
+  }
+  h16x8 qh[NB], ql[LO ? NB : 1];
+  const float c1 = q_operands<NB, LO>(A, x, qh, ql);
+  const bool capped = A.softcap > 0.0f, plain = !capped && !A.slopes;
   const float c0 = capped ? c1 / A.softcap : c1 * LOG2E, cap = A.softcap * LOG2E;
+  const float k0 = plain ? c0 : 1.0f;   // the factor can wait for the exponent
 
   float m = NO_MAX, l = 0.0f;
   f32x4 o[2 * NB];
 #pragma unroll
   for (int i = 0; i < 2 * NB; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int end = min(max_len, part_hi);   // slots from here on may hold anything
 
-  const int page_mask = A.page - 1;
-  const int hb_k = kv_head_bytes(TK, D, A.page), hb_v = kv_head_bytes(TV, D, A.page);
-  const int cb_k = kv_code_bytes(TK, D, A.page), cb_v = kv_code_bytes(TV, D, A.page);
-  const int64_t pb_k = (int64_t)A.n_kv_head * hb_k, pb_v = (int64_t)A.n_kv_head * hb_v;
+  // Each load goes out as soon as its registers are free, a step (of this wave) ahead;
+  // behind the last step the last one is loaded again.
+  for (int i = s0; i < s_end; i += NW) {
+    const int next = min(i + NW, s_last);
+    const int key0 = steps.block(i) * ATTN_STEP, last = key0 + ATTN_STEP - 1;
+    const int kg = key0 + 16 * g;
+    const bool all = key0 >= part_lo && last < min(min_len, part_hi) &&
+                     (((!A.causal || last <= min_pos) && (!A.window || key0 > max_pos - (int)A.window)) || last < min_pfx);
+    // scales through LDS (the wave's own); those of slots past the sequence count as zero
+    uint32_t top_d = 0;
+#pragma unroll
+    for (int n = 0; n < SL; ++n) {
+      const int p = lane + 64 * n, key = key0 + my_s;
+      if (last >= end) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sc[n][k] &= (key + 2 * k < end ? 0xFFFFu : 0u) | (key + 2 * k + 1 < end ? 0xFFFF0000u : 0u);
+      }
+      if (p >= NB * 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top_d = max(top_d, max(sc[n][k] & 0x7FFFu, (sc[n][k] >> 16) & 0x7FFFu));
+      }
+      s_sc[wave][p] = sc[n];
+    }
+    top_d = wave_umax(top_d);
+    wave_lds_sync();
+    const u32x4 *kd = &s_sc[wave][2 * g], *vd = &s_sc[wave][NB * 8 + 2 * g];
+    load_scales(next, id);
 
-  for (int i = split * A.split_steps + wave; i < s_end; i += NW) {
-    const int key0 = steps.block(i) * ATTN_STEP;
-    // lane row r = col holds key (r/4)*16 + 4t + r%4 of score tile t, so that the four
-    // scores a lane group gets of every tile are its own 16 keys 16g .. 16g+15
-    const int kk = key0 + (col >> 2) * 16 + (col & 3), kg = key0 + 16 * g;
-    const int pk = page_at(pages, kk >> A.page_shift, A.cols, A.n_pages);
-    const int pg = page_at(pages, kg >> A.page_shift, A.cols, A.n_pages);
-    const uint8_t* kc = A.k_pages + pk * pb_k + (int64_t)hk * hb_k;
-    const uint8_t* ks = A.k_pages + pg * pb_k + (int64_t)hk * hb_k + cb_k + 2 * (kg & page_mask);
-    const uint8_t* vc = A.v_pages + pg * pb_v + (int64_t)hk * hb_v + (kg & page_mask);
-    const uint8_t* vs = A.v_pages + pg * pb_v + (int64_t)hk * hb_v + cb_v + 2 * (kg & page_mask);
-
-    // scores: s[t][i] of key kg + 4t + i
+    // scores: s[t][e] of key kg + 4t + e
     f32x4 s[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t kcode[4][NB * C::CB / 4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int j = (kk + 4 * t) & page_mask;
-#pragma unroll
-      for (int p = 0; p < NG; ++p) {
-        constexpr int W = C::GROUP * C::CB / 4;
-        const int words = (NB - p * C::GROUP < C::GROUP ? NB - p * C::GROUP : C::GROUP) * C::CB / 4;
-        load_words(kc + kv_k_at<TK, NB>(A.page, j, p * C::GROUP, g), words, &kcode[t][p * W]);
-      }
-    }
-    uint32_t kd[NB][8], vd[NB][8];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      *(u32x4*)&kd[b][0] = *(const u32x4*)(ks + 2 * b * A.page);
-      *(u32x4*)&kd[b][4] = *(const u32x4*)(ks + 2 * b * A.page + 16);
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      *(u32x4*)&vd[b][0] = *(const u32x4*)(vs + 2 * b * A.page);
-      *(u32x4*)&vd[b][4] = *(const u32x4*)(vs + 2 * b * A.page + 16);
-    }
-    constexpr int VT = TV == FT_Q8_0 ? 2 * NB : NB;
-    u32x4 vcode[VT];
-#pragma unroll
-    for (int d = 0; d < VT; ++d) vcode[d] = *(const u32x4*)(vc + (16 * d + col) * A.page);
-
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
+      const u32x4 d[2] = {kd[8 * b], kd[8 * b + 1]};
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         h16x8 a;
         if constexpr (TK == FT_Q8_0) a = codes8_q8(u32x2{kcode[t][2 * b], kcode[t][2 * b + 1]});
         else a = codes8_q4(kcode[t][b]);
-        f32x4 x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[b], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-        if constexpr (LO) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[b], x, 0, 0, 0);
-        const h16x2 d0 = halves(kd[b][2 * t]), d1 = halves(kd[b][2 * t + 1]);
-        s[t][0] = fmaf((float)d0[0], x[0], s[t][0]);
-        s[t][1] = fmaf((float)d0[1], x[1], s[t][1]);
-        s[t][2] = fmaf((float)d1[0], x[2], s[t][2]);
-        s[t][3] = fmaf((float)d1[1], x[3], s[t][3]);
+        f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[b], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+        if constexpr (LO) y = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[b], y, 0, 0, 0);
+        const h16x2 d0 = halves(d[t >> 1][2 * (t & 1)]), d1 = halves(d[t >> 1][2 * (t & 1) + 1]);
+        s[t][0] = fmaf((float)d0[0], y[0], s[t][0]);
+        s[t][1] = fmaf((float)d0[1], y[1], s[t][1]);
+        s[t][2] = fmaf((float)d1[0], y[2], s[t][2]);
+        s[t][3] = fmaf((float)d1[1], y[3], s[t][3]);
       }
     }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] *= c0;
-    if (capped) {
+    load_k(next, id);
+    if (!plain) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] = capped_score<LO>(s[t][e], cap);
-    }
-    if (A.slopes) {
+        for (int e = 0; e < 4; ++e) s[t][e] *= c0;
+      if (capped) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] -= slope * fabsf((float)(row.pos - kg) - (float)(4 * t + e));
+          for (int e = 0; e < 4; ++e) s[t][e] = capped_score<LO>(s[t][e], cap);
+      }
+      if (A.slopes) {
+        const float away = (float)(row.pos - kg);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][e] -= slope * fabsf(away - (float)(4 * t + e));
+      }
     }
-    const int last = key0 + ATTN_STEP - 1;
-    const bool all = key0 >= part_lo && last < min(min_len, part_hi) &&
-                     (((!A.causal || last <= min_pos) && (!A.window || key0 > max_pos - (int)A.window)) || last < min_pfx);
     if (!all) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[t][e] = sees(seen, part_lo, kg + 4 * t + e) ? s[t][e] : -INFINITY;
-      // slots past the sequence may hold anything: their scales count as zero
-      const int end = min(max_len, part_hi);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t keep = (kg + 2 * k < end ? 0xFFFFu : 0u) | (kg + 2 * k + 1 < end ? 0xFFFF0000u : 0u);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) vd[b][k] &= keep;
-      }
     }
-    // the step's largest V scale: with C = 29 - its fp16 exponent, exp2(s - m) * d stays
+    // with C = 29 - the fp16 exponent of the step's largest V scale, exp2(s - m) * d stays
     // below 2^15 where m is at least the largest score minus C
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 big = {0, 0};
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, vd[b][k] & 0x7FFF7FFFu));
-    const uint32_t vmax = groups_umax(max((uint32_t)big[0], (uint32_t)big[1]));
-    const float lift = (float)(29 - (int)(vmax >> 10));
+    const float lift = (float)(29 - (int)(top_d >> 10));
     float top = s[0][0];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = fmaxf(top, s[t][e]);
-    top = groups_max(top);
+    top = groups_max(top) * k0;
     const float mn = fmaxf(m, top - lift);
     if (__ballot(mn != m)) {
       const float al = __builtin_amdgcn_exp2f(m - mn);
       l *= al;
 #pragma unroll
-      for (int i2 = 0; i2 < 2 * NB; ++i2)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i2][e] *= al;
+      for (int n = 0; n < 2 * NB; ++n) o[n] *= al;
       m = mn;
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[t][e] = __builtin_amdgcn_exp2f(s[t][e] - m);
+        s[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], k0, -m));
         l += s[t][e];
       }
     // o += V^T p: p times V's scale of (key, block) as fp16 (fp32 rows: and its remainder)
@@ -465,16 +532,13 @@ attn_step_kernel(AttnArgs A) {
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {   // keys 16g + 8h .. + 7
+        const u32x4 dw = vd[8 * b + h];
         float p[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const h16x2 d = halves(vd[b][4 * h + k]);
-          p[2 * k] = s[2 * h + (k >> 1)][2 * (k & 1)] * (float)d[0];
-          p[2 * k + 1] = s[2 * h + (k >> 1)][2 * (k & 1) + 1] * (float)d[1];
-        }
+        for (int k = 0; k < 8; ++k) p[k] = s[2 * h + (k >> 2)][k & 3] * (float)halves(dw[k >> 1])[k & 1];
         if constexpr (TV == FT_Q4_0) {   // its codes come as keys 0, 2, 1, 3
-          float x = p[1]; p[1] = p[2]; p[2] = x;
-          x = p[5]; p[5] = p[6]; p[6] = x;
+          float y = p[1]; p[1] = p[2]; p[2] = y;
+          y = p[5]; p[5] = p[6]; p[6] = y;
         }
         h16x8 ph, pl;
         split8<LO>(p, ph, pl);
@@ -489,11 +553,12 @@ attn_step_kernel(AttnArgs A) {
         }
       }
     }
+    load_v(next, id);
+    id = ids_of(min(next + NW, s_last));
+    wave_lds_sync();   // the scales are read before the next step's take their place
   }
 
   // the waves' states meet in LDS: rows of D floats per wave, and (m, l) per wave and row
-  __shared__ __align__(16) float s_o[NW][16][D + 4];
-  __shared__ float s_m[NW][16], s_l[NW][16];
   l = groups_sum(l);
   if (g == 0) {
     s_m[wave][col] = m;
@@ -513,11 +578,11 @@ attn_step_kernel(AttnArgs A) {
     f[w] = __builtin_amdgcn_exp2f(s_m[w][r] - M);
     L += f[w] * s_l[w][r];
   }
-  const AttnRow out = attn_row(A, seq, first, r);
+  const AttnRow out = attn_row(A, sq, first, r);
   if (!out.real) return;
   const int oh = hk * A.group + out.head;
   if (A.part_o) {
-    const int64_t at = A.step_rows ? ((int64_t)seq * A.step_rows + first + r) * A.n_kv_head + hk : (int64_t)out.tok * A.n_head + oh;
+    const int64_t at = A.step_rows ? ((int64_t)sq.seq * A.step_rows + first + r) * A.n_kv_head + hk : (int64_t)out.tok * A.n_head + oh;
     const int64_t ps = (A.split0 + split) * A.part_rows + at;
     if ((threadIdx.x & 15) == 0) {
       A.part_ml[2 * ps] = L > 0.0f ? M : NO_MAX;
@@ -598,27 +663,27 @@ attn_tile_kernel(AttnArgs A) {
   __shared__ TileLds<NB> L;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int col = lane & 15, g = lane >> 4;
-  const int hk = blockIdx.x % A.n_kv_head;
-  const int split = (blockIdx.x / A.n_kv_head) % A.n_split;
   // the last tiles first: under the causal mask they have the most keys
-  const int64_t tile = A.tiles - 1 - blockIdx.x / A.n_kv_head / A.n_split;
+  const int back = blockIdx.x / (unsigned)A.n_kv_head, hk = blockIdx.x - back * A.n_kv_head;
+  const int tile = (int)A.tiles - 1 - back, split = blockIdx.y;
 
-  int seq = -1;
-  int64_t first = tile * ROWS;
-  if (!A.shared_part) {
-    seq = seq_of_tile(A, tile, ROWS, lane);
-    const int64_t q0 = min(max(A.q_start[seq], 0), A.n_tok);
-    first = (tile - (q0 * A.group / ROWS + seq)) * ROWS;
-    if (A.step_rows && seq_rows(A, seq) <= A.step_rows) return;    // the other kernel's
+  AttnSeq sq;
+  int first = tile * ROWS;
+  if (A.shared_part) {
+    sq = all_rows(A);
+  } else {
+    sq = seq_of_tile<ROWS>(A, tile, lane);
+    first = (tile - (sq.q0 * A.group / ROWS + sq.seq)) * ROWS;
+    if (A.step_rows && (sq.q1 - sq.q0) * A.group <= A.step_rows) return;   // the other kernel's
   }
-  if (!attn_row(A, seq, first, 0).real) return;
+  if (!attn_row(A, sq, first, 0).real) return;
   // what the whole workgroup's rows can see (row 0 and the last are the extremes of a
   // sequence; rows of many sequences are looked at one by one)
   AttnRow row[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    row[c] = attn_row(A, seq, first, (wave * CT + c) * 16 + col);
-    row_facts(A, A.shared_part ? seq_of_token(A, row[c].tok) : seq, row[c]);
+    row[c] = attn_row(A, sq, first, (wave * CT + c) * 16 + col);
+    if (A.shared_part) own_seq(A, row[c]);
   }
   int lo_pos = row[0].pos, hi_pos = row[0].pos, lo_len = row[0].len, hi_len = row[0].len, lo_pfx = row[0].pfx, hi_pfx = row[0].pfx;
 #pragma unroll
@@ -657,10 +722,8 @@ attn_tile_kernel(AttnArgs A) {
   for (int c = 0; c < CT; ++c) pos[c] = row[c].pos;
   const AttnSteps steps = attn_steps(A, part_lo, part_hi, w_min_pos, w_max_pos, w_max_len, w_max_pfx);
   const int s0 = split * A.split_steps, s_end = min(steps.total, s0 + A.split_steps);
-  const int32_t* pages = A.table + (int64_t)max(seq, 0) * A.table_ld;
+  const int32_t* pages = A.table + (int64_t)max(sq.seq, 0) * A.table_ld;
 
-  // q as the step kernel holds it; a negative scale turns q's sign, so that the factor
-  // of the scores is positive and their maximum can be taken before it
   h16x8 qh[CT][NB];
   h16x8 ql[LO ? CT : 1][LO ? NB : 1];
   float c0[CT];
@@ -671,28 +734,14 @@ attn_tile_kernel(AttnArgs A) {
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     const int head = hk * A.group + row[c].head;
-    float x[NB][8], amax = 0.0f;
+    float x[NB][8];
     kv_load_row<NB>(A.ftype, A.q, row[c].tok * A.q_token + head * A.q_head + 8 * g, A.q_vec, x);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
-    }
-    amax = groups_max(amax);
-    const int ex = amax > 0.0f && amax < INFINITY ? min(max(11 - __builtin_amdgcn_frexp_expf(amax), -120), 120) : 0;
-    const float up = __builtin_ldexpf(A.scale < 0.0f ? -1.0f : 1.0f, ex);
-    const float c1 = fabsf(A.scale) * __builtin_ldexpf(1.0f, -ex);
+    const float c1 = q_operands<NB, LO>(A, x, qh[c], ql[LO ? c : 0]);
     c0[c] = capped ? c1 / A.softcap : c1 * LOG2E;
     if (g == 0) {
       s_tok[wave][c][col] = row[c].real ? row[c].tok : -1;
       s_head[wave][c][col] = head;
       s_slope[wave][c][col] = A.slopes ? A.slopes[head] * LOG2E : 0.0f;
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[b][e] *= up;
-      split8<LO>(x[b], qh[c][b], ql[LO ? c : 0][LO ? b : 0]);
     }
   }
 
@@ -1021,7 +1070,7 @@ constexpr int TILE_WAVES = 8, TILE_CT = 1, TILE_ROWS = 16 * TILE_WAVES * TILE_CT
 
 template <int TK, int TV, int NB, int PREC>
 static hipError_t tile_launch(const AttnArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)(a.tiles * a.n_split * a.n_kv_head);
+  const dim3 grid((unsigned)(a.tiles * a.n_kv_head), a.n_split);
   attn_tile_kernel<TK, TV, NB, TILE_WAVES, TILE_CT, PREC><<<grid, 64 * TILE_WAVES, 0, st>>>(a);
   return hipGetLastError();
 }
@@ -1033,7 +1082,7 @@ static hipError_t attn_launch(const AttnArgs& a, hipStream_t st) {
     if (a.ftype == FT_F16) return tile_launch<TK, TV, NB, PREC_F16>(a, st);
     return tile_launch<TK, TV, NB, PREC_BF16>(a, st);
   }
-  const unsigned grid = (unsigned)(a.tiles * a.n_split * a.n_kv_head);
+  const dim3 grid((unsigned)(a.tiles * a.n_kv_head), a.n_split);
   if (a.ftype == FT_F32) attn_step_kernel<TK, TV, NB, true><<<grid, 256, 0, st>>>(a);
   else attn_step_kernel<TK, TV, NB, false><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();

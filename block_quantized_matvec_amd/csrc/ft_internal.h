@@ -156,6 +156,7 @@ struct AttnArgs {
   int64_t out_token, out_head;
   int out_vec;
   int n_head, group;       // group = n_head / n_kv_head
+  uint64_t group_mul;      // 2^40 / group, rounded up: n / group = n * group_mul >> 40 for n < 2^30
   int n_tok, n_seq;
   const int32_t* q_start;  // [n_seq + 1]
   const int32_t* kv_len;   // [n_seq]
