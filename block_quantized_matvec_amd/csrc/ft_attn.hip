@@ -7,14 +7,17 @@
 namespace ftk {
 
 // One row's parts into its output: with M = max m, o = sum exp2(m - M) o_part / sum
-// exp2(m - M) l, the parts in order, so the result does not depend on which part was
-// done first.  D / 4 threads per row, four elements each.
+// exp2(m - M) l.  A wave per row: a lane per part for m and l, then D / 4 lanes per part
+// and 64 / (D / 4) parts at a time for o, added up in an order of their own, so the
+// result does not depend on which part was done first.  Bound by the latency of the
+// loads: all of a row's (m, l) go out at once, then four rounds of parts (31 parts of 80
+// rows: 22 us with a thread walking the parts, 6 us so).
 template <int D>
 __global__ void __launch_bounds__(256)
 attn_join_kernel(AttnArgs A, int parts) {
-  constexpr int TPR = D / 4;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = id / TPR;
+  constexpr int TPR = D / 4, PG = 64 / TPR;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
   if (row >= A.part_rows) return;
   int tok, head;
   if (A.step_rows && !A.tile_kernel) {   // the step kernel's rows: [seq][step_rows][n_kv_head]
@@ -30,28 +33,51 @@ attn_join_kernel(AttnArgs A, int parts) {
     if (tok < A.q_start[0] || tok >= A.q_start[A.n_seq]) return;   // no sequence's token
     if (A.step_rows && seq_rows(A, seq_of_token(A, tok)) <= A.step_rows) return;
   }
-  const int e = (int)(id - row * TPR) * 4;
   const f32x2* ml = (const f32x2*)A.part_ml;
-  float M = NO_MAX;
-  for (int p = 0; p < parts; ++p) M = fmaxf(M, ml[p * A.part_rows + row][0]);
-  float L = 0.0f;
+  float M = NO_MAX, L = 0.0f;
   f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const f32x2 v = ml[p * A.part_rows + row];
-    if (v[1] > 0.0f) {   // a part without keys wrote no row
-      const float f = __builtin_amdgcn_exp2f(v[0] - M);
-      L += f * v[1];
-      x += f * *(const f32x4*)(A.part_o + (p * A.part_rows + row) * D + e);
+  const int sub = lane / TPR, e = (lane - sub * TPR) * 4;
+  for (int p0 = 0; p0 < parts; p0 += 64) {
+    const int p = p0 + lane;
+    const f32x2 v = p < parts ? ml[p * A.part_rows + row] : f32x2{NO_MAX, 0.0f};
+    const float m = v[1] > 0.0f ? v[0] : NO_MAX;   // a part without keys wrote no row
+    const float Mn = fmaxf(M, route_val(wave_umax(route_key(m))));
+    const float back = __builtin_amdgcn_exp2f(M - Mn), f = v[1] > 0.0f ? __builtin_amdgcn_exp2f(m - Mn) : 0.0f;
+    M = Mn;
+    L = L * back + f * v[1];
+    x *= back;
+    const int n = min(64, parts - p0);
+    for (int q0 = 0; q0 < n; q0 += 4 * PG) {
+      float w[4];
+      f32x4 y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = q0 + u * PG + sub;
+        w[u] = __shfl(f, min(at, 63), 64);
+        y[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (at < n && sub < PG && w[u] > 0.0f) y[u] = *(const f32x4*)(A.part_o + ((p0 + at) * A.part_rows + row) * D + e);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x += w[u] * y[u];
     }
   }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d, 64);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float y = x[k];
+#pragma unroll
+    for (int s = 1; s < PG; ++s) y += __shfl(x[k], (lane + s * TPR) & 63, 64);   // lanes of the first part group
+    x[k] = y;
+  }
+  if (sub != 0) return;
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
   const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
   kv_store_n<4>(A.ftype, A.out, tok * A.out_token + head * A.out_head + e, A.out_vec, y);
 }
 
 static hipError_t join(const AttnArgs& a, int parts, hipStream_t st) {
-  const unsigned grid = (unsigned)((a.part_rows * (a.dim / 4) + 255) / 256);
+  const unsigned grid = (unsigned)((a.part_rows + 3) / 4);
   switch (a.dim) {
     case 64: attn_join_kernel<64><<<grid, 256, 0, st>>>(a, parts); break;
     case 96: attn_join_kernel<96><<<grid, 256, 0, st>>>(a, parts); break;
@@ -73,14 +99,15 @@ static hipError_t attn_dim(const AttnArgs& a, hipStream_t st) {
 
 }  // namespace ftk
 
-// Splits: `want` workgroups, but `least` steps in each.  Depends on the host's bounds
-// alone (max_kv, not the lengths on the device), so a captured call can be replayed
-// with other lengths.
-static AttnSplit split_keys(const AttnArgs& a, int64_t tiles, int64_t steps, int64_t want, int64_t least) {
+// Splits: `want` workgroups, of `least` steps or a few more each (whole rounds of `waves`
+// steps where a workgroup's waves take them in turn).  Depends on the host's bounds alone
+// (max_kv, not the lengths on the device), so a captured call can be replayed with other
+// lengths.
+static AttnSplit split_keys(const AttnArgs& a, int64_t tiles, int64_t steps, int64_t want, int64_t least, int64_t waves) {
   const int64_t wgs = std::max<int64_t>(tiles * a.n_kv_head, 1);
-  const int64_t n = std::max<int64_t>(1, std::min<int64_t>((want + wgs - 1) / wgs, steps / least));
+  const int64_t n = std::max<int64_t>(1, std::min<int64_t>((want + wgs - 1) / wgs, (steps + least - 1) / least));
   int64_t per = (steps + n - 1) / n;
-  per = std::max<int64_t>(least, (per + 3) / 4 * 4);
+  per = std::max<int64_t>(least, (per + waves - 1) / waves * waves);
   return {tiles, (int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per};
 }
 
@@ -98,15 +125,30 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
   };
   const bool many = rows > (int64_t)kStepRows * a.n_seq;   // more rows per sequence than the step kernel is for
   const int64_t part = (a.dim + 2) * sizeof(float);
-  if (many) p.tile = split_keys(a, rows / tile_rows + a.n_seq, steps(tile_rows), 512, 8);
+  if (many) p.tile = split_keys(a, rows / tile_rows + a.n_seq, steps(tile_rows), 512, 8, 1);
   if (many && a.n_seq > 1 && !a.n_shared) p.step_rows = kStepRows;
-  if (p.step_rows) p.step = split_keys(a, (int64_t)a.n_seq * (kStepRows / 16), steps(16), 512, 4);
-  else if (!many) p.step = split_keys(a, rows / 16 + a.n_seq, steps(16), 512, 4);
+  // Two workgroups per CU; twice as many, of eight steps at least, where there are some
+  // sequences already but not that many workgroups (32 ragged sequences of 8 heads: 80 us
+  // against 86; 8 of them: 28 against 33; two of 100000 keys: 90 against 101 the other way,
+  // as each workgroup takes 5 us to start and end)
+  const auto step_split = [&](int64_t tiles) {
+    const int64_t wgs = tiles * a.n_kv_head;
+    return wgs >= 64 && wgs < 512 ? split_keys(a, tiles, steps(16), 1024, 8, 4) : split_keys(a, tiles, steps(16), 512, 4, 4);
+  };
+  if (p.step_rows) p.step = step_split((int64_t)a.n_seq * (kStepRows / 16));
+  else if (!many) p.step = step_split(rows / 16 + a.n_seq);
+  // few workgroups with a block for each of eight waves: no split, no join (one user, 250
+  // keys: 9.2 us against 11.7; with two rounds, 777 keys, 13.8 against 11.2)
+  const AttnSplit whole = {rows / 16 + a.n_seq, 1, (int)steps(16)};
+  if (!many && !a.n_shared && a.dim <= 128 && p.step.n_split > 1 && whole.tiles * a.n_kv_head <= 256 && whole.split_steps <= 9) {
+    p.step = whole;
+    p.eight = 1;
+  }
   if (a.n_shared > 0) {
     p.shared_tile = rows > kStepRows;
     const int64_t n = a.n_shared / 64 + 1;
-    p.shared = p.shared_tile ? split_keys(a, (rows + tile_rows - 1) / tile_rows, n, 512, 8)
-                             : split_keys(a, (rows + 15) / 16, n, 512, 4);
+    p.shared = p.shared_tile ? split_keys(a, (rows + tile_rows - 1) / tile_rows, n, 512, 8, 1)
+                             : split_keys(a, (rows + 15) / 16, n, 512, 4, 4);
   }
   const int64_t all = (int64_t)a.n_tok * a.n_head;
   const int64_t parts = p.shared.n_split + (p.step_rows ? p.tile.n_split : p.tile.n_split + p.step.n_split);
@@ -134,6 +176,16 @@ hipError_t ftk_launch_attn(AttnArgs a, const AttnPlan& p, void* scratch, hipStre
   };
   with_parts(parts, (int64_t)a.n_tok * a.n_head, 0);
   hipError_t e = hipSuccess;
+  if (p.shared.tiles && !p.shared_tile && p.step.tiles) {   // both on the step kernel: one launch
+    a.shared_splits = p.shared.n_split;
+    a.shared_steps = p.shared.split_steps;
+    a.shared_tiles = (int)p.shared.tiles;
+    AttnSplit s = p.step;
+    s.tiles = std::max(p.step.tiles, p.shared.tiles);
+    s.n_split += p.shared.n_split;
+    e = run(s, 0);
+    return e == hipSuccess ? join(a, parts, st) : e;
+  }
   if (p.shared.tiles) {
     a.shared_part = 1;
     a.tile_kernel = p.shared_tile;
@@ -149,6 +201,7 @@ hipError_t ftk_launch_attn(AttnArgs a, const AttnPlan& p, void* scratch, hipStre
   if (p.step_rows) with_parts(p.step.n_split, (int64_t)a.n_seq * p.step_rows * a.n_kv_head, p.step_at);
   if (e == hipSuccess && p.step.tiles) {
     a.tile_kernel = 0;
+    a.eight = p.eight;
     e = run(p.step, p.step_rows ? 0 : p.shared.n_split);
   }
   const int last = p.step_rows ? p.step.n_split : parts;

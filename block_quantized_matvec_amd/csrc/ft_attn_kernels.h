@@ -16,13 +16,6 @@ constexpr float LOG2E = 1.44269504088896340736f;
 constexpr int ATTN_STEP = 64;    // keys per step of a wave
 constexpr float NO_MAX = -1e30f; // below every score
 
-// what this wave's lanes wrote to LDS is there for all of them (LDS serves a wave in
-// order; the fence keeps the compiler from moving accesses across)
-__device__ __forceinline__ void wave_lds_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // a value of the four lane groups (lanes l, l^16, l^32, l^48) met in all of them
 __device__ __forceinline__ float groups_max(float v) {
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -310,13 +303,12 @@ __device__ __forceinline__ float q_operands(const AttnArgs& A, float (&x)[NB][8]
 }
 
 // ---------------------------------------------------------------------------
-// up to 16 query rows per workgroup, its four waves taking the 64-key blocks in turn
+// up to 16 query rows per workgroup, its waves taking the 64-key blocks in turn
 // ---------------------------------------------------------------------------
-template <int TK, int TV, int NB, bool LO>
-__global__ void __launch_bounds__(256, NB <= 4 ? 2 : 1)
+template <int TK, int TV, int NB, int NW, bool LO>
+__global__ void __launch_bounds__(64 * NW, NB <= 4 || NW > 4 ? 2 : 1)
 attn_step_kernel(AttnArgs A) {
   constexpr int D = NB * 32;
-  constexpr int NW = 4;
   using C = KvCodes<TK>;
   constexpr int NG = (NB + C::GROUP - 1) / C::GROUP;
   constexpr int VT = TV == FT_Q8_0 ? 2 * NB : NB;            // 16-row pieces of V^T
@@ -327,7 +319,12 @@ attn_step_kernel(AttnArgs A) {
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int col = lane & 15, g = lane >> 4;
   const int tile = blockIdx.x / (unsigned)A.n_kv_head, hk = blockIdx.x - tile * A.n_kv_head;
-  const int split = blockIdx.y;
+  // the part of the keys: those that all share (the first splits, where there are any of
+  // them in this launch), or the sequence's own
+  const bool shared = A.shared_part || (int)blockIdx.y < A.shared_splits;
+  const int split = shared ? (int)blockIdx.y : (int)blockIdx.y - A.shared_splits;
+  const int per_split = shared && A.shared_splits ? A.shared_steps : A.split_steps;
+  if (shared && A.shared_splits && tile >= A.shared_tiles) return;
 
   AttnSeq sq;
   int first = tile * 16;
@@ -336,7 +333,7 @@ attn_step_kernel(AttnArgs A) {
     sq = seq_facts(A, (int)((unsigned)tile / per));
     first = (int)((unsigned)tile % per) * 16;
     if ((sq.q1 - sq.q0) * A.group > A.step_rows) return;
-  } else if (A.shared_part) {
+  } else if (shared) {
     sq = all_rows(A);
   } else {
     sq = seq_of_tile<16>(A, tile, lane);
@@ -344,16 +341,16 @@ attn_step_kernel(AttnArgs A) {
   }
   AttnRow row = attn_row(A, sq, first, col);
   if (!__ballot(row.real)) return;   // a tile past its sequence's rows
-  if (A.shared_part) own_seq(A, row);
+  if (shared) own_seq(A, row);
 
   const int min_pos = row_min(row.pos), max_pos = row_max(row.pos);
   const int min_len = row_min(row.len), max_len = row_max(row.len);
   const int min_pfx = row_min(row.pfx), max_pfx = row_max(row.pfx);
-  const int part_lo = A.shared_part ? 0 : A.n_shared, part_hi = A.shared_part ? A.n_shared : A.max_kv;
+  const int part_lo = shared ? 0 : A.n_shared, part_hi = shared ? A.n_shared : A.max_kv;
   const AttnSeen seen = seen_by(A, row, part_hi);
   const AttnSteps steps = attn_steps(A, part_lo, part_hi, min_pos, max_pos, max_len, max_pfx);
-  const int s_end = min(steps.total, (split + 1) * A.split_steps);
-  const int s0 = split * A.split_steps + wave;
+  const int s_end = min(steps.total, (split + 1) * per_split);
+  const int s0 = split * per_split + wave;
   const int s_last = s0 + (s_end - 1 - s0) / NW * NW;   // this wave's last step (where there is one)
   const int32_t* pages = A.table + (int64_t)max(sq.seq, 0) * A.table_ld;
 
@@ -428,7 +425,8 @@ attn_step_kernel(AttnArgs A) {
   const int end = min(max_len, part_hi);   // slots from here on may hold anything
 
   // Each load goes out as soon as its registers are free, a step (of this wave) ahead;
-  // behind the last step the last one is loaded again.
+  // behind the last step the last one is loaded again (a branch around the loads costs
+  // registers on both its sides: spills, 112 -> 176 us at 64 x 4096 keys).
   for (int i = s0; i < s_end; i += NW) {
     const int next = min(i + NW, s_last);
     const int key0 = steps.block(i) * ATTN_STEP, last = key0 + ATTN_STEP - 1;
@@ -564,11 +562,14 @@ attn_step_kernel(AttnArgs A) {
     s_m[wave][col] = m;
     s_l[wave][col] = l;
   }
+  if (row.real) {
 #pragma unroll
-  for (int i = 0; i < 2 * NB; ++i) *(f32x4*)&s_o[wave][col][16 * i + 4 * g] = o[i];
-  __syncthreads();
-  // 16 threads per row, four consecutive elements each at a time
-  const int r = threadIdx.x >> 4, e0 = (threadIdx.x & 15) * 4;
+    for (int i = 0; i < 2 * NB; ++i) *(f32x4*)&s_o[wave][col][16 * i + 4 * g] = o[i];
+  }
+  lds_barrier();
+  // 4 NW threads per row, four consecutive elements each at a time
+  constexpr int TR = 4 * NW;
+  const int r = threadIdx.x / TR, e0 = (threadIdx.x % TR) * 4;
   float M = s_m[0][r];
 #pragma unroll
   for (int w = 1; w < NW; ++w) M = fmaxf(M, s_m[w][r]);
@@ -583,13 +584,13 @@ attn_step_kernel(AttnArgs A) {
   const int oh = hk * A.group + out.head;
   if (A.part_o) {
     const int64_t at = A.step_rows ? ((int64_t)sq.seq * A.step_rows + first + r) * A.n_kv_head + hk : (int64_t)out.tok * A.n_head + oh;
-    const int64_t ps = (A.split0 + split) * A.part_rows + at;
-    if ((threadIdx.x & 15) == 0) {
+    const int64_t ps = (A.split0 + (int)blockIdx.y) * A.part_rows + at;
+    if (threadIdx.x % TR == 0) {
       A.part_ml[2 * ps] = L > 0.0f ? M : NO_MAX;
       A.part_ml[2 * ps + 1] = L;
     }
     if (!(L > 0.0f)) return;   // the join skips it
-    for (int e = e0; e < D; e += 64) {
+    for (int e = e0; e < D; e += 4 * TR) {
       f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < NW; ++w) x += f[w] * *(const f32x4*)&s_o[w][r][e];
@@ -598,7 +599,7 @@ attn_step_kernel(AttnArgs A) {
     return;
   }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  for (int e = e0; e < D; e += 64) {
+  for (int e = e0; e < D; e += 4 * TR) {
     f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < NW; ++w) x += f[w] * *(const f32x4*)&s_o[w][r][e];
@@ -1083,8 +1084,14 @@ static hipError_t attn_launch(const AttnArgs& a, hipStream_t st) {
     return tile_launch<TK, TV, NB, PREC_BF16>(a, st);
   }
   const dim3 grid((unsigned)(a.tiles * a.n_kv_head), a.n_split);
-  if (a.ftype == FT_F32) attn_step_kernel<TK, TV, NB, true><<<grid, 256, 0, st>>>(a);
-  else attn_step_kernel<TK, TV, NB, false><<<grid, 256, 0, st>>>(a);
+  if (NB <= 4 && a.eight) {   // eight waves for a few blocks of keys: one launch, nothing to join
+    constexpr int B = NB <= 4 ? NB : 4;
+    if (a.ftype == FT_F32) attn_step_kernel<TK, TV, B, 8, true><<<grid, 512, 0, st>>>(a);
+    else attn_step_kernel<TK, TV, B, 8, false><<<grid, 512, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  if (a.ftype == FT_F32) attn_step_kernel<TK, TV, NB, 4, true><<<grid, 256, 0, st>>>(a);
+  else attn_step_kernel<TK, TV, NB, 4, false><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -172,7 +172,9 @@ struct AttnArgs {
   int n_shared;            // leading keys that all sequences share; 0: none
   // set by the planner, per launch
   int shared_part;         // 1: the rows of all sequences over the shared keys
+  int shared_splits, shared_steps, shared_tiles;   // > 0: this launch's first splits are the shared part
   int tile_kernel;         // 1: many rows per workgroup
+  int eight;               // the step kernel with eight waves
   int step_rows;           // both kernels run: sequences of at most this many rows go to the step kernel
   int64_t tiles;
   int n_split, split_steps, split0;   // splits of the keys; this launch's first partial
@@ -187,7 +189,7 @@ struct AttnSplit {
 struct AttnPlan {
   AttnSplit shared, tile, step;   // tiles 0: no such launch
   int shared_tile;         // the shared part runs on the tile kernel
-  int step_rows;
+  int step_rows, eight;
   size_t scratch;          // bytes of partial results; 0: none
   size_t step_at;          // byte offset of the step kernel's, with step_rows
 };

@@ -16,6 +16,13 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
 
+// what this wave's lanes wrote to LDS is there for all of them (LDS serves a wave in
+// order; the fence keeps the compiler from moving accesses across)
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // One page head: the codes of `page` keys (D elements each), then the fp16 scales
 // [D/32][page].
 __host__ __device__ constexpr int kv_code_bytes(int type, int dim, int page) {

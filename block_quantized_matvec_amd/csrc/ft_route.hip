@@ -57,13 +57,6 @@ __device__ __forceinline__ f32x4 quad_at(const RouteArgs& A, int64_t tok, int e)
   return v;
 }
 
-// what this wave's lanes wrote to LDS is there for all of them (LDS serves a wave in
-// order; the fence keeps the compiler from moving accesses across)
-__device__ __forceinline__ void wave_lds_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // One token by a whole wave in fp64: lane l holds experts l*M .. l*M + M-1, so lane
 // order is expert order.  LDS of the wave's own: choices (groups only), w and id.
 template <int MAXE>

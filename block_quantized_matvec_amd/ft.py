@@ -217,47 +217,33 @@ def moe_route(logits: torch.Tensor, topk: int, ids: torch.Tensor | None = None, 
 
 
 def _float_type(t: torch.Tensor, name: str) -> int:
-    try:
-        return FLOATS[t.dtype]
-    except KeyError:
-        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}") from None
+    ty = FLOATS.get(t.dtype)
+    if ty is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    return ty
 
 
-def _same_device(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, not {t.device}")
+def _plain(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> int:
+    """Pointer of a contiguous tensor of this type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _ints(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)}")
-    return t
-
-
-class _on:
-    """The stream for a call on `device`: the caller's, or the current one of that device (which the library
-    then sees as its current device)."""
-
-    def __init__(self, device, stream):
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        if s.device != self.device:
-            self.__exit__()
-            raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
-        return s.cuda_stream
-
-    def __exit__(self, *_):
-        if self.guard is not None:
-            self.guard.__exit__(None, None, None)
+def _call(name: str, device, stream, *args) -> None:
+    """The entry point `name` on the caller's stream, or the current one of `device`, which the library then sees as
+    its current device (torch's own handles of both: its Stream objects cost more than the rest of a small call)."""
+    f = getattr(lib(), name)
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            status = f(*args, s.cuda_stream)
+    _check(status, name)
 
 
 def moe_route_ex(logits: torch.Tensor, topk: int, score: str = "softmax", bias: torch.Tensor | None = None,
@@ -272,29 +258,22 @@ def moe_route_ex(logits: torch.Tensor, topk: int, score: str = "softmax", bias: 
     if score not in ("softmax", "sigmoid"):
         raise ValueError(f"score must be softmax or sigmoid, not {score}")
     t, e = logits.shape
-    if e > 1 and logits.stride(1) != 1 or (t > 1 and logits.stride(0) < e):
+    ld, step = logits.stride()
+    if e > 1 and step != 1 or (t > 1 and ld < e):
         raise ValueError("logits must have unit element stride and rows at least n_expert apart")
-    dev = logits.device
-    _same_device(dev, bias=bias, ids=ids, w=w)
-    if bias is not None:
-        _ints(bias, "bias", torch.float32, (e,))
-    if ids is None:
-        ids = torch.empty((t, topk), dtype=torch.int32, device=dev)
-    else:
-        _ints(ids, "ids", torch.int32, (t, topk))
-    if w is None:
-        w = torch.empty((t, topk), dtype=torch.float32, device=dev)
-    else:
-        _ints(w, "w", torch.float32, (t, topk))
     if not scale:
         raise ValueError("scale must not be 0")
-    if n_group < 1 or topk_group is not None and topk_group < 1 or group_top < 1:
-        raise ValueError("n_group, topk_group and group_top start at 1")
-    o = _RouteOpts(score == "sigmoid", None if bias is None else bias.data_ptr(), n_group, topk_group or 0, group_top,
-                   not renorm, scale)
-    with _on(dev, stream) as s:
-        _check(lib().ft_moe_route_ex(logits.data_ptr(), ty, t, e, logits.stride(0) if t > 1 else e, topk,
-                                     ctypes.byref(o), ids.data_ptr(), w.data_ptr(), s), "ft_moe_route_ex")
+    if n_group < 1 or topk_group is not None and topk_group < 1 or group_top < 1 or topk < 1:
+        raise ValueError("topk, n_group, topk_group and group_top start at 1")
+    dev = logits.device
+    if ids is None:
+        ids = torch.empty((t, topk), dtype=torch.int32, device=dev)
+    if w is None:
+        w = torch.empty((t, topk), dtype=torch.float32, device=dev)
+    o = _RouteOpts(score == "sigmoid", None if bias is None else _plain(bias, "bias", torch.float32, (e,), dev), n_group,
+                   topk_group or 0, group_top, not renorm, scale)
+    _call("ft_moe_route_ex", dev, stream, logits.data_ptr(), ty, t, e, ld if t > 1 else e, topk, ctypes.byref(o),
+          _plain(ids, "ids", torch.int32, (t, topk), dev), _plain(w, "w", torch.float32, (t, topk), dev))
     return ids, w
 
 
@@ -428,7 +407,8 @@ class KvCache:
         if not n or k_pages.numel() != n * kb or v_pages.numel() != n * vb:
             raise ValueError(f"the pools hold {k_pages.numel()} and {v_pages.numel()} bytes: want a whole number of "
                              f"pages, the same for both, of {kb} and {vb} bytes")
-        _same_device(k_pages.device, v_pages=v_pages)
+        if v_pages.device != k_pages.device:
+            raise ValueError(f"k_pages are on {k_pages.device}, v_pages on {v_pages.device}")
         self.k_pages, self.v_pages, self.device = k_pages, v_pages, k_pages.device
         self.k, self.v = k, v
         self.n_pages, self.page_size, self.n_kv_head, self.head_dim = n, page_size, n_kv_head, head_dim
@@ -444,53 +424,44 @@ class KvCache:
         return cls(*pools, page_size, n_kv_head, head_dim, k, v)
 
 
-def _rows(t: torch.Tensor, name: str, shape, device, ty: int):
-    """Token and head strides of a (tokens, heads, dim) tensor."""
-    if t.device != device or tuple(t.shape) != tuple(shape) or FLOATS.get(t.dtype) != ty:
-        raise ValueError(f"{name} must be {tuple(shape)} of one float type on {device}, "
-                         f"not {tuple(t.shape)} {t.dtype} on {t.device}")
-    if t.stride(2) != 1:
-        raise ValueError(f"{name} must have unit element stride")
-    return t.stride(0), t.stride(1)
+def _rows(t: torch.Tensor, name: str, shape: tuple, dtype, device) -> tuple:
+    """Strides of a (tokens, heads, dim) tensor."""
+    st = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.device != device or st[2] != 1:
+        raise ValueError(f"{name} must be {shape} {dtype} on {device} with unit element stride, "
+                         f"not {tuple(t.shape)} {t.dtype} on {t.device} with strides {st}")
+    return st
 
 
 def kv_store(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
     """Quantize k, v ((t, n_kv_head, head_dim), float32, float16 or bfloat16, strided tokens and heads) into the slots
     (int64 (t,), distinct; a negative one is skipped)."""
-    t = k.shape[0]
-    ty = _float_type(k, "k")
-    dev, shape = cache.device, (t, cache.n_kv_head, cache.head_dim)
-    kt, kh = _rows(k, "k", shape, dev, ty)
-    vt, vh = _rows(v, "v", shape, dev, ty)
-    _same_device(dev, slots=slots)
-    _ints(slots, "slots", torch.int64, (t,))
-    with _on(dev, stream) as s:
-        _check(lib().ft_kv_store(cache._ref, ty, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), t, s),
-               "ft_kv_store")
+    t, dev = k.shape[0], cache.device
+    ty, shape = _float_type(k, "k"), (t, cache.n_kv_head, cache.head_dim)
+    ks, vs = _rows(k, "k", shape, k.dtype, dev), _rows(v, "v", shape, k.dtype, dev)
+    _call("ft_kv_store", dev, stream, cache._ref, ty, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+          _plain(slots, "slots", torch.int64, (t,), dev), t)
 
 
 def kv_load(cache: KvCache, slots: torch.Tensor, dtype=torch.float32, k: torch.Tensor | None = None,
             v: torch.Tensor | None = None, stream=None):
     """The slots' rows as plain numbers: (k, v), each (t, n_kv_head, head_dim) of dtype, into the given tensors where
     there are any (whose type then counts).  A negative slot gives zeros."""
-    t = slots.shape[0]
-    dev, shape = cache.device, (t, cache.n_kv_head, cache.head_dim)
+    t, dev = slots.shape[0], cache.device
+    shape = (t, cache.n_kv_head, cache.head_dim)
     if k is not None or v is not None:
         dtype = (k if k is not None else v).dtype
     if dtype not in FLOATS:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
-    ty = FLOATS[dtype]
-    if k is None:
+    if k is None and v is None:
+        k, v = torch.empty((2, *shape), dtype=dtype, device=dev)
+    elif k is None:
         k = torch.empty(shape, dtype=dtype, device=dev)
-    if v is None:
+    elif v is None:
         v = torch.empty(shape, dtype=dtype, device=dev)
-    kt, kh = _rows(k, "k", shape, dev, ty)
-    vt, vh = _rows(v, "v", shape, dev, ty)
-    _same_device(dev, slots=slots)
-    _ints(slots, "slots", torch.int64, (t,))
-    with _on(dev, stream) as s:
-        _check(lib().ft_kv_load(cache._ref, slots.data_ptr(), t, ty, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, s),
-               "ft_kv_load")
+    ks, vs = _rows(k, "k", shape, dtype, dev), _rows(v, "v", shape, dtype, dev)
+    _call("ft_kv_load", dev, stream, cache._ref, _plain(slots, "slots", torch.int64, (t,), dev), t, FLOATS[dtype],
+          k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
     return k, v
 
 
@@ -514,38 +485,31 @@ def attn_kv(cache: KvCache, q: torch.Tensor, table: torch.Tensor, kv_len: torch.
     (pages of table row 0).  workspace: uint8, attn_kv_scratch_bytes (default: the stream's pool)."""
     if q.dim() != 3:
         raise ValueError("q must be (n_tok, n_head, head_dim)")
-    ty = _float_type(q, "q")
-    n_tok, n_head, dim = q.shape
-    dev = cache.device
-    qt, qh = _rows(q, "q", (n_tok, n_head, cache.head_dim), dev, ty)
+    ty, dev, shape = _float_type(q, "q"), cache.device, q.shape
+    n_tok, n_head, dim = shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q has rows of {dim}, the cache of {cache.head_dim}")
+    qs = _rows(q, "q", shape, q.dtype, dev)
     n_seq = kv_len.shape[0]
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_seq or \
-            (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("table must be int32 (n_seq, pages) with unit element stride")
+    ld, step = table.stride() if table.dim() == 2 else (0, 0)
+    if step != 1 or table.shape[0] != n_seq or table.dtype is not torch.int32 or table.device != dev:
+        raise ValueError(f"table must be int32 (n_seq, pages) on {dev} with unit element stride")
     cols = table.shape[1]
-    table_ld = table.stride(0) if n_seq > 1 else cols
-    _ints(kv_len, "kv_len", torch.int32, (n_seq,))
-    _ints(q_start, "q_start", torch.int32, (n_seq + 1,))
-    _same_device(dev, table=table, kv_len=kv_len, q_start=q_start, slopes=slopes, prefix_len=prefix_len,
-                 workspace=workspace)
-    if slopes is not None:
-        _ints(slopes, "slopes", torch.float32, (n_head,))
-    if prefix_len is not None:
-        _ints(prefix_len, "prefix_len", torch.int32, (n_seq,))
     if scale is not None and not scale:
         raise ValueError("scale must not be 0")
     if out is None:
-        out = torch.empty((n_tok, n_head, dim), dtype=q.dtype, device=dev)
-    ot, oh = _rows(out, "out", (n_tok, n_head, dim), dev, ty)
-    ws, ws_bytes = None, 0
+        out = q.new_empty(shape)
+    os_ = _rows(out, "out", shape, q.dtype, dev)
+    o = _AttnOpts(scale or 0.0, softcap, not causal, window,
+                  None if slopes is None else _plain(slopes, "slopes", torch.float32, (n_head,), dev),
+                  None if prefix_len is None else _plain(prefix_len, "prefix_len", torch.int32, (n_seq,), dev), n_shared,
+                  None, 0)
     if workspace is not None:
-        _dev(workspace, "workspace")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    o = _AttnOpts(scale or 0.0, softcap, not causal, window, None if slopes is None else slopes.data_ptr(),
-                  None if prefix_len is None else prefix_len.data_ptr(), n_shared, ws, ws_bytes)
-    with _on(dev, stream) as s:
-        _check(lib().ft_attn_kv(cache._ref, ty, q.data_ptr(), qt, qh, n_tok, n_head, q_start.data_ptr(),
-                                kv_len.data_ptr(), table.data_ptr(), table_ld, cols, n_seq,
-                                cols * cache.page_size if max_kv is None else max_kv, out.data_ptr(), ot, oh,
-                                ctypes.byref(o), s), "ft_attn_kv")
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        o.workspace, o.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call("ft_attn_kv", dev, stream, cache._ref, ty, q.data_ptr(), qs[0], qs[1], n_tok, n_head,
+          _plain(q_start, "q_start", torch.int32, (n_seq + 1,), dev), _plain(kv_len, "kv_len", torch.int32, (n_seq,), dev),
+          table.data_ptr(), ld if n_seq > 1 else cols, cols, n_seq,
+          cols * cache.page_size if max_kv is None else max_kv, out.data_ptr(), os_[0], os_[1], ctypes.byref(o))
     return out

@@ -127,7 +127,7 @@ def test_attention_scratch():
     n = lambda *a: ft.lib().ft_attn_kv_scratch_bytes(ctypes.byref(c), *a, None)  # noqa: E731
     assert n(1, 4, 1, 16000) > 0
     assert n(0, 4, 1, 16000) == 0 and n(1, 3, 1, 16000) == 0
-    assert n(4096, 4, 1, 4096) == 0                              # enough rows: the keys stay whole
+    assert n(1 << 17, 4, 1, 1 << 17) == 0                        # enough rows: the keys stay whole
 
 
 def test_route_refused():
