@@ -108,7 +108,7 @@ static AttnSplit split_keys(const AttnArgs& a, int64_t tiles, int64_t steps, int
   const int64_t n = std::max<int64_t>(1, std::min<int64_t>((want + wgs - 1) / wgs, (steps + least - 1) / least));
   int64_t per = (steps + n - 1) / n;
   per = std::max<int64_t>(least, (per + waves - 1) / waves * waves);
-  return {tiles, (int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per};
+  return {tiles, (int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per, 0};
 }
 
 AttnPlan ftk_attn_plan(const AttnArgs& a) {
@@ -116,7 +116,7 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
   AttnPlan p = {};
   constexpr int kStepRows = 32;
   const int64_t rows = (int64_t)a.n_tok * a.group;
-  constexpr int tile_rows = TILE_ROWS;
+  const int prec = a.ftype == FT_F32 ? PREC_F32 : a.ftype == FT_F16 ? PREC_F16 : PREC_BF16;
   // under a causal window a tile sees the window of its tokens only
   const auto steps = [&](int64_t tile) {
     int64_t span = a.max_kv - a.n_shared;
@@ -125,7 +125,21 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
   };
   const bool many = rows > (int64_t)kStepRows * a.n_seq;   // more rows per sequence than the step kernel is for
   const int64_t part = (a.dim + 2) * sizeof(float);
-  if (many) p.tile = split_keys(a, rows / tile_rows + a.n_seq, steps(tile_rows), 512, 8, 1);
+  // the tile kernel over `rows` in `seqs` sequences.  Twice the rows per workgroup where
+  // the half tile that each sequence leaves empty on average weighs little and the keys'
+  // steps are many
+  const auto tiles = [&](int64_t rows, int64_t seqs, bool shared) {
+    const auto n_tiles = [&](int64_t tile) { return shared ? (rows + tile - 1) / tile : rows / tile + seqs; };
+    const auto n_steps = [&](int64_t tile) { return shared ? (int64_t)a.n_shared / 64 + 1 : steps(tile); };
+    const int64_t two = 2 * TILE_ROWS;
+    const bool fits = shared ? 20 * n_tiles(TILE_ROWS) >= 36 * n_tiles(two) : rows >= 2 * two * seqs;
+    const bool wide = tile_has_wide(prec, a.dim / 32) && fits && n_tiles(two) * n_steps(two) * a.n_kv_head >= 2048;
+    const int64_t tile = wide ? two : TILE_ROWS;
+    AttnSplit s = split_keys(a, n_tiles(tile), n_steps(tile), 512, 8, 1);
+    s.wide = wide;
+    return s;
+  };
+  if (many) p.tile = tiles(rows, a.n_seq, false);
   if (many && a.n_seq > 1 && !a.n_shared) p.step_rows = kStepRows;
   // Two workgroups per CU; twice as many, of eight steps at least, where there are some
   // sequences already but not that many workgroups (32 ragged sequences of 8 heads: 80 us
@@ -139,16 +153,14 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
   else if (!many) p.step = step_split(rows / 16 + a.n_seq);
   // few workgroups with a block for each of eight waves: no split, no join (one user, 250
   // keys: 9.2 us against 11.7; with two rounds, 777 keys, 13.8 against 11.2)
-  const AttnSplit whole = {rows / 16 + a.n_seq, 1, (int)steps(16)};
+  const AttnSplit whole = {rows / 16 + a.n_seq, 1, (int)steps(16), 0};
   if (!many && !a.n_shared && a.dim <= 128 && p.step.n_split > 1 && whole.tiles * a.n_kv_head <= 256 && whole.split_steps <= 9) {
     p.step = whole;
     p.eight = 1;
   }
   if (a.n_shared > 0) {
     p.shared_tile = rows > kStepRows;
-    const int64_t n = a.n_shared / 64 + 1;
-    p.shared = p.shared_tile ? split_keys(a, (rows + tile_rows - 1) / tile_rows, n, 512, 8, 1)
-                             : split_keys(a, (rows + 15) / 16, n, 512, 4, 4);
+    p.shared = p.shared_tile ? tiles(rows, 1, true) : split_keys(a, (rows + 15) / 16, a.n_shared / 64 + 1, 512, 4, 4);
   }
   const int64_t all = (int64_t)a.n_tok * a.n_head;
   const int64_t parts = p.shared.n_split + (p.step_rows ? p.tile.n_split : p.tile.n_split + p.step.n_split);
@@ -171,6 +183,7 @@ hipError_t ftk_launch_attn(AttnArgs a, const AttnPlan& p, void* scratch, hipStre
     a.tiles = s.tiles;
     a.n_split = s.n_split;
     a.split_steps = s.split_steps;
+    a.tile_wide = s.wide;
     a.split0 = split0;
     return attn_dim(a, st);
   };

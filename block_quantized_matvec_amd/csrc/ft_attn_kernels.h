@@ -44,25 +44,25 @@ __device__ __forceinline__ int row_min(int v) {
 }
 __device__ __forceinline__ int row_max(int v) { return -row_min(-v); }
 
-// c * tanh(x / c) in the units of `cap`; x comes divided by c.
+// c * tanh(x / c) in the units of `cap`; x comes divided by c, without EXACT times 2 log2(e).
 // EXACT: an odd series below 0.35 (its next term is under 2^-26 of the result), else
 // 1 - 2 / (exp(2x) + 1), within 2^-22.6 absolute; without EXACT the latter throughout
 // (its absolute error is what matters to a score, and 2^-22 * c is far below the
 // rounding of 16-bit probabilities).
 template <bool EXACT>
 __device__ __forceinline__ float capped_score(float x, float cap) {
-  const float t = __builtin_amdgcn_exp2f(x * (2.0f * LOG2E));
-  float y = fmaf(-2.0f, __builtin_amdgcn_rcpf(t + 1.0f), 1.0f);
+  const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(EXACT ? x * (2.0f * LOG2E) : x) + 1.0f);
   if constexpr (EXACT) {
+    const float y = fmaf(-2.0f, r, 1.0f);
     const float q = x * x;
     float p = fmaf(q, -1382.0f / 155925.0f, 62.0f / 2835.0f);
     p = fmaf(q, p, -17.0f / 315.0f);
     p = fmaf(q, p, 2.0f / 15.0f);
     p = fmaf(q, p, -1.0f / 3.0f);
     p = fmaf(x * q, p, x);
-    y = fabsf(x) < 0.35f ? p : y;
+    return cap * (fabsf(x) < 0.35f ? p : y);
   }
-  return cap * y;
+  return fmaf(-2.0f * cap, r, cap);
 }
 
 // two fp16 numbers of a word (by value: a bit cast of a vector's element would read the
@@ -415,7 +415,7 @@ attn_step_kernel(AttnArgs A) {
   h16x8 qh[NB], ql[LO ? NB : 1];
   const float c1 = q_operands<NB, LO>(A, x, qh, ql);
   const bool capped = A.softcap > 0.0f, plain = !capped && !A.slopes;
-  const float c0 = capped ? c1 / A.softcap : c1 * LOG2E, cap = A.softcap * LOG2E;
+  const float c0 = capped ? c1 / A.softcap * (LO ? 1.0f : 2.0f * LOG2E) : c1 * LOG2E, cap = A.softcap * LOG2E;
   const float k0 = plain ? c0 : 1.0f;   // the factor can wait for the exponent
 
   float m = NO_MAX, l = 0.0f;
@@ -652,7 +652,7 @@ struct TileLds {
 };
 
 template <int TK, int TV, int NB, int NW, int CT, int PREC>
-__global__ void __launch_bounds__(64 * NW, NB <= 3 || (NB == 4 && PREC != PREC_F32) ? 4 : 2)
+__global__ void __launch_bounds__(64 * NW, CT == 1 && (NB <= 3 || (NB == 4 && PREC != PREC_F32)) ? 4 : 2)
 attn_tile_kernel(AttnArgs A) {
   constexpr int D = NB * 32, T = 64 * NW, ROWS = NW * 16 * CT;
   constexpr bool LO = PREC == PREC_F32;
@@ -738,7 +738,7 @@ attn_tile_kernel(AttnArgs A) {
     float x[NB][8];
     kv_load_row<NB>(A.ftype, A.q, row[c].tok * A.q_token + head * A.q_head + 8 * g, A.q_vec, x);
     const float c1 = q_operands<NB, LO>(A, x, qh[c], ql[LO ? c : 0]);
-    c0[c] = capped ? c1 / A.softcap : c1 * LOG2E;
+    c0[c] = capped ? c1 / A.softcap * (LO ? 1.0f : 2.0f * LOG2E) : c1 * LOG2E;
     if (g == 0) {
       s_tok[wave][c][col] = row[c].real ? row[c].tok : -1;
       s_head[wave][c][col] = head;
@@ -761,7 +761,11 @@ attn_tile_kernel(AttnArgs A) {
   const int cb_k = kv_code_bytes(TK, D, A.page), cb_v = kv_code_bytes(TV, D, A.page);
   const uint32_t pb_k = (uint32_t)A.n_kv_head * hb_k, pb_v = (uint32_t)A.n_kv_head * hb_v;   // under 2^30
   const uint8_t *k_head = A.k_pages + (uint32_t)hk * hb_k, *v_head = A.v_pages + (uint32_t)hk * hb_v;
-  const auto page_of = [&](int key) { return (uint32_t)page_at(pages, key >> A.page_shift, A.cols, A.n_pages); };
+  // page ids are known a step before the loads that need them, as a load behind an id waits
+  // for every load before it; not where the registers for it would be spilled
+  constexpr bool AHEAD = !(NB == 4 && CT == 1 && PREC != PREC_F32);
+  const auto raw_page = [&](int key) { return pages[min(key >> A.page_shift, A.cols - 1)]; };
+  const auto pool_page = [&](int id) { return (uint32_t)min(max(id, 0), A.n_pages - 1); };   // clamped, never followed
 
   const int slot = operand_slot(g, col);
   // this thread's part of a step: K units (group p of blocks, key j, lane group kg_) and V
@@ -771,10 +775,17 @@ attn_tile_kernel(AttnArgs A) {
   uint32_t kw[KU][4];
   uint16_t ksc[PREC == PREC_BF16 ? NB : 1];
   u32x4 vw[VU], sc;
+  int id_k, id_v, id_s;
+  const auto fetch_ids = [&](int key0) {
+    id_k = raw_page(key0 + j);
+    id_v = raw_page(key0 + 16 * vg_);
+    id_s = raw_page(key0 + 8 * (lane & 7));
+  };
   const auto fetch = [&](int key0) {
     const int key = key0 + j, keyv = key0 + 16 * vg_;
-    const uint8_t* kc = k_head + (uint64_t)page_of(key) * pb_k;
-    const uint8_t* vc = v_head + (uint64_t)page_of(keyv) * pb_v;
+    if constexpr (!AHEAD) fetch_ids(key0);
+    const uint8_t* kc = k_head + (uint64_t)pool_page(id_k) * pb_k;
+    const uint8_t* vc = v_head + (uint64_t)pool_page(id_v) * pb_v;
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       const int p = (tid + i * T) >> 8;   // uniform over a wave
@@ -800,7 +811,7 @@ attn_tile_kernel(AttnArgs A) {
     }
     if (wave < (PREC == PREC_BF16 ? 1 : 2) && lane < NB * 8) {   // the scales, eight keys per lane: V's, and K's
       const int kk = key0 + 8 * (lane & 7), b = lane >> 3;
-      const uint64_t pg = page_of(kk);
+      const uint64_t pg = pool_page(id_s);
       const uint8_t* src = wave == 0 ? v_head + pg * pb_v + cb_v : k_head + pg * pb_k + cb_k;
       sc = *(const u32x4*)(src + 2 * (b * A.page + (kk & page_mask)));
     }
@@ -883,17 +894,20 @@ attn_tile_kernel(AttnArgs A) {
 
   if (s0 < s_end) {
     const int key0 = steps.block(s0) * ATTN_STEP;
+    if constexpr (AHEAD) fetch_ids(key0);
     fetch(key0);
+    if constexpr (AHEAD) fetch_ids(steps.block(min(s0 + 1, s_end - 1)) * ATTN_STEP);
     commit(0, key0);
   }
   for (int i = s0; i < s_end; ++i) {
     const int buf = (i - s0) & 1;
     const int key0 = steps.block(i) * ATTN_STEP;
     int key1 = 0;
-    __syncthreads();
+    lds_barrier();
     if (i + 1 < s_end) {
       key1 = steps.block(i + 1) * ATTN_STEP;
       fetch(key1);
+      if constexpr (AHEAD) fetch_ids(steps.block(min(i + 2, s_end - 1)) * ATTN_STEP);
     }
     const int last = key0 + ATTN_STEP - 1;
     {
@@ -1066,13 +1080,21 @@ attn_tile_kernel(AttnArgs A) {
   }
 }
 
-// rows of a workgroup of the tile kernel
-constexpr int TILE_WAVES = 8, TILE_CT = 1, TILE_ROWS = 16 * TILE_WAVES * TILE_CT;
+// the tile kernel: rows of a workgroup with one 16-row operand per wave, or with two (wide)
+constexpr int TILE_WAVES = 8, TILE_ROWS = 16 * TILE_WAVES;
+// where two fit the registers
+constexpr bool tile_has_wide(int prec, int nb) { return prec == PREC_BF16 && nb == 4; }
 
 template <int TK, int TV, int NB, int PREC>
 static hipError_t tile_launch(const AttnArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.tiles * a.n_kv_head), a.n_split);
-  attn_tile_kernel<TK, TV, NB, TILE_WAVES, TILE_CT, PREC><<<grid, 64 * TILE_WAVES, 0, st>>>(a);
+  if constexpr (tile_has_wide(PREC, NB)) {
+    if (a.tile_wide) {
+      attn_tile_kernel<TK, TV, NB, TILE_WAVES, 2, PREC><<<grid, 64 * TILE_WAVES, 0, st>>>(a);
+      return hipGetLastError();
+    }
+  }
+  attn_tile_kernel<TK, TV, NB, TILE_WAVES, 1, PREC><<<grid, 64 * TILE_WAVES, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -174,6 +174,7 @@ struct AttnArgs {
   int shared_part;         // 1: the rows of all sequences over the shared keys
   int shared_splits, shared_steps, shared_tiles;   // > 0: this launch's first splits are the shared part
   int tile_kernel;         // 1: many rows per workgroup
+  int tile_wide;           // ... and twice as many
   int eight;               // the step kernel with eight waves
   int step_rows;           // both kernels run: sequences of at most this many rows go to the step kernel
   int64_t tiles;
@@ -184,7 +185,7 @@ struct AttnArgs {
 };
 struct AttnSplit {
   int64_t tiles;
-  int n_split, split_steps;
+  int n_split, split_steps, wide;
 };
 struct AttnPlan {
   AttnSplit shared, tile, step;   // tiles 0: no such launch
