@@ -1,6 +1,7 @@
 // ft_attn.hip -- attention over the cache: which kernel takes which rows, how the keys
 // are split, and the join of the parts.
 #include <algorithm>
+#include <cmath>
 
 #include "ft_attn_kernels.h"
 
@@ -111,6 +112,24 @@ static AttnSplit split_keys(const AttnArgs& a, int64_t tiles, int64_t steps, int
   return {tiles, (int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per, 0};
 }
 
+// Time of the tile kernel with n splits of `per` steps, in steps of one CU (256 rows, 64
+// keys; 3 to 4 us at head size 128), as measured over 130 to 4000 rows and 130 to 6000
+// keys of each type.  A CU holds one workgroup, or two where the registers allow; a step
+// of two costs 1 (bf16 rows 1.2 of a wide step), one alone 0.7 of that.  A workgroup's
+// start and end take two steps, the join 1.4 and one per 20000 rows of each part.  Under
+// the causal mask the workgroups' shares of the keys run from 1 down to 2 seen - 1; whole
+// ones start longest first and fill the CUs, the first of several splits are all full.
+static double tile_cost(const AttnArgs& a, int prec, int wide, int64_t wgs, int64_t n, int64_t per, double seen) {
+  const bool two = !wide && a.dim <= (prec == ftk::PREC_F32 ? 96 : 128);
+  const double pair = prec == ftk::PREC_BF16 ? 1.2 : 1.0;
+  const double c = wgs * (double)n / 256, rounds = std::ceil(c), least = 2 * seen - 1;
+  const double load = n == 1 ? std::max(c * seen, rounds * (1 - (1 - least) * rounds / (2 * c)))
+                             : std::min(rounds, c * seen + least);
+  const double rate = two ? pair * (std::floor(rounds / 2) + (std::fmod(rounds, 2) != 0 ? 0.7 : 0.0)) / rounds : 1.0;
+  const double join = n > 1 ? 1.4 + n * (double)a.n_tok * a.n_head / 20000 : 0.0;
+  return ((double)per + 2) * std::max(load * rate, two ? 0.7 * pair : 1.0) + join;
+}
+
 AttnPlan ftk_attn_plan(const AttnArgs& a) {
   using namespace ftk;
   AttnPlan p = {};
@@ -125,19 +144,28 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
   };
   const bool many = rows > (int64_t)kStepRows * a.n_seq;   // more rows per sequence than the step kernel is for
   const int64_t part = (a.dim + 2) * sizeof(float);
-  // the tile kernel over `rows` in `seqs` sequences.  Twice the rows per workgroup where
-  // the half tile that each sequence leaves empty on average weighs little and the keys'
-  // steps are many
-  const auto tiles = [&](int64_t rows, int64_t seqs, bool shared) {
-    const auto n_tiles = [&](int64_t tile) { return shared ? (rows + tile - 1) / tile : rows / tile + seqs; };
-    const auto n_steps = [&](int64_t tile) { return shared ? (int64_t)a.n_shared / 64 + 1 : steps(tile); };
-    const int64_t two = 2 * TILE_ROWS;
-    const bool fits = shared ? 20 * n_tiles(TILE_ROWS) >= 36 * n_tiles(two) : rows >= 2 * two * seqs;
-    const bool wide = tile_has_wide(prec, a.dim / 32) && fits && n_tiles(two) * n_steps(two) * a.n_kv_head >= 2048;
-    const int64_t tile = wide ? two : TILE_ROWS;
-    AttnSplit s = split_keys(a, n_tiles(tile), n_steps(tile), 512, 8, 1);
-    s.wide = wide;
-    return s;
+  const auto tiles = [&](int64_t n_rows, int64_t seqs, bool shared) {
+    AttnSplit best = {};
+    double best_cost = 0.0;
+    for (int wide = 0; wide <= (tile_has_wide(prec, a.dim / 32) ? 1 : 0); ++wide) {
+      const int64_t tile = wide ? 2 * TILE_ROWS : TILE_ROWS;
+      const int64_t n_tiles = shared ? (n_rows + tile - 1) / tile : n_rows / tile + seqs;
+      const int64_t n_steps = shared ? (int64_t)a.n_shared / 64 + 1 : steps(tile);
+      // under the causal mask a row sees half of its sequence's new tokens on average
+      double seen = 1.0;
+      if (!shared && a.causal && !a.prefix_len)
+        seen -= 0.5 * std::min(n_rows / (64.0 * a.group * seqs), (double)n_steps) / n_steps;
+      for (int64_t n = 1, per; n <= n_steps; n = (n_steps + per - 2) / (per - 1)) {
+        per = (n_steps + n - 1) / n;
+        const double cost = tile_cost(a, prec, wide, n_tiles * a.n_kv_head, n, per, seen);
+        if (best.tiles == 0 || cost < best_cost) {
+          best = {n_tiles, (int)n, (int)per, wide};
+          best_cost = cost;
+        }
+        if (per <= 4) break;
+      }
+    }
+    return best;
   };
   if (many) p.tile = tiles(rows, a.n_seq, false);
   if (many && a.n_seq > 1 && !a.n_shared) p.step_rows = kStepRows;
