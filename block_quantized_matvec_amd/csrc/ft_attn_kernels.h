@@ -761,27 +761,41 @@ attn_tile_kernel(AttnArgs A) {
   const int cb_k = kv_code_bytes(TK, D, A.page), cb_v = kv_code_bytes(TV, D, A.page);
   const uint32_t pb_k = (uint32_t)A.n_kv_head * hb_k, pb_v = (uint32_t)A.n_kv_head * hb_v;   // under 2^30
   const uint8_t *k_head = A.k_pages + (uint32_t)hk * hb_k, *v_head = A.v_pages + (uint32_t)hk * hb_v;
-  // page ids are known a step before the loads that need them, as a load behind an id waits
-  // for every load before it; not where the registers for it would be spilled
-  constexpr bool AHEAD = !(NB == 4 && CT == 1 && PREC != PREC_F32);
+  // TIGHT, where the 128 registers of two workgroups per CU are short: the compiler must not
+  // keep over the loop what follows from the thread's number, as a spilled value's reload
+  // waits for every load in flight (64 bf16 prompts of 70 tokens over 1700 keys: 354 us
+  // against 425; fp32 at head size 96 560 against 588; no gain elsewhere).
+  // AHEAD: page ids are known a step before the loads that need them, which otherwise wait
+  // for the loads before them (fp32 378 us against 407); for fp16 at head size 128 the
+  // registers for it cost more (549 us against 531).
+  constexpr bool TIGHT = CT == 1 && ((NB == 3 && PREC == PREC_F32) || (NB == 4 && PREC == PREC_BF16));
+  constexpr bool AHEAD = !(NB == 4 && PREC == PREC_F16);
   const auto raw_page = [&](int key) { return pages[min(key >> A.page_shift, A.cols - 1)]; };
   const auto pool_page = [&](int id) { return (uint32_t)min(max(id, 0), A.n_pages - 1); };   // clamped, never followed
 
   const int slot = operand_slot(g, col);
   // this thread's part of a step: K units (group p of blocks, key j, lane group kg_) and V
   // units (row of V^T, 16 keys 16 * vg_ ..)
-  const int j = (tid >> 2) & 63, kg_ = tid & 3;
-  const int vg_ = tid & 3;
+  struct Part {
+    int tid, lane, j, kg, vg;
+  };
+  const auto my_part = [&] {
+    int x = tid;
+    if constexpr (TIGHT) asm volatile("" : "+v"(x));
+    return Part{x, x & 63, (x >> 2) & 63, x & 3, x & 3};
+  };
   uint32_t kw[KU][4];
   uint16_t ksc[PREC == PREC_BF16 ? NB : 1];
   u32x4 vw[VU], sc;
   int id_k, id_v, id_s;
   const auto fetch_ids = [&](int key0) {
-    id_k = raw_page(key0 + j);
-    id_v = raw_page(key0 + 16 * vg_);
-    id_s = raw_page(key0 + 8 * (lane & 7));
+    const Part my = my_part();
+    id_k = raw_page(key0 + my.j);
+    id_v = raw_page(key0 + 16 * my.vg);
+    id_s = raw_page(key0 + 8 * (my.lane & 7));
   };
   const auto fetch = [&](int key0) {
+    const auto [tid, lane, j, kg_, vg_] = my_part();
     const int key = key0 + j, keyv = key0 + 16 * vg_;
     if constexpr (!AHEAD) fetch_ids(key0);
     const uint8_t* kc = k_head + (uint64_t)pool_page(id_k) * pb_k;
@@ -818,6 +832,7 @@ attn_tile_kernel(AttnArgs A) {
   };
   const int end = min(w_max_len, part_hi);   // slots from here on may hold anything
   const auto commit = [&](int buf, int key0) {
+    const auto [tid, lane, j, kg_, vg_] = my_part();
     const int r = (j >> 4) * 4 + (j & 3), t = (j >> 2) & 3;   // key j's row and tile
     h16x2 df[PREC == PREC_BF16 ? NB : 1];
     if constexpr (PREC == PREC_BF16) {
