@@ -115,13 +115,13 @@ static AttnSplit split_keys(const AttnArgs& a, int64_t tiles, int64_t steps, int
 // Time of the tile kernel with n splits of `per` steps, in steps of one CU (256 rows, 64
 // keys; 3 to 4 us at head size 128), as measured over 130 to 4000 rows and 130 to 6000
 // keys of each type.  A CU holds one workgroup, or two where the registers allow; a step
-// of two costs 1 (bf16 rows 1.2 of a wide step), one alone 0.7 of that.  A workgroup's
+// of two costs 1 (bf16 rows 1.12 of a wide step), one alone 0.7 of that.  A workgroup's
 // start and end take two steps, the join 1.4 and one per 20000 rows of each part.  Under
 // the causal mask the workgroups' shares of the keys run from 1 down to 2 seen - 1; whole
 // ones start longest first and fill the CUs, the first of several splits are all full.
 static double tile_cost(const AttnArgs& a, int prec, int wide, int64_t wgs, int64_t n, int64_t per, double seen) {
   const bool two = !wide && a.dim <= (prec == ftk::PREC_F32 ? 96 : 128);
-  const double pair = prec == ftk::PREC_BF16 ? 1.2 : 1.0;
+  const double pair = prec == ftk::PREC_BF16 ? 1.12 : 1.0;
   const double c = wgs * (double)n / 256, rounds = std::ceil(c), least = 2 * seen - 1;
   const double load = n == 1 ? std::max(c * seen, rounds * (1 - (1 - least) * rounds / (2 * c)))
                              : std::min(rounds, c * seen + least);

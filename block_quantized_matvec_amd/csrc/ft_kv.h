@@ -52,20 +52,18 @@ __host__ __device__ inline int kv_k_at(int page, int j, int b, int g) {
   return page * 64 * p + j * 4 * m * CB + g * m * CB + (b - p * G) * CB;
 }
 
-// Eight codes as the cache holds them (each plus 128, or plus 8): Q8_0 in element
-// order; Q4_0 with element e in nibble e/2 + 4*(e%2), so that (w >> 4i) & 0x000F000F
-// is the pair of elements 2i, 2i+1 in the two halves of a register.
-__device__ __forceinline__ u32x2 kv_pack8(const int (&q)[8]) {
-  u32x2 w = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(q[i] + 128) << (8 * (i & 3));
-  return w;
+// Eight codes (each plus 128, or plus 8, in the low byte of a word) as the cache holds
+// them: Q8_0, and Q4_0 where a byte each is wanted, in element order; Q4_0 with element e
+// in nibble e/2 + 4*(e%2), so that (w >> 4i) & 0x000F000F is the pair of elements 2i, 2i+1
+// in the two halves of a register.
+__device__ __forceinline__ uint32_t kv_bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u), 0x05040100u);
 }
-__device__ __forceinline__ uint32_t kv_pack4(const int (&q)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w |= (uint32_t)(q[i] + 8) << (4 * ((i >> 1) + 4 * (i & 1)));
-  return w;
+__device__ __forceinline__ u32x2 kv_bytes(const uint32_t (&u)[8]) {
+  return u32x2{kv_bytes4(u[0], u[1], u[2], u[3]), kv_bytes4(u[4], u[5], u[6], u[7])};
+}
+__device__ __forceinline__ uint32_t kv_nibbles(const uint32_t (&u)[8]) {
+  return kv_bytes4(u[0], u[4], u[1], u[5]) | (kv_bytes4(u[2], u[6], u[3], u[7]) << 4);
 }
 
 // eight consecutive elements of a float tensor; vec: 16-byte aligned
@@ -103,7 +101,52 @@ __device__ __forceinline__ void kv_load8(int type, const void* base, int64_t at,
   }
 }
 
-// The same of N blocks, 32 elements apart: every load goes out before the first value
+// The same N times as loaded (two words of 16 bytes for fp32, one else), all loads in
+// flight together; and the values of one.
+template <int N>
+__device__ __forceinline__ void kv_load_raw(int type, const void* base, const int64_t (&at)[N], bool vec,
+                                            uint32_t __attribute__((ext_vector_type(4))) (&r)[N][2]) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  if (type == FT_F32) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t* p = (const uint32_t*)base + at[n];
+      if (vec) {
+        r[n][0] = ((const u4*)p)[0];
+        r[n][1] = ((const u4*)p)[1];
+      } else {
+        r[n][0] = u4{p[0], p[1], p[2], p[3]};
+        r[n][1] = u4{p[4], p[5], p[6], p[7]};
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint16_t* p = (const uint16_t*)base + at[n];
+    if (vec) r[n][0] = *(const u4*)p;
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[n][0][i] = p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+  }
+}
+__device__ __forceinline__ void kv_raw_values(int type, const uint32_t __attribute__((ext_vector_type(4))) (&r)[2], float (&v)[8]) {
+  if (type == FT_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i >> 2][i & 3]);
+  } else if (type == FT_BF16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? r[0][i >> 1] & 0xFFFF0000u : r[0][i >> 1] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = r[0][i >> 1];
+      v[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? w >> 16 : w));
+    }
+  }
+}
+
+// Of N blocks, 32 elements apart: every load goes out before the first value
 // is converted.
 template <int N>
 __device__ __forceinline__ void kv_load_row(int type, const void* base, int64_t at, bool vec, float (&v)[N][8]) {
@@ -147,14 +190,11 @@ __device__ __forceinline__ void kv_load_row(int type, const void* base, int64_t 
   }
 }
 
-// round to nearest even; a NaN keeps its top bits and stays a NaN
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-__device__ __forceinline__ uint32_t float_bits16(int type, float f) {
-  return type == FT_BF16 ? bf16_bits(f) : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f);
+// two values as bf16 or fp16, to nearest even
+__device__ __forceinline__ uint32_t float_bits16x2(int type, float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  if (type == FT_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, h16x2));
 }
 template <int N>   // N consecutive elements (4 or 8)
 __device__ __forceinline__ void kv_store_n(int type, void* base, int64_t at, bool vec, const float (&v)[N]) {
@@ -172,7 +212,7 @@ __device__ __forceinline__ void kv_store_n(int type, void* base, int64_t at, boo
   uint16_t* p = (uint16_t*)base + at;
   uint32_t w[N / 2];
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) w[i] = float_bits16(type, v[2 * i]) | (float_bits16(type, v[2 * i + 1]) << 16);
+  for (int i = 0; i < N / 2; ++i) w[i] = float_bits16x2(type, v[2 * i], v[2 * i + 1]);
   if (vec) {
 #pragma unroll
     for (int i = 0; i < N / 2; i += 2) *(u32x2*)(p + 2 * i) = u32x2{w[i], w[i + 1]};

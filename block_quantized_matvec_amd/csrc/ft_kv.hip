@@ -8,14 +8,21 @@
 //         q = clamp(round_half_away(x / d), -8, 7)
 // (d limited to the largest finite fp16; a zero d gives zero codes.)
 //
-// Both are bound by HBM at thousands of tokens and by latency at a decode step.  A
-// workgroup takes 64 consecutive tokens of one head and of K or V; four lanes hold a
-// block, eight elements each, so amax (or m) meets in two DPP steps.  K codes go
-// straight to the page, eight at a time.  V is held transposed (a row per element,
-// the page's keys side by side: the operand order of the attention's second
-// product), so its codes meet in LDS and leave as 16-byte rows wherever 16
-// consecutive tokens fill 16 consecutive slots from a multiple of 16 on; other
-// tokens' codes are single bytes.
+// A workgroup takes 64 consecutive tokens of one head and of K or V; four lanes hold a
+// block, eight elements each, so amax (or m) meets in two DPP steps, and a wave takes four
+// tokens of each of its blocks.  K codes go straight to the page, eight at a time.  V is
+// held transposed (a row per element, the page's keys side by side: the operand order of
+// the attention's second product): the codes of four tokens change places between lanes,
+// so that words of four keys meet in LDS, and leave as 16-byte rows wherever 16
+// consecutive tokens fill 16 consecutive slots from a multiple of 16 on; other tokens'
+// codes are single bytes.
+//
+// At a decode step both are launch and latency (4 us each).  8192 bf16 tokens of 8 heads
+// of 128, K in Q8_0 and V in Q4_0 (33 MB of rows, 14 MB of cache): reading back 9.3 us,
+// at the rate of a copy; writing 15 us, bound by vector instructions, 170 per eight
+// elements and wave (208, and 18 us, while every value near a half-integer divided; byte
+// writes to LDS in place of the exchange between lanes: 17.6 and 12.6 us).  fp32 rows, twice
+// the bytes: 36 us together, 4.5 TB/s.
 #include "ft_device.h"
 #include "ft_internal.h"
 #include "ft_kv.h"
@@ -25,32 +32,50 @@ namespace ftk {
 constexpr int KV_TILE = 64;    // tokens per workgroup
 constexpr int KV_PITCH = 68;   // bytes between the rows of the transposed tile in LDS (a bank further per row)
 
-// The codes of N values of one block.  t = v * rcp(d) is within 1.5 * 2^-16 of v / d
-// while |v / d| < 128, so it rounds to the code unless it lies within 2^-14 of a
-// half-integer; there, and for a scale outside 2^+-100, the lane divides.
-template <int LOW, int HIGH, int N>
-__device__ __forceinline__ void kv_codes(const float (&v)[N], float d, int (&q)[N]) {
-  const float r = __builtin_amdgcn_rcpf(d), ad = fabsf(d);
-  bool slow = !(ad >= 0x1p-100f && ad <= 0x1p100f);
+// The codes of eight values of one block, each plus HIGH + 1, in the low bytes of u.  top:
+// the block's largest magnitude; d is an fp16 number.  The sum of v * rcp(d) and 3 * 2^22 +
+// HIGH + 1 leaves the rounded quotient in its last bits; v * rcp(d) is within 1.5 * 2^-16 of
+// v / d while that is below 128, so the rounding is the code's unless it lies within 2^-14
+// of a half-integer (bf16 values often lie on one).  There a code n is held against
+// (|n| -+ 1/2) |d|, which are exact.  Past the range of codes (a scale that fp16 holds
+// with few bits or not at all) the lane divides.
+template <int LOW, int HIGH>
+__device__ __forceinline__ void kv_codes(const float (&v)[8], float d, float top, uint32_t (&u)[8]) {
+  constexpr float MAGIC = 12582912.0f + HIGH + 1;
+  const float r = __builtin_amdgcn_rcpf(d);
+  float off = 0.0f;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float t = v[j] * r;
-    slow |= fabsf(__builtin_amdgcn_fractf(t) - 0.5f) <= 0x1p-14f;
-    q[j] = (int)__builtin_rintf(fminf(fmaxf(t, (float)LOW), (float)HIGH));
+  for (int j = 0; j < 8; ++j) {
+    // Q4_0: the last code stands for everything above it
+    const float t = LOW == -8 ? fminf(v[j] * r, (float)HIGH) : v[j];
+    const float c = LOW == -8 ? t + MAGIC : fmaf(t, r, MAGIC);
+    const float e = LOW == -8 ? t - (c - MAGIC) : fmaf(t, r, MAGIC - c);
+    off = fmaxf(off, fabsf(e));
+    u[j] = __float_as_uint(c);
   }
-  if (slow) {
+  if (!(top * fabsf(r) < 0.4f - LOW)) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const float t = roundf(v[j] / (d == 0.0f ? 1.0f : d));
-      q[j] = d == 0.0f ? 0 : (int)fminf(fmaxf(t, (float)LOW), (float)HIGH);
+      u[j] = (uint32_t)((d == 0.0f ? 0 : (int)fminf(fmaxf(t, (float)LOW), (float)HIGH)) + HIGH + 1);
+    }
+  } else if (off >= 0.5f - 0x1p-14f) {
+    const float ad = fabsf(d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float n = fabsf(__uint_as_float(u[j]) - MAGIC);
+      const float x = fabsf(v[j]), up = fmaf(n, ad, 0.5f * ad), down = fmaf(n, ad, -0.5f * ad);
+      n += x >= up ? 1.0f : x < down ? -1.0f : 0.0f;
+      n = __uint_as_float(__float_as_uint(n) | ((__float_as_uint(v[j]) ^ __float_as_uint(d)) & 0x80000000u));
+      u[j] = __float_as_uint(fminf(n, (float)HIGH) + MAGIC);
     }
   }
 }
 
-// One block's scale (fp16 bits) and this lane's eight codes; its four lanes call it
+// One block's scale (fp16 bits) and this lane's eight codes as kv_codes leaves them; its four lanes call it
 // together, lane l4 with elements 8*l4 .. 8*l4+7.
 template <int T>
-__device__ __forceinline__ uint32_t kv_quantize(const float (&v)[8], int l4, int (&q)[8]) {
+__device__ __forceinline__ uint32_t kv_quantize(const float (&v)[8], int l4, uint32_t (&u)[8]) {
   float d;
   uint32_t dh;
   if constexpr (T == FT_Q8_0) {
@@ -59,9 +84,11 @@ __device__ __forceinline__ uint32_t kv_quantize(const float (&v)[8], int l4, int
     for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
     a = fmaxf(a, xchg<1>(a));
     a = fmaxf(a, xchg<2>(a));
-    dh = f2h_bits(fminf(a / 127.0f, 65504.0f));
+    // a / 127, correctly rounded: a product with the rounded reciprocal, and its remainder
+    const float q = a * (1.0f / 127.0f), q1 = fmaf(fmaf(-127.0f, q, a), 1.0f / 127.0f, q);
+    dh = f2h_bits(fminf(q1, 65504.0f));
     d = h2f(dh);
-    kv_codes<-127, 127, 8>(v, d, q);
+    kv_codes<-127, 127>(v, d, a, u);
   } else {
     float m = v[0];
 #pragma unroll
@@ -73,21 +100,30 @@ __device__ __forceinline__ uint32_t kv_quantize(const float (&v)[8], int l4, int
     m = (l4 & 2) ? (fabsf(o2) >= fabsf(m) ? o2 : m) : (fabsf(o2) > fabsf(m) ? o2 : m);
     dh = f2h_bits(fminf(fmaxf(m * -0.125f, -65504.0f), 65504.0f));
     d = h2f(dh);
-    kv_codes<-8, 7, 8>(v, d, q);
+    kv_codes<-8, 7>(v, d, fabsf(m), u);
   }
   return d == 0.0f ? 0u : dh;
 }
 
-// The tile's slots, and which of its tokens start a run that fills 16 slots from a
-// multiple of 16 on.  Every wave computes the same masks; s_slot[j] < 0: token j is
-// not in the cache (padding, or out of range).
-__device__ __forceinline__ uint64_t kv_runs(const int64_t* slots, int64_t t0, int64_t t, int64_t n_slot, int64_t* s_slot,
-                                            uint64_t& valid) {
+// this lane's token's slot
+__device__ __forceinline__ int64_t kv_slot(const int64_t* slots, int64_t t0, int64_t t) {
   const int lane = threadIdx.x & 63;
-  int64_t s = -1;
-  if (t0 + lane < t) s = slots[t0 + lane];
-  if (s >= n_slot) s = -1;
-  if (threadIdx.x < 64) s_slot[lane] = s;
+  return t0 + lane < t ? slots[t0 + lane] : -1;
+}
+struct KvTokens {
+  int64_t at[KV_TILE];   // byte of the page head in the pool
+  int key[KV_TILE];      // the key in its page; -1: not in the cache (padding, or out of range)
+};
+// The tile's slots, and which of its tokens start a run that fills 16 slots from a
+// multiple of 16 on.  Every wave computes the same masks.
+template <class IO>
+__device__ __forceinline__ uint64_t kv_runs(const IO& io, int64_t s, int head_bytes, int head, KvTokens& tk, uint64_t& valid) {
+  const int lane = threadIdx.x & 63;
+  if (s >= io.n_slot) s = -1;
+  if (threadIdx.x < 64) {
+    tk.at[lane] = (s >> io.page_shift) * ((int64_t)io.heads * head_bytes) + (int64_t)head * head_bytes;
+    tk.key[lane] = s < 0 ? -1 : (int)(s & (io.page - 1));
+  }
   const int64_t before = __shfl_up(s, 1, 64);
   valid = __ballot(s >= 0);
   const uint64_t next = __ballot(lane > 0 && s >= 0 && s == before + 1);   // continues the token before it
@@ -112,6 +148,43 @@ __device__ __forceinline__ uint64_t cover16(uint64_t m) {   // bits j .. j+15 of
   return m | (m << 8);
 }
 
+// A unit is one block of four tokens, in 16 lanes: lane 16r + 4u + l4 of a wave holds
+// elements 8 l4 .. 8 l4 + 7 of its token r, u one of the wave's four units.  A workgroup
+// takes 16 units at a time, NB times; unit n is block n % NB of tokens 4 (n / NB) ..
+struct KvUnit {
+  int tok, b, l4;
+};
+template <int NB>
+__device__ __forceinline__ KvUnit kv_unit(int it) {
+  const int lane = threadIdx.x & 63, n = it * 16 + (threadIdx.x >> 6) * 4 + ((lane >> 2) & 3);
+  const int quad = n / NB;
+  return {4 * quad + (lane >> 4), n - quad * NB, lane & 3};
+}
+template <int NB>   // the first token of the wave's first unit
+__device__ __forceinline__ int kv_unit_first(int it) {
+  return 4 * ((it * 16 + wave_id() * 4) / NB);
+}
+
+// Eight bytes of a token per lane (a: 0..3, b: 4..7) <-> two bytes of four tokens: lane
+// 16r + .. gets bytes 2r and 2r + 1 of tokens 0, 1, 2, 3.
+__device__ __forceinline__ u32x2 kv_to_rows(u32x2 w) {
+  const auto h = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);   // of tokens r & 1 and (r & 1) + 2
+  const uint32_t lo = __builtin_amdgcn_perm(h[1], h[0], 0x05010400u), hi = __builtin_amdgcn_perm(h[1], h[0], 0x07030602u);
+  const auto q = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+  return u32x2{__builtin_amdgcn_perm(q[1], q[0], 0x05010400u), __builtin_amdgcn_perm(q[1], q[0], 0x07030602u)};
+}
+__device__ __forceinline__ u32x2 kv_from_rows(u32x2 w) {
+  const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], 0x06040200u), hi = __builtin_amdgcn_perm(w[1], w[0], 0x07050301u);
+  const auto q = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+  const uint32_t a = __builtin_amdgcn_perm(q[1], q[0], 0x06040200u), b = __builtin_amdgcn_perm(q[1], q[0], 0x07050301u);
+  const auto h = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return u32x2{h[0], h[1]};
+}
+
+// Rounds of units whose loads go out together (four at head size 128: 1.5 us slower, for
+// the registers).
+template <int NB> constexpr int KV_AHEAD = NB % 2 ? 1 : 2;
+
 struct KvIo {
   uint8_t* pages;
   int64_t n_slot;              // n_pages * page
@@ -123,53 +196,70 @@ struct KvIo {
 
 template <int T, int NB, bool V>
 __device__ __forceinline__ void kv_store_side(const KvIo& io, int ftype, const int64_t* slots, int64_t t, int64_t t0,
-                                              int head, int64_t* s_slot, uint8_t* s_tile) {
+                                              int head, KvTokens& tk, uint8_t* s_tile) {
   constexpr int D = NB * 32;
   constexpr int ROWS = T == FT_Q8_0 ? D : D / 2;   // rows of the transposed tile
-  const int tid = threadIdx.x, l4 = tid & 3;
-  uint64_t valid;
-  const uint64_t runs = kv_runs(slots, t0, t, io.n_slot, s_slot, valid);
-  __syncthreads();
+  constexpr int N = KV_AHEAD<NB>;
+  const int tid = threadIdx.x;
   const int nt = (int)min((int64_t)KV_TILE, t - t0);
   const int hb = kv_head_bytes(T, D, io.page), cb = kv_code_bytes(T, D, io.page);
-  const int64_t page_bytes = (int64_t)io.heads * hb;
-  for (int i = tid >> 2; i < nt * NB; i += 64) {
-    const int tok = i / NB, b = i - tok * NB;
-    const int64_t slot = s_slot[tok];
-    if (slot < 0) continue;   // the block's four lanes together
-    float v[8];
-    kv_load8(ftype, io.x, (t0 + tok) * io.x_token + head * io.x_head + 32 * b + 8 * l4, io.vec, v);
-    int q[8];
-    const uint32_t dh = kv_quantize<T>(v, l4, q);
-    const int j = (int)(slot & (io.page - 1));
-    uint8_t* ph = io.pages + (slot >> io.page_shift) * page_bytes + (int64_t)head * hb;
-    if (l4 == 0) *(uint16_t*)(ph + cb + 2 * (b * io.page + j)) = (uint16_t)dh;
-    if constexpr (!V) {
-      uint8_t* o = ph + kv_k_at<T, NB>(io.page, j, b, l4);
-      if constexpr (T == FT_Q8_0) *(u32x2*)o = kv_pack8(q);
-      else *(uint32_t*)o = kv_pack4(q);
-    } else if constexpr (T == FT_Q8_0) {
+  const int64_t my_slot = kv_slot(slots, t0, t);
+  uint64_t valid, runs = 0;
+  for (int it0 = 0; it0 < NB; it0 += N) {
+    // the rows' loads wait for nothing (those behind the last token: its own once more)
+    u32x4 raw[N][2];
+    int64_t at[N];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s_tile[(32 * b + 8 * l4 + e) * KV_PITCH + tok] = (uint8_t)(q[e] + 128);
-    } else {   // lanes 0, 1 hold elements 0..15, whose partners in lanes 2, 3 share their bytes
-      int hi[8];
+    for (int n = 0; n < N; ++n) {
+      const KvUnit u = kv_unit<NB>(it0 + n);
+      at[n] = min(t0 + u.tok, t - 1) * io.x_token + head * io.x_head + 32 * u.b + 8 * u.l4;
+    }
+    kv_load_raw<N>(ftype, io.x, at, io.vec, raw);
+    if (it0 == 0) {
+      runs = kv_runs(io, my_slot, hb, head, tk, valid);
+      __syncthreads();
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) hi[e] = __float_as_int(xchg<2>(__int_as_float(q[e] + 8)));
-      if (l4 < 2) {
+    for (int n = 0; n < N; ++n) {
+      if (kv_unit_first<NB>(it0 + n) >= nt) break;   // the wave's units are all behind the last token
+      const KvUnit u = kv_unit<NB>(it0 + n);
+      float v[8];
+      kv_raw_values(ftype, raw[n], v);
+      uint32_t q[8];
+      const uint32_t dh = kv_quantize<T>(v, u.l4, q);
+      const int j = tk.key[u.tok];
+      uint8_t* ph = io.pages + tk.at[u.tok];   // not followed where j < 0
+      if (j >= 0 && u.l4 == 0) *(uint16_t*)(ph + cb + 2 * (u.b * io.page + j)) = (uint16_t)dh;
+      if constexpr (!V) {
+        if (j >= 0) {
+          uint8_t* o = ph + kv_k_at<T, NB>(io.page, j, u.b, u.l4);
+          if constexpr (T == FT_Q8_0) *(u32x2*)o = kv_bytes(q);
+          else *(uint32_t*)o = kv_nibbles(q);
+        }
+      } else {
+        u32x2 w = kv_bytes(q);
+        int row = 32 * u.b + 8 * u.l4;
+        if constexpr (T == FT_Q4_0) {   // elements 0..15, in lanes 0, 1, share their bytes with 16..31, in lanes 2, 3
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          s_tile[(16 * b + 8 * l4 + e) * KV_PITCH + tok] = (uint8_t)((q[e] + 8) | (hi[e] << 4));
+          for (int i = 0; i < 2; ++i) w[i] |= __float_as_uint(xchg<2>(__uint_as_float(w[i]))) << 4;
+          row = 16 * u.b + 8 * (u.l4 & 1);
+        }
+        w = kv_to_rows(w);
+        const int r = row + 2 * (u.tok & 3);
+        if (T == FT_Q8_0 || u.l4 < 2) {
+          *(uint32_t*)(s_tile + r * KV_PITCH + (u.tok & ~3)) = w[0];
+          *(uint32_t*)(s_tile + (r + 1) * KV_PITCH + (u.tok & ~3)) = w[1];
+        }
       }
     }
   }
   if constexpr (V) {
     __syncthreads();
     const int n_run = __popcll(runs);
-    for (int i = tid; i < n_run * ROWS; i += 256) {
-      const int c = i / ROWS, r = i - c * ROWS;
+    for (int i = tid; i < n_run * ROWS; i += 256) {   // a row's runs side by side: often one piece of a page
+      const int r = i / n_run, c = i - r * n_run;
       const int tok = nth_bit(runs, c);
-      const int64_t slot = s_slot[tok];
-      uint8_t* ph = io.pages + (slot >> io.page_shift) * page_bytes + (int64_t)head * hb;
+      uint8_t* ph = io.pages + tk.at[tok];
       u32x4 w;
       const uint8_t* src = s_tile + r * KV_PITCH + tok;
       if ((tok & 3) == 0) {
@@ -180,16 +270,15 @@ __device__ __forceinline__ void kv_store_side(const KvIo& io, int ftype, const i
         for (int k = 0; k < 4; ++k)
           w[k] = src[4 * k] | (src[4 * k + 1] << 8) | (src[4 * k + 2] << 16) | ((uint32_t)src[4 * k + 3] << 24);
       }
-      *(u32x4*)(ph + r * io.page + (int)(slot & (io.page - 1))) = w;
+      *(u32x4*)(ph + r * io.page + tk.key[tok]) = w;
     }
     const uint64_t rest = valid & ~cover16(runs);
     const int n_rest = __popcll(rest);
     for (int i = tid; i < n_rest * ROWS; i += 256) {
       const int c = i / ROWS, r = i - c * ROWS;
       const int tok = nth_bit(rest, c);
-      const int64_t slot = s_slot[tok];
-      uint8_t* ph = io.pages + (slot >> io.page_shift) * page_bytes + (int64_t)head * hb;
-      ph[r * io.page + (int)(slot & (io.page - 1))] = s_tile[r * KV_PITCH + tok];
+      uint8_t* ph = io.pages + tk.at[tok];
+      ph[r * io.page + tk.key[tok]] = s_tile[r * KV_PITCH + tok];
     }
   }
 }
@@ -198,33 +287,32 @@ __device__ __forceinline__ void kv_store_side(const KvIo& io, int ftype, const i
 template <int TK, int TV, int NB>
 __global__ void __launch_bounds__(256)
 kv_store_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int64_t t) {
-  __shared__ int64_t s_slot[KV_TILE];
+  __shared__ KvTokens s_tok;
   __shared__ __align__(16) uint8_t s_tile[NB * 32 * KV_PITCH];
   const int64_t t0 = (int64_t)blockIdx.x * KV_TILE;
-  if (blockIdx.z == 0) kv_store_side<TK, NB, false>(k, ftype, slots, t, t0, blockIdx.y, s_slot, s_tile);
-  else kv_store_side<TV, NB, true>(v, ftype, slots, t, t0, blockIdx.y, s_slot, s_tile);
+  if (blockIdx.z == 0) kv_store_side<TK, NB, false>(k, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
+  else kv_store_side<TV, NB, true>(v, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
 }
 
 template <int T, int NB, bool V>
 __device__ __forceinline__ void kv_load_side(const KvIo& io, int ftype, const int64_t* slots, int64_t t, int64_t t0,
-                                             int head, int64_t* s_slot, uint8_t* s_tile) {
+                                             int head, KvTokens& tk, uint8_t* s_tile) {
   constexpr int D = NB * 32;
   constexpr int ROWS = T == FT_Q8_0 ? D : D / 2;
-  const int tid = threadIdx.x, l4 = tid & 3;
+  constexpr int N = KV_AHEAD<NB>;
+  const int tid = threadIdx.x;
   uint64_t valid;
-  const uint64_t runs = kv_runs(slots, t0, t, io.n_slot, s_slot, valid);
+  const int hb = kv_head_bytes(T, D, io.page), cb = kv_code_bytes(T, D, io.page);
+  const uint64_t runs = kv_runs(io, kv_slot(slots, t0, t), hb, head, tk, valid);
   __syncthreads();
   const int nt = (int)min((int64_t)KV_TILE, t - t0);
-  const int hb = kv_head_bytes(T, D, io.page), cb = kv_code_bytes(T, D, io.page);
-  const int64_t page_bytes = (int64_t)io.heads * hb;
   if constexpr (V) {   // the codes into the transposed tile first
     const int n_run = __popcll(runs);
-    for (int i = tid; i < n_run * ROWS; i += 256) {
-      const int c = i / ROWS, r = i - c * ROWS;
+    for (int i = tid; i < n_run * ROWS; i += 256) {   // a row's runs side by side: often one piece of a page
+      const int r = i / n_run, c = i - r * n_run;
       const int tok = nth_bit(runs, c);
-      const int64_t slot = s_slot[tok];
-      const uint8_t* ph = io.pages + (slot >> io.page_shift) * page_bytes + (int64_t)head * hb;
-      const u32x4 w = *(const u32x4*)(ph + r * io.page + (int)(slot & (io.page - 1)));
+      const uint8_t* ph = io.pages + tk.at[tok];
+      const u32x4 w = *(const u32x4*)(ph + r * io.page + tk.key[tok]);
       uint8_t* dst = s_tile + r * KV_PITCH + tok;
       if ((tok & 3) == 0) {
 #pragma unroll
@@ -239,54 +327,65 @@ __device__ __forceinline__ void kv_load_side(const KvIo& io, int ftype, const in
     for (int i = tid; i < n_rest * ROWS; i += 256) {
       const int c = i / ROWS, r = i - c * ROWS;
       const int tok = nth_bit(rest, c);
-      const int64_t slot = s_slot[tok];
-      const uint8_t* ph = io.pages + (slot >> io.page_shift) * page_bytes + (int64_t)head * hb;
-      s_tile[r * KV_PITCH + tok] = ph[r * io.page + (int)(slot & (io.page - 1))];
+      const uint8_t* ph = io.pages + tk.at[tok];
+      s_tile[r * KV_PITCH + tok] = ph[r * io.page + tk.key[tok]];
     }
     __syncthreads();
   }
-  for (int i = tid >> 2; i < nt * NB; i += 64) {
-    const int tok = i / NB, b = i - tok * NB;
-    const int64_t slot = s_slot[tok];
-    float x[8];
-    if (slot < 0) {
+  for (int it0 = 0; it0 < NB; it0 += N) {
+    uint32_t d[N];
+    u32x2 w[N];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-    } else {
-      const int j = (int)(slot & (io.page - 1));
-      const uint8_t* ph = io.pages + (slot >> io.page_shift) * page_bytes + (int64_t)head * hb;
-      const float d = h2f(*(const uint16_t*)(ph + cb + 2 * (b * io.page + j)));
-      int q[8];
-      if constexpr (V) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if constexpr (T == FT_Q8_0) q[e] = (int)s_tile[(32 * b + 8 * l4 + e) * KV_PITCH + tok] - 128;
-          else q[e] = (int)((s_tile[(16 * b + 8 * (l4 & 1) + e) * KV_PITCH + tok] >> (l4 & 2 ? 4 : 0)) & 15u) - 8;
+    for (int n = 0; n < N; ++n) {
+      const KvUnit u = kv_unit<NB>(it0 + n);
+      const int j = tk.key[u.tok];
+      d[n] = 0;
+      w[n] = u32x2{0u, 0u};
+      if (j >= 0) {
+        const uint8_t* ph = io.pages + tk.at[u.tok];
+        d[n] = *(const uint16_t*)(ph + cb + 2 * (u.b * io.page + j));
+        if constexpr (!V) {
+          if constexpr (T == FT_Q8_0) w[n] = *(const u32x2*)(ph + kv_k_at<T, NB>(io.page, j, u.b, u.l4));
+          else w[n][0] = *(const uint32_t*)(ph + kv_k_at<T, NB>(io.page, j, u.b, u.l4));
         }
-      } else if constexpr (T == FT_Q8_0) {
-        const u32x2 w = *(const u32x2*)(ph + kv_k_at<T, NB>(io.page, j, b, l4));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = (int)((w[e >> 2] >> (8 * (e & 3))) & 255u) - 128;
-      } else {
-        const uint32_t w = *(const uint32_t*)(ph + kv_k_at<T, NB>(io.page, j, b, l4));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = (int)((w >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15u) - 8;
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = d * (float)q[e];   // exact in fp32
     }
-    kv_store_n<8>(ftype, io.x, (t0 + tok) * io.x_token + head * io.x_head + 32 * b + 8 * l4, io.vec, x);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (kv_unit_first<NB>(it0 + n) >= nt) break;
+      const KvUnit u = kv_unit<NB>(it0 + n);
+      if constexpr (V) {
+        const int r = (T == FT_Q8_0 ? 32 * u.b + 8 * u.l4 : 16 * u.b + 8 * (u.l4 & 1)) + 2 * (u.tok & 3);
+        w[n] = kv_from_rows(u32x2{*(const uint32_t*)(s_tile + r * KV_PITCH + (u.tok & ~3)),
+                                  *(const uint32_t*)(s_tile + (r + 1) * KV_PITCH + (u.tok & ~3))});
+      }
+      if constexpr (T == FT_Q4_0) {   // a byte per code
+        if constexpr (V) {
+          w[n] = (w[n] >> (u.l4 & 2 ? 4 : 0)) & 0x0F0F0F0Fu;
+        } else {
+          const uint32_t even = w[n][0] & 0x0F0F0F0Fu, odd = (w[n][0] >> 4) & 0x0F0F0F0Fu;   // elements 0 4 1 5, 2 6 3 7
+          w[n] = u32x2{__builtin_amdgcn_perm(odd, even, 0x06040200u), __builtin_amdgcn_perm(odd, even, 0x07050301u)};
+        }
+      }
+      // d * (code - 128), exact in fp32; a token that is not there has d = 0
+      const float df = h2f(d[n]), less = df * (T == FT_Q8_0 ? -128.0f : -8.0f);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(df, (float)((w[n][e >> 2] >> (8 * (e & 3))) & 255u), less);
+      if (u.tok < nt)
+        kv_store_n<8>(ftype, io.x, (t0 + u.tok) * io.x_token + head * io.x_head + 32 * u.b + 8 * u.l4, io.vec, x);
+    }
   }
 }
 
 template <int TK, int TV, int NB>
 __global__ void __launch_bounds__(256)
 kv_load_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int64_t t, int first) {
-  __shared__ int64_t s_slot[KV_TILE];
+  __shared__ KvTokens s_tok;
   __shared__ __align__(16) uint8_t s_tile[NB * 32 * KV_PITCH];
   const int64_t t0 = (int64_t)blockIdx.x * KV_TILE;
-  if (blockIdx.z + first == 0) kv_load_side<TK, NB, false>(k, ftype, slots, t, t0, blockIdx.y, s_slot, s_tile);
-  else kv_load_side<TV, NB, true>(v, ftype, slots, t, t0, blockIdx.y, s_slot, s_tile);
+  if (blockIdx.z + first == 0) kv_load_side<TK, NB, false>(k, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
+  else kv_load_side<TV, NB, true>(v, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
 }
 
 static KvIo kv_io(const KvArgs& a, bool v) {
