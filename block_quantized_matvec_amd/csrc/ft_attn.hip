@@ -125,7 +125,7 @@ static double tile_cost(const AttnArgs& a, int prec, int wide, int64_t wgs, int6
   const double c = wgs * (double)n / 256, rounds = std::ceil(c), least = 2 * seen - 1;
   const double load = n == 1 ? std::max(c * seen, rounds * (1 - (1 - least) * rounds / (2 * c)))
                              : std::min(rounds, c * seen + least);
-  const double rate = two ? pair * (std::floor(rounds / 2) + (std::fmod(rounds, 2) != 0 ? 0.7 : 0.0)) / rounds : 1.0;
+  const double rate = two ? pair * (0.5 + (std::fmod(rounds, 2) != 0 ? 0.2 * least / rounds : 0.0)) : 1.0;
   const double join = n > 1 ? 1.4 + n * (double)a.n_tok * a.n_head / 20000 : 0.0;
   return ((double)per + 2) * std::max(load * rate, two ? 0.7 * pair : 1.0) + join;
 }
