@@ -150,6 +150,7 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
     for (int wide = 0; wide <= (tile_has_wide(prec, a.dim / 32) ? 1 : 0); ++wide) {
       const int64_t tile = wide ? 2 * TILE_ROWS : TILE_ROWS;
       const int64_t n_tiles = shared ? (n_rows + tile - 1) / tile : n_rows / tile + seqs;
+      const int64_t filled = seqs == 1 ? (n_rows + tile - 1) / tile : n_rows / tile + seqs / 2;   // about
       const int64_t n_steps = shared ? (int64_t)a.n_shared / 64 + 1 : steps(tile);
       // under the causal mask a row sees half of its sequence's new tokens on average
       double seen = 1.0;
@@ -157,7 +158,7 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
         seen -= 0.5 * std::min(n_rows / (64.0 * a.group * seqs), (double)n_steps) / n_steps;
       for (int64_t n = 1, per; n <= n_steps; n = (n_steps + per - 2) / (per - 1)) {
         per = (n_steps + n - 1) / n;
-        const double cost = tile_cost(a, prec, wide, n_tiles * a.n_kv_head, n, per, seen);
+        const double cost = tile_cost(a, prec, wide, filled * a.n_kv_head, n, per, seen);
         if (best.tiles == 0 || cost < best_cost) {
           best = {n_tiles, (int)n, (int)per, wide};
           best_cost = cost;

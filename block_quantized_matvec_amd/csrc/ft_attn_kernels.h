@@ -907,23 +907,44 @@ attn_tile_kernel(AttnArgs A) {
     }
   };
 
-  if (s0 < s_end) {
-    const int key0 = steps.block(s0) * ATTN_STEP;
-    if constexpr (AHEAD) fetch_ids(key0);
-    fetch(key0);
-    if constexpr (AHEAD) fetch_ids(steps.block(min(s0 + 1, s_end - 1)) * ATTN_STEP);
-    commit(0, key0);
+  // A step's keys are fetched during the step before it and laid out at its end, between two
+  // barriers.  With two row operands per wave (STAGGER) half of the waves, which share the
+  // SIMDs with the other half, lay out a step earlier, before their products in place of
+  // after them, so that one half's matrix instructions run beside the other's vector
+  // instructions (4096 rows over 16384 keys: 1379 us against 1445; with one operand there
+  // are two workgroups per CU out of step already: fp32 chunk 376 us against 360).
+  constexpr bool STAGGER = CT == 2;
+  const bool late = STAGGER && wave >= NW / 2;
+  const auto get = [&](int i) {
+    if (i >= s_end) return;
+    fetch(steps.block(i) * ATTN_STEP);
+    if constexpr (AHEAD) fetch_ids(steps.block(min(i + 1, s_end - 1)) * ATTN_STEP);
+  };
+  const auto lay_out = [&](int i) {
+    if (i < s_end) commit((i - s0) & 1, steps.block(i) * ATTN_STEP);
+  };
+  if constexpr (AHEAD) {
+    if (s0 < s_end) fetch_ids(steps.block(s0) * ATTN_STEP);
+  }
+  get(s0);
+  lay_out(s0);
+  if constexpr (STAGGER) {
+    get(s0 + 1);
+    lds_barrier();
+    if (late) {
+      lay_out(s0 + 1);
+      get(s0 + 2);
+    }
   }
   for (int i = s0; i < s_end; ++i) {
     const int buf = (i - s0) & 1;
     const int key0 = steps.block(i) * ATTN_STEP;
-    int key1 = 0;
-    lds_barrier();
-    if (i + 1 < s_end) {
-      key1 = steps.block(i + 1) * ATTN_STEP;
-      fetch(key1);
-      if constexpr (AHEAD) fetch_ids(steps.block(min(i + 2, s_end - 1)) * ATTN_STEP);
+    if constexpr (!STAGGER) {
+      lds_barrier();
+      get(i + 1);
     }
+    // the products first where waves compete (fp32 chunk: 351 us against 360)
+    if constexpr (LO) __builtin_amdgcn_s_setprio(1);
     const int last = key0 + ATTN_STEP - 1;
     {
       const bool all = key0 >= part_lo && last < min(min_len, part_hi) &&
@@ -961,6 +982,7 @@ attn_tile_kernel(AttnArgs A) {
         }
         if constexpr (PREC != PREC_BF16) __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (LO) __builtin_amdgcn_s_setprio(0);
       const int ev = min((int)(L.vmax[buf] >> 10), 30);
       const float lift = (float)(29 - ev);
       if constexpr (PREC == PREC_BF16) {
@@ -1070,7 +1092,14 @@ attn_tile_kernel(AttnArgs A) {
         if constexpr (PREC != PREC_BF16) __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (i + 1 < s_end) commit(buf ^ 1, key1);
+    if constexpr (STAGGER) {
+      if (late) lds_barrier();
+      lay_out(i + 1 + (late ? 1 : 0));
+      get(i + 2 + (late ? 1 : 0));
+      if (!late) lds_barrier();
+    } else {
+      lay_out(i + 1);
+    }
   }
 
 #pragma unroll
