@@ -327,7 +327,7 @@ ft_status ft_moe_route_ex(const void* logits, ft_float type, int64_t t, int64_t 
   ft_route_opts o = {};
   if (opts) o = *opts;
   if (!is_float(type)) return FT_ERR_UNSUPPORTED;
-  if (t < 0 || n_expert < 1 || n_expert > 1024 || t > ((int64_t)1 << 32)) return FT_ERR_SHAPE;
+  if (t < 0 || n_expert < 1 || n_expert > 1024 || t > (1 << 25)) return FT_ERR_SHAPE;
   if ((o.sigmoid != 0 && o.sigmoid != 1) || (o.no_renorm != 0 && o.no_renorm != 1) || !std::isfinite(o.scale) ||
       o.group_top < 0 || o.group_top > 2 || (ld < n_expert && t > 1) || ld < 0 || ld > ((int64_t)1 << 30))
     return FT_ERR_INVALID_ARG;
@@ -401,7 +401,12 @@ size_t ft_attn_kv_scratch_bytes(const ft_kv_cache* cache, int64_t n_tok, int64_t
   if (opts) o = *opts;
   AttnArgs a = {};
   if (!cache || attn_sizes(cache, n_tok, n_head, n_seq, max_kv, o, &a) != FT_OK || n_tok == 0 || n_seq == 0) return 0;
-  return align256(ftk_attn_plan(a).scratch);
+  size_t most = 0;
+  for (const int type : {FT_F32, FT_F16, FT_BF16}) {   // the split depends on the type
+    a.ftype = type;
+    most = std::max(most, ftk_attn_plan(a).scratch);
+  }
+  return align256(most);
 }
 
 ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int64_t q_token, int64_t q_head,
@@ -448,8 +453,10 @@ ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int
   a.table_ld = table_ld;
   a.cols = (int)n_col;
   const AttnPlan p = ftk_attn_plan(a);
+  // launches of under 2^32 threads (512 a tile, 64 a row of a join)
   for (const AttnSplit& x : {p.shared, p.tile, p.step})
-    if (x.tiles * a.n_kv_head > INT32_MAX || x.n_split > 65535) return FT_ERR_SHAPE;
+    if (x.tiles * a.n_kv_head >= (1 << 23) || x.n_split > 65535) return FT_ERR_SHAPE;
+  if (p.scratch && std::max(n_tok * n_head, p.step_rows * n_seq * cache->n_kv_head) >= (1 << 26)) return FT_ERR_SHAPE;
   void* base = o.workspace;
   if (p.scratch && base && o.workspace_bytes < p.scratch) return FT_ERR_NO_SCRATCH;
   if (p.scratch && !base) {

@@ -65,6 +65,14 @@ __device__ __forceinline__ float capped_score(float x, float cap) {
   return fmaf(-2.0f * cap, r, cap);
 }
 
+// from a product of operands to what capped_score takes, or to the score in powers of two;
+// finite, as a product may be 0
+template <bool EXACT>
+__device__ __forceinline__ float score_factor(float c, float softcap) {
+  const float f = softcap > 0.0f ? c / softcap * (EXACT ? 1.0f : 2.0f * LOG2E) : c * LOG2E;
+  return fminf(f, 3.0e38f);
+}
+
 // two fp16 numbers of a word (by value: a bit cast of a vector's element would read the
 // vector's first)
 __device__ __forceinline__ h16x2 halves(uint32_t w) { return __builtin_bit_cast(h16x2, w); }
@@ -415,7 +423,7 @@ attn_step_kernel(AttnArgs A) {
   h16x8 qh[NB], ql[LO ? NB : 1];
   const float c1 = q_operands<NB, LO>(A, x, qh, ql);
   const bool capped = A.softcap > 0.0f, plain = !capped && !A.slopes;
-  const float c0 = capped ? c1 / A.softcap * (LO ? 1.0f : 2.0f * LOG2E) : c1 * LOG2E, cap = A.softcap * LOG2E;
+  const float c0 = score_factor<LO>(c1, A.softcap), cap = A.softcap * LOG2E;
   const float k0 = plain ? c0 : 1.0f;   // the factor can wait for the exponent
 
   float m = NO_MAX, l = 0.0f;
@@ -738,7 +746,7 @@ attn_tile_kernel(AttnArgs A) {
     float x[NB][8];
     kv_load_row<NB>(A.ftype, A.q, row[c].tok * A.q_token + head * A.q_head + 8 * g, A.q_vec, x);
     const float c1 = q_operands<NB, LO>(A, x, qh[c], ql[LO ? c : 0]);
-    c0[c] = capped ? c1 / A.softcap * (LO ? 1.0f : 2.0f * LOG2E) : c1 * LOG2E;
+    c0[c] = score_factor<LO>(c1, A.softcap);
     if (g == 0) {
       s_tok[wave][c][col] = row[c].real ? row[c].tok : -1;
       s_head[wave][c][col] = head;

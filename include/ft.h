@@ -277,7 +277,7 @@ ft_status ft_debug_ceiling(int which, const void* buf, int64_t bytes, int64_t it
      `renorm`, times scale.
    Every tie goes to the lower index.  Scores, choices and sums are held in 64 bits,
    w is rounded to fp32 once.  A logit of -inf has score 0; NaN logits count as -inf
-   when experts are chosen.  1 <= topk <= min(32, topk_group * n_expert / n_group),
+   when experts are chosen.  t <= 2^25, 1 <= topk <= min(32, topk_group * n_expert / n_group),
    n_expert <= 1024, n_group <= 64 and a divisor of n_expert, 1 <= topk_group <=
    n_group.  opts NULL: softmax, no bias, one group, renorm, scale 1. */
 typedef struct {
@@ -325,7 +325,8 @@ size_t ft_kv_page_bytes(ft_type type, int64_t page_size, int64_t n_kv_head, int6
               q = clamp(round_half_away(x / d), -8, 7);
    against the stored d (q = 0 where it is 0); d is limited to +-65504.  The slots of
    one call must be distinct: of two tokens with one slot, each code and scale is one or
-   the other's. */
+   the other's.  A NaN has no magnitude and an unspecified code.  t <= 2^24, here and in
+   ft_kv_load. */
 ft_status ft_kv_store(const ft_kv_cache* cache, ft_float type, const void* k, int64_t k_token, int64_t k_head,
                       const void* v, int64_t v_token, int64_t v_head, const int64_t* slots, int64_t t,
                       ft_stream_t stream);
@@ -354,7 +355,9 @@ ft_status ft_kv_load(const ft_kv_cache* cache, const int64_t* slots, int64_t t, 
    fp32: products of fp16 pairs summed in fp32, about fp32 accuracy; fp16: the
    probabilities times V's scales are rounded to fp16, everything else as for fp32; bf16:
    with many query tokens the keys and the probabilities are rounded to fp16 too.
-   Page ids outside the pool are clamped.  opts NULL: causal, scale 1/sqrt(head_dim).
+   Page ids outside the pool are clamped.  Refused as too large: n_tok > 2^24, n_seq > 2^20,
+   n_head > 1024, max_kv > 2^30, n_tok * G >= 2^30, and more rows than one launch takes
+   (n_tok * n_head past 2^30, less where the keys are split).  opts NULL: causal, scale 1/sqrt(head_dim).
    Scratch (parts of split keys): the stream's pool, or the caller's `workspace` (16-byte
    aligned, ft_attn_kv_scratch_bytes).  Graphs captured on one stream share its pool: give
    those that may replay at the same time a workspace each. */
@@ -373,7 +376,7 @@ ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int
                      int64_t n_tok, int64_t n_head, const int32_t* q_start, const int32_t* kv_len,
                      const int32_t* table, int64_t table_ld, int64_t n_col, int64_t n_seq, int64_t max_kv, void* out,
                      int64_t out_token, int64_t out_head, const ft_attn_opts* opts, ft_stream_t stream);
-/* scratch bytes ft_attn_kv needs for these sizes and options */
+/* scratch bytes ft_attn_kv needs for these sizes and options, whatever the type */
 size_t ft_attn_kv_scratch_bytes(const ft_kv_cache* cache, int64_t n_tok, int64_t n_head, int64_t n_seq, int64_t max_kv,
                                 const ft_attn_opts* opts);
 

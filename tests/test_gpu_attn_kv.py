@@ -247,6 +247,48 @@ def test_bounds_of_the_host():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("new,heads,max_kv,shared", [([130], 32, 6000, 0), ([300], 32, 3000, 0), ([20, 130, 1], 32, 2000, 0),
+                                                     ([1] * 20, 32, 3000, 1024), ([2], 32, 9000, 0)])
+def test_a_workspace_holds_every_type(new, heads, max_kv, shared, dtype):
+    """The split of the keys depends on the type, the workspace's size does not."""
+    kv = [shared + max(new) + 70] * len(new)
+    cache, table, _ = build(kv, 8, 128, 16, "Q8_0", "Q8_0", 5, shared)
+    table = torch.cat([table, torch.zeros(len(new), max_kv // 16, dtype=torch.int32, device="cuda")], 1).contiguous()
+    q = torch.randn(sum(new), heads, 128, generator=torch.Generator().manual_seed(6)).to(TYPES[dtype]).cuda()
+    args = (cache, q, table, ints(kv), ints(np.concatenate([[0], np.cumsum(new)])))
+    want = ft.attn_kv(*args, max_kv=max_kv, n_shared=shared)
+    ws = torch.empty(ft.attn_kv_scratch_bytes(cache, sum(new), heads, len(new), max_kv, n_shared=shared), dtype=torch.uint8, device="cuda")
+    assert torch.equal(ft.attn_kv(*args, max_kv=max_kv, n_shared=shared, workspace=ws if ws.numel() else None), want)
+
+
+# rows enough that the kernel with two row operands per wave is taken (two workgroups per CU of the other would be
+# slower): 264 tokens of 32 query heads per key/value head
+@pytest.mark.parametrize("k,v", PAIRS)
+def test_many_rows_of_bf16(k, v):
+    check([500], [264], 128, 4, 128, k=k, v=v, dtype="bf16", causal=False)
+
+
+@pytest.mark.parametrize("kv,new,kw", [([2900], [264], dict(softcap=20.0, max_kv=3000)),
+                                       ([590, 450, 3], [150, 130, 3], dict(causal=False, slopes=[0.5 / (1 + h) for h in range(128)])),
+                                       ([700], [270], dict(causal=False, window=300, prefix=[40]))])
+def test_masks_of_many_rows_of_bf16(kv, new, kw):
+    check(kv, new, 128, 4, 128, dtype="bf16", **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_a_cap_far_below_every_score(dtype):
+    """cap * tanh(s / cap) with a cap of 1e-37 and q rows of large and zero elements: all visible keys weigh alike."""
+    cache, table, refs = build([70], 1, 64, 16, "Q8_0", "Q8_0", 9)
+    q = torch.zeros(2, 2, 64)
+    q[0] = 1e4
+    out = ft.attn_kv(cache, q.to(TYPES[dtype]).cuda(), table, ints([70]), ints([0, 2]), causal=False, softcap=1e-37, scale=1e3)
+    mean = refs[0][1].mean(0)[0]
+    # the weights' sum in 32 bits (70 terms), their product with V's scales and the output's rounding at half a step each
+    tol = {"f32": 2 ** -17, "f16": 2 ** -10, "bf16": 2 ** -7}[dtype] * np.abs(refs[0][1]).mean(0)[0]
+    assert np.all(np.abs(out.double().cpu().numpy() - mean) <= tol)
+
+
 def test_workspace_and_streams():
     kv = [2000, 900]
     cache, table, _ = build(kv, 2, 64, 32, "Q8_0", "Q8_0", 6)

@@ -102,6 +102,8 @@ def test_attention_refused():
     assert attn(max_kv=-1) == "FT_ERR_INVALID_ARG"
     assert attn(n_tok=-1) == "FT_ERR_INVALID_ARG"
     assert attn(n_tok=(1 << 24) + 1) == "FT_ERR_SHAPE"
+    wide = dict(c=cache(n_kv_head=64), n_tok=1 << 24, n_head=64, qt=64 * 64, ot=64 * 64)
+    assert attn(**wide) == "FT_ERR_SHAPE"                        # more rows than one launch takes
     assert attn(window=-1) == "FT_ERR_INVALID_ARG"
     for bad in (-1.0, float("nan"), float("inf")):
         assert attn(softcap=bad) == "FT_ERR_INVALID_ARG"
@@ -134,6 +136,7 @@ def test_route_refused():
     assert route(ty=3) == "FT_ERR_UNSUPPORTED"
     assert route(e=1025, ld=1025) == "FT_ERR_SHAPE"
     assert route(e=0, ld=0) == "FT_ERR_SHAPE"
+    assert route(t=(1 << 25) + 1) == "FT_ERR_SHAPE"
     assert route(topk=0) == "FT_ERR_SHAPE"
     assert route(topk=33) == "FT_ERR_SHAPE"
     assert route(e=3, ld=3, topk=4) == "FT_ERR_SHAPE"
