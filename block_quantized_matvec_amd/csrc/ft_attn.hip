@@ -163,7 +163,7 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
           best = {n_tiles, (int)n, (int)per, wide};
           best_cost = cost;
         }
-        if (per <= 4) break;
+        if (per <= 4 || n * filled * a.n_kv_head > 2048) break;   // eight rounds of the chip
       }
     }
     return best;
