@@ -14,9 +14,12 @@
 // that token again in fp64 (route_exact).
 //
 // Bound by instruction issue and the length of a token's chain, not by HBM: 16384 tokens
-// x 256 experts, sigmoid, bias, 8 groups, top 8 (16.8 MB in) take 19.5 us (12 us without
-// groups), of which 4.4 us are the tail of the few tokens that fp64 decides; with every
-// exponential in fp64 and a wave per token 33 us.
+// x 256 experts, sigmoid, bias, 8 groups, top 8 (16.8 MB in) take 18.6 us (10.8 us without
+// bias and groups), of which 4 us are the tail of the few tokens that fp64 decides (bf16
+// logits without a bias, where one token in a hundred has three equal ones at the last
+// slot: 17 us); with every exponential in fp64 and a wave per token 33 us.  3 tokens x 128
+// experts: 4.7 us.  More than 14 slots go to the kernels with more lanes per token (top 16
+// of 1024, 16384 tokens: 43 us; every token in fp64: 126).
 #include "ft_device.h"
 #include "ft_internal.h"
 #include "ft_kv.h"
@@ -163,20 +166,9 @@ __device__ __forceinline__ void route_exact(const RouteArgs& A, int64_t tok, dou
   wave_lds_sync();   // the LDS may be used again
 }
 
-template <int MAXE>
-__global__ void __launch_bounds__(256)
-route_exact_kernel(RouteArgs A) {
-  __shared__ double s_choice[4][64 * MAXE];
-  __shared__ double s_w[4][32];
-  __shared__ int s_id[4][32];
-  const int wave = wave_id();
-  const int64_t tok = (int64_t)blockIdx.x * 4 + wave;
-  if (tok < A.t) route_exact<MAXE>(A, tok, s_choice[wave], s_w[wave], s_id[wave]);   // no barrier: a wave meets only itself
-}
-
 // ---------------------------------------------------------------------------
 // fp32 with a bound: LANES lanes per token, lane l holds experts 4 (i LANES + l) ..+3,
-// i < Q (16-byte loads, a token's lanes side by side).  topk <= 14.
+// i < Q (16-byte loads, a token's lanes side by side).  topk + 2 <= LANES.
 //
 // With s the largest score and c the largest choice, expert e's key is its distance
 // from c in units of s 2^-20 above its index (24 bits and 8 for up to 256 experts, else
@@ -481,20 +473,11 @@ route_fast_kernel(RouteArgs A) {
   // every lane look for its next four.
   uint32_t mine4[4];
   smallest4<N>(key, true, 0u, mine4);
-  uint32_t before = 0, two_before = 0;
   uint32_t my_key = ~0u, last = 0;
   int left = 4;
-  bool gave = false, near = false;
+  bool gave = false;
   for (int r = 0; r < A.topk + 2; ++r) {
     const uint32_t best = lanes_umin<LANES>(mine4[0]);
-    const uint32_t far = best >> IB;
-    // the order of the slots, and of the last with the first left out, is open ...
-    near |= (r > 0) & (r <= A.topk) & (far - before < room);
-    // ... and cannot be settled among them: too far to tell, or a third that close
-    close |= (far >= FAR) & ((r < A.topk) | ((r <= A.topk + 1) & (FAR - before < room)));
-    close |= (r == A.topk + 1) & (far - two_before < room);
-    two_before = before;
-    before = far;
     my_key = l == r ? best : my_key;
     const bool won = mine4[0] == best;
     last = won ? best : last;
@@ -512,9 +495,20 @@ route_fast_kernel(RouteArgs A) {
 
   // the slots' scores in fp64, a slot per lane; softmax: over exp of the largest logit
   wave_lds_sync();
-  const bool have = (my_key >> IB) < FAR;
+  const uint32_t far = my_key >> IB;
+  const bool have = far < FAR;
   const int my_id = min((int)(my_key & ((1u << IB) - 1)), E - 1);
-  const double v = have ? (double)sx[my_id] : 0.0;
+  const float xv = have ? sx[my_id] : 0.0f;
+  const double v = (double)xv;
+  // The order of the slots, and of the last with the first left out, is open between
+  // neighbours that close; but equal logits (16-bit ones often are) without a bias are equal
+  // in 64 bits too, and their keys are in the order of the index ...
+  const uint32_t before = __shfl_up(far, 1, 64), two_before = __shfl_up(far, 2, 64);
+  const bool same = !A.bias && __shfl_up(xv, 1, 64) == xv;
+  const bool near = (l > 0) & (l <= A.topk) & (far - before < room) & !same;
+  // ... and cannot be settled among the slots: too far to tell, or a third that close
+  close |= (far >= FAR) & ((l < A.topk) | ((l <= A.topk + 1) & (FAR - before < room)));
+  close |= (l == A.topk + 1) & (far - two_before < room);
   double w = A.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)top);
   const bool settle = __ballot(near) != 0;
   if (!A.sigmoid && (!A.renorm || (settle && A.bias))) {
@@ -564,11 +558,7 @@ hipError_t ftk_launch_route_ex(const RouteArgs& a0, hipStream_t st) {
   a.vec_bias = ((uintptr_t)a.bias & 15) == 0 && a.n_expert % 4 == 0;
   const int E = a.n_expert;
   const auto grid = [&](int per) { return (unsigned)((a.t + per - 1) / per); };
-  if (a.topk > 14) {
-    if (E <= 64) route_exact_kernel<1><<<grid(4), 256, 0, st>>>(a);
-    else if (E <= 256) route_exact_kernel<4><<<grid(4), 256, 0, st>>>(a);
-    else route_exact_kernel<16><<<grid(4), 256, 0, st>>>(a);
-  } else if (E <= 256 && a.t <= 2048) {   // a wave per token: fewer steps after one another
+  if (E <= 256 && (a.t <= 2048 || a.topk > 14)) {   // a wave per token: fewer steps after one another
     route_fast_kernel<64, 1, 4><<<grid(4), 256, 0, st>>>(a);
   } else if (E <= 64) {
     route_fast_kernel<16, 1, 1><<<grid(16), 256, 0, st>>>(a);
@@ -576,7 +566,7 @@ hipError_t ftk_launch_route_ex(const RouteArgs& a0, hipStream_t st) {
     route_fast_kernel<16, 2, 2><<<grid(16), 256, 0, st>>>(a);
   } else if (E <= 256) {
     route_fast_kernel<16, 4, 4><<<grid(16), 256, 0, st>>>(a);
-  } else if (E <= 512) {
+  } else if (E <= 512 && a.topk <= 30) {
     route_fast_kernel<32, 4, 8><<<grid(8), 256, 0, st>>>(a);
   } else {
     route_fast_kernel<64, 4, 16><<<grid(4), 256, 0, st>>>(a);
