@@ -88,6 +88,20 @@ def test_neighbours():
         check(x, 16, score=score, bias=bias)
 
 
+@pytest.mark.parametrize("t", [5, 2049])
+@pytest.mark.parametrize("e,topk", [(40, 15), (64, 32), (256, 15), (256, 32), (300, 30), (512, 31), (1000, 32)])
+def test_many_slots_and_equal_logits(t, e, topk):
+    """16-bit logits, of which many are equal, the last slot's and the first left out's among them."""
+    g = torch.Generator().manual_seed(e + topk)
+    for dtype, size in ((torch.bfloat16, 1.0), (torch.float16, 1.0), (torch.bfloat16, 0.02), (torch.bfloat16, 30.0)):
+        x = (size * torch.randn(t, e, generator=g)).to(dtype)
+        check(x, topk, score="sigmoid")
+        check(x, topk, renorm=False)
+    x = torch.randint(0, 6, (t, e), generator=g).to(torch.bfloat16)       # a few values only
+    check(x, topk)
+    check(x, topk, score="sigmoid", bias=(torch.randint(0, 3, (e,), generator=g) / 4).float())
+
+
 def test_many_from_one_lane():
     """The best experts side by side: one lane of the kernel gives up all of its own, more than once."""
     for e, first in ((256, 0), (256, 64), (512, 128), (1024, 256), (64, 0), (128, 4)):
