@@ -187,6 +187,13 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
     p.step = whole;
     p.eight = 1;
   }
+  // beside the tile kernel there may be no such sequence at all, and a join would still be
+  // launched (three prompts of 130 to 200 tokens: 23.3 us against 25.0; with 64 steps and a
+  // short sequence among eight, 79 against 65 the other way)
+  if (p.step_rows && a.dim <= 128 && p.step.n_split > 1 && steps(16) <= 16) {
+    p.step = {p.step.tiles, 1, (int)steps(16), 0};
+    p.eight = 1;
+  }
   if (a.n_shared > 0) {
     p.shared_tile = rows > kStepRows;
     p.shared = p.shared_tile ? tiles(rows, 1, true) : split_keys(a, (rows + 15) / 16, a.n_shared / 64 + 1, 512, 4, 4);
