@@ -990,16 +990,30 @@ attn_tile_kernel(AttnArgs A) {
       for (int c = 0; c < CT; ++c)
 #pragma unroll
         for (int t = 0; t < 4; ++t) s[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      // READ_AHEAD: a block's operands are read from LDS while the one before is multiplied
+      // (fp32 rows at head size 128, where there are registers for it: chunk 340 us against
+      // 365; at 96 it spills, at 64 and 256 it gains nothing)
+      constexpr bool READ_AHEAD = LO && NB == 4;
+      u32x4 ka[READ_AHEAD ? 2 : 1][4], kd[READ_AHEAD ? 2 : 1][2];
+      const auto read_k = [&](int b) {
+        const int to = READ_AHEAD ? b & 1 : 0;
+        if constexpr (READ_AHEAD) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) ka[to][t] = L.k[buf][t][b][slot];
+        }
+        if constexpr (PREC != PREC_BF16) {
+          kd[to][0] = *(const u32x4*)&L.kd[buf][b][16 * g];
+          kd[to][1] = *(const u32x4*)&L.kd[buf][b][16 * g + 8];
+        }
+      };
+      if constexpr (READ_AHEAD) read_k(0);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        u32x4 kd[2];
-        if constexpr (PREC != PREC_BF16) {
-          kd[0] = *(const u32x4*)&L.kd[buf][b][16 * g];
-          kd[1] = *(const u32x4*)&L.kd[buf][b][16 * g + 8];
-        }
+        if constexpr (!READ_AHEAD) read_k(b);
+        else if (b + 1 < NB) read_k(b + 1);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const h16x8 a = __builtin_bit_cast(h16x8, L.k[buf][t][b][slot]);
+          const h16x8 a = __builtin_bit_cast(h16x8, READ_AHEAD ? ka[b & 1][t] : L.k[buf][t][b][slot]);
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             if constexpr (PREC == PREC_BF16) {
@@ -1007,7 +1021,8 @@ attn_tile_kernel(AttnArgs A) {
             } else {
               f32x4 x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[c][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
               if constexpr (LO) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[c][b], x, 0, 0, 0);
-              const h16x2 d0 = halves(kd[t >> 1][2 * (t & 1)]), d1 = halves(kd[t >> 1][2 * (t & 1) + 1]);
+              const u32x4 d = kd[READ_AHEAD ? b & 1 : 0][t >> 1];
+              const h16x2 d0 = halves(d[2 * (t & 1)]), d1 = halves(d[2 * (t & 1) + 1]);
               s[c][t][0] = fmaf((float)d0[0], x[0], s[c][t][0]);
               s[c][t][1] = fmaf((float)d0[1], x[1], s[c][t][1]);
               s[c][t][2] = fmaf((float)d1[0], x[2], s[c][t][2]);
@@ -1092,11 +1107,22 @@ attn_tile_kernel(AttnArgs A) {
           l[c] += sum;
         }
       }
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
+      u32x4 va[2][2][2], vd[2][2];
+      const auto read_v = [&](int b) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32x4 dw = *(const u32x4*)&L.vd[buf][b][16 * g + 8 * h];
+          vd[b & 1][h] = *(const u32x4*)&L.vd[buf][b][16 * g + 8 * h];
+#pragma unroll
+          for (int d2 = 0; d2 < 2; ++d2) va[b & 1][h][d2] = L.v[buf][2 * b + d2][h][slot];
+        }
+      };
+      if constexpr (READ_AHEAD) read_v(0);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (READ_AHEAD && b + 1 < NB) read_v(b + 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x4 dw = READ_AHEAD ? vd[b & 1][h] : *(const u32x4*)&L.vd[buf][b][16 * g + 8 * h];
           h16x8 hi[CT], lo[LO ? CT : 1];
           if constexpr (PREC == PREC_BF16) {
             const h16x8 d = __builtin_bit_cast(h16x8, dw);
@@ -1116,7 +1142,7 @@ attn_tile_kernel(AttnArgs A) {
           }
 #pragma unroll
           for (int d2 = 0; d2 < 2; ++d2) {
-            const h16x8 a = __builtin_bit_cast(h16x8, L.v[buf][2 * b + d2][h][slot]);
+            const h16x8 a = __builtin_bit_cast(h16x8, READ_AHEAD ? va[b & 1][h][d2] : L.v[buf][2 * b + d2][h][slot]);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
               o[c][2 * b + d2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, hi[c], o[c][2 * b + d2], 0, 0, 0);
