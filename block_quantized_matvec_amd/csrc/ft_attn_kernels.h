@@ -943,12 +943,12 @@ attn_tile_kernel(AttnArgs A) {
   };
 
   // A step's keys are fetched during the step before it and laid out at its end, between two
-  // barriers.  With two row operands per wave (STAGGER) half of the waves, which share the
+  // barriers.  Where one workgroup fills a CU (STAGGER) half of its waves, which share the
   // SIMDs with the other half, lay out a step earlier, before their products in place of
   // after them, so that one half's matrix instructions run beside the other's vector
-  // instructions (4096 rows over 16384 keys: 1379 us against 1445; with one operand there
-  // are two workgroups per CU out of step already: fp32 chunk 376 us against 360).
-  constexpr bool STAGGER = CT == 2;
+  // instructions (4096 bf16 rows over 16384 keys: 1379 us against 1445, fp32 causal prompts
+  // 732 against 767).  Two workgroups are out of step already (fp16 the same to 2 % slower).
+  constexpr bool STAGGER = CT == 2 || NB == 8 || (NB == 4 && PREC == PREC_F32);
   const bool late = STAGGER && wave >= NW / 2;
   const auto get = [&](int i) {
     if (i >= s_end) return;
