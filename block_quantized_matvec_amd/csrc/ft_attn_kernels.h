@@ -640,7 +640,7 @@ attn_step_kernel(AttnArgs A) {
 // Bound by vector instructions, not by the matrix unit (busy a quarter of the time): 4096
 // bf16 rows over 16384 keys of 8 heads of 128 take 1380 us, 797 TFLOP/s; ragged causal
 // prompts of 2239 to 4096 tokens 400 us, with a cap 487 us (two exponentials and a
-// reciprocal per score); an fp32 chunk of 1000 tokens over 7000 keys 352 us, 300 TFLOP/s of
+// reciprocal per score); an fp32 chunk of 1000 tokens over 7000 keys 332 us, 320 TFLOP/s of
 // the result and twice that of fp16 products.
 // Two row operands per wave (CT = 2) halve the layout's share for bf16 at head size 128
 // (423 us against 461); fp16 and fp32 rows then spill (1066 us against 535), other head
@@ -992,7 +992,8 @@ attn_tile_kernel(AttnArgs A) {
         for (int t = 0; t < 4; ++t) s[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       // READ_AHEAD: a block's operands are read from LDS while the one before is multiplied
       // (fp32 rows at head size 128, where there are registers for it: chunk 340 us against
-      // 365; at 96 it spills, at 64 and 256 it gains nothing)
+      // 365, and 332 with V's first block ahead of the softmax; at 96 it spills, at 64 and
+      // 256 it gains nothing)
       constexpr bool READ_AHEAD = LO && NB == 4;
       u32x4 ka[READ_AHEAD ? 2 : 1][4], kd[READ_AHEAD ? 2 : 1][2];
       const auto read_k = [&](int b) {
@@ -1032,6 +1033,16 @@ attn_tile_kernel(AttnArgs A) {
         }
         if constexpr (PREC != PREC_BF16) __builtin_amdgcn_sched_barrier(0);
       }
+      u32x4 va[2][2][2], vd[2][2];
+      const auto read_v = [&](int b) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          vd[b & 1][h] = *(const u32x4*)&L.vd[buf][b][16 * g + 8 * h];
+#pragma unroll
+          for (int d2 = 0; d2 < 2; ++d2) va[b & 1][h][d2] = L.v[buf][2 * b + d2][h][slot];
+        }
+      };
+      if constexpr (READ_AHEAD) read_v(0);
       if constexpr (LO) __builtin_amdgcn_s_setprio(0);
       const int ev = min((int)(L.vmax[buf] >> 10), 30);
       const float lift = (float)(29 - ev);
@@ -1107,16 +1118,6 @@ attn_tile_kernel(AttnArgs A) {
           l[c] += sum;
         }
       }
-      u32x4 va[2][2][2], vd[2][2];
-      const auto read_v = [&](int b) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          vd[b & 1][h] = *(const u32x4*)&L.vd[buf][b][16 * g + 8 * h];
-#pragma unroll
-          for (int d2 = 0; d2 < 2; ++d2) va[b & 1][h][d2] = L.v[buf][2 * b + d2][h][slot];
-        }
-      };
-      if constexpr (READ_AHEAD) read_v(0);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         if (READ_AHEAD && b + 1 < NB) read_v(b + 1);
