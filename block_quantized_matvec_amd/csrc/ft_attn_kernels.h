@@ -990,11 +990,11 @@ attn_tile_kernel(AttnArgs A) {
       for (int c = 0; c < CT; ++c)
 #pragma unroll
         for (int t = 0; t < 4; ++t) s[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      // READ_AHEAD: a block's operands are read from LDS while the one before is multiplied
-      // (fp32 rows at head size 128, where there are registers for it: chunk 340 us against
-      // 365, and 332 with V's first block ahead of the softmax; at 96 it spills, at 64 and
-      // 256 it gains nothing)
-      constexpr bool READ_AHEAD = LO && NB == 4;
+      // READ_AHEAD: a block's operands are read from LDS while the one before is multiplied,
+      // V's first ones ahead of the softmax, where one workgroup fills a CU and leaves
+      // registers for it (fp32 chunk 332 us against 365; head size 256 825, 1026 and 1334 us
+      // against 836, 1072 and 1370; at 96 it spills, at 64 it gains nothing)
+      constexpr bool READ_AHEAD = NB == 8 || (LO && NB == 4);
       u32x4 ka[READ_AHEAD ? 2 : 1][4], kd[READ_AHEAD ? 2 : 1][2];
       const auto read_k = [&](int b) {
         const int to = READ_AHEAD ? b & 1 : 0;
