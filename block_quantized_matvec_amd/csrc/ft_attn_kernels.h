@@ -638,7 +638,7 @@ attn_step_kernel(AttnArgs A) {
 //   bf16 rows: K's scales in the operand (fp16, a power of two per key apart), p and its
 //     product with V's scale in fp16: no fp32 work per block.
 // Bound by vector instructions, not by the matrix unit (busy a quarter of the time): 4096
-// bf16 rows over 16384 keys of 8 heads of 128 take 1380 us, 797 TFLOP/s; ragged causal
+// bf16 rows over 16384 keys of 8 heads of 128 take 1318 us, 835 TFLOP/s; ragged causal
 // prompts of 2239 to 4096 tokens 400 us, with a cap 487 us (two exponentials and a
 // reciprocal per score); an fp32 chunk of 1000 tokens over 7000 keys 332 us, 320 TFLOP/s of
 // the result and twice that of fp16 products.
@@ -943,13 +943,13 @@ attn_tile_kernel(AttnArgs A) {
   };
 
   // A step's keys are fetched during the step before it and laid out at its end, between two
-  // barriers.  Where one workgroup fills a CU (STAGGER) half of its waves, which share the
+  // barriers.  Where one workgroup fills a CU (ALONE) half of its waves, which share the
   // SIMDs with the other half, lay out a step earlier, before their products in place of
   // after them, so that one half's matrix instructions run beside the other's vector
   // instructions (4096 bf16 rows over 16384 keys: 1379 us against 1445, fp32 causal prompts
   // 732 against 767).  Two workgroups are out of step already (fp16 the same to 2 % slower).
-  constexpr bool STAGGER = CT == 2 || NB == 8 || (NB == 4 && PREC == PREC_F32);
-  const bool late = STAGGER && wave >= NW / 2;
+  constexpr bool ALONE = CT == 2 || NB == 8 || (NB == 4 && PREC == PREC_F32);
+  const bool late = ALONE && wave >= NW / 2;
   const auto get = [&](int i) {
     if (i >= s_end) return;
     fetch(steps.block(i) * ATTN_STEP);
@@ -963,7 +963,7 @@ attn_tile_kernel(AttnArgs A) {
   }
   get(s0);
   lay_out(s0);
-  if constexpr (STAGGER) {
+  if constexpr (ALONE) {
     get(s0 + 1);
     lds_barrier();
     if (late) {
@@ -974,7 +974,7 @@ attn_tile_kernel(AttnArgs A) {
   for (int i = s0; i < s_end; ++i) {
     const int buf = (i - s0) & 1;
     const int key0 = steps.block(i) * ATTN_STEP;
-    if constexpr (!STAGGER) {
+    if constexpr (!ALONE) {
       lds_barrier();
       get(i + 1);
     }
@@ -990,15 +990,14 @@ attn_tile_kernel(AttnArgs A) {
       for (int c = 0; c < CT; ++c)
 #pragma unroll
         for (int t = 0; t < 4; ++t) s[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      // READ_AHEAD: a block's operands are read from LDS while the one before is multiplied,
-      // V's first ones ahead of the softmax, where one workgroup fills a CU and leaves
-      // registers for it (fp32 chunk 332 us against 365; head size 256 825, 1026 and 1334 us
-      // against 836, 1072 and 1370; at 96 it spills, at 64 it gains nothing)
-      constexpr bool READ_AHEAD = NB == 8 || (LO && NB == 4);
-      u32x4 ka[READ_AHEAD ? 2 : 1][4], kd[READ_AHEAD ? 2 : 1][2];
+      // ALONE, which leaves registers for it: a block's operands are read from LDS while the
+      // one before is multiplied, V's first ones ahead of the softmax (fp32 chunk 332 us
+      // against 365; head size 256 825, 1026 and 1334 us against 836, 1072 and 1370; 4096 bf16
+      // rows 1318 against 1344; elsewhere it spills or gains nothing)
+      u32x4 ka[ALONE ? 2 : 1][4], kd[ALONE ? 2 : 1][2];
       const auto read_k = [&](int b) {
-        const int to = READ_AHEAD ? b & 1 : 0;
-        if constexpr (READ_AHEAD) {
+        const int to = ALONE ? b & 1 : 0;
+        if constexpr (ALONE) {
 #pragma unroll
           for (int t = 0; t < 4; ++t) ka[to][t] = L.k[buf][t][b][slot];
         }
@@ -1007,14 +1006,14 @@ attn_tile_kernel(AttnArgs A) {
           kd[to][1] = *(const u32x4*)&L.kd[buf][b][16 * g + 8];
         }
       };
-      if constexpr (READ_AHEAD) read_k(0);
+      if constexpr (ALONE) read_k(0);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        if constexpr (!READ_AHEAD) read_k(b);
+        if constexpr (!ALONE) read_k(b);
         else if (b + 1 < NB) read_k(b + 1);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const h16x8 a = __builtin_bit_cast(h16x8, READ_AHEAD ? ka[b & 1][t] : L.k[buf][t][b][slot]);
+          const h16x8 a = __builtin_bit_cast(h16x8, ALONE ? ka[b & 1][t] : L.k[buf][t][b][slot]);
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             if constexpr (PREC == PREC_BF16) {
@@ -1022,7 +1021,7 @@ attn_tile_kernel(AttnArgs A) {
             } else {
               f32x4 x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[c][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
               if constexpr (LO) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[c][b], x, 0, 0, 0);
-              const u32x4 d = kd[READ_AHEAD ? b & 1 : 0][t >> 1];
+              const u32x4 d = kd[ALONE ? b & 1 : 0][t >> 1];
               const h16x2 d0 = halves(d[2 * (t & 1)]), d1 = halves(d[2 * (t & 1) + 1]);
               s[c][t][0] = fmaf((float)d0[0], x[0], s[c][t][0]);
               s[c][t][1] = fmaf((float)d0[1], x[1], s[c][t][1]);
@@ -1042,7 +1041,7 @@ attn_tile_kernel(AttnArgs A) {
           for (int d2 = 0; d2 < 2; ++d2) va[b & 1][h][d2] = L.v[buf][2 * b + d2][h][slot];
         }
       };
-      if constexpr (READ_AHEAD) read_v(0);
+      if constexpr (ALONE) read_v(0);
       if constexpr (LO) __builtin_amdgcn_s_setprio(0);
       const int ev = min((int)(L.vmax[buf] >> 10), 30);
       const float lift = (float)(29 - ev);
@@ -1120,10 +1119,10 @@ attn_tile_kernel(AttnArgs A) {
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        if (READ_AHEAD && b + 1 < NB) read_v(b + 1);
+        if (ALONE && b + 1 < NB) read_v(b + 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32x4 dw = READ_AHEAD ? vd[b & 1][h] : *(const u32x4*)&L.vd[buf][b][16 * g + 8 * h];
+          const u32x4 dw = ALONE ? vd[b & 1][h] : *(const u32x4*)&L.vd[buf][b][16 * g + 8 * h];
           h16x8 hi[CT], lo[LO ? CT : 1];
           if constexpr (PREC == PREC_BF16) {
             const h16x8 d = __builtin_bit_cast(h16x8, dw);
@@ -1143,7 +1142,7 @@ attn_tile_kernel(AttnArgs A) {
           }
 #pragma unroll
           for (int d2 = 0; d2 < 2; ++d2) {
-            const h16x8 a = __builtin_bit_cast(h16x8, READ_AHEAD ? va[b & 1][h][d2] : L.v[buf][2 * b + d2][h][slot]);
+            const h16x8 a = __builtin_bit_cast(h16x8, ALONE ? va[b & 1][h][d2] : L.v[buf][2 * b + d2][h][slot]);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
               o[c][2 * b + d2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, hi[c], o[c][2 * b + d2], 0, 0, 0);
@@ -1154,7 +1153,7 @@ attn_tile_kernel(AttnArgs A) {
         if constexpr (PREC != PREC_BF16) __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if constexpr (STAGGER) {
+    if constexpr (ALONE) {
       if (late) lds_barrier();
       lay_out(i + 1 + (late ? 1 : 0));
       get(i + 2 + (late ? 1 : 0));
