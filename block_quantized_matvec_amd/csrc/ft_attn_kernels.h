@@ -639,7 +639,7 @@ attn_step_kernel(AttnArgs A) {
 //     product with V's scale in fp16: no fp32 work per block.
 // Bound by vector instructions, not by the matrix unit (busy a quarter of the time): 4096
 // bf16 rows over 16384 keys of 8 heads of 128 take 1318 us, 835 TFLOP/s; ragged causal
-// prompts of 2239 to 4096 tokens 400 us, with a cap 487 us (two exponentials and a
+// prompts of 2239 to 4096 tokens 395 us, with a cap 477 us (two exponentials and a
 // reciprocal per score); an fp32 chunk of 1000 tokens over 7000 keys 332 us, 320 TFLOP/s of
 // the result and twice that of fp16 products.
 // Two row operands per wave (CT = 2) halve the layout's share for bf16 at head size 128
