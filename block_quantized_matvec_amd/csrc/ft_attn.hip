@@ -106,7 +106,10 @@ static hipError_t attn_dim(const AttnArgs& a, hipStream_t st) {
 // lengths.
 static AttnSplit split_keys(const AttnArgs& a, int64_t tiles, int64_t steps, int64_t want, int64_t least, int64_t waves) {
   const int64_t wgs = std::max<int64_t>(tiles * a.n_kv_head, 1);
-  const int64_t n = std::max<int64_t>(1, std::min<int64_t>((want + wgs - 1) / wgs, (steps + least - 1) / least));
+  // the join walks the parts 64 at a time (one KV head, 100000 keys: 391 parts 43 us, 128 31,
+  // 64 33; 30000 keys: 118 parts 24.5 us, 64 18.9)
+  const int64_t most = std::max<int64_t>(64, steps / 12);
+  const int64_t n = std::max<int64_t>(1, std::min<int64_t>({(want + wgs - 1) / wgs, (steps + least - 1) / least, most}));
   int64_t per = (steps + n - 1) / n;
   per = std::max<int64_t>(least, (per + waves - 1) / waves * waves);
   return {tiles, (int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per, 0};
