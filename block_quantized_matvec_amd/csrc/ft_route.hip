@@ -434,6 +434,8 @@ route_fast_kernel(RouteArgs A) {
       else close |= (with & ~(1ull << (g & 63))) != 0;
     }
     if (l < A.n_group) close |= (alike & (((kept >> (l & 63)) & 1) ? ~kept : kept)) != 0;
+    // groups equal in fp32 have one rank: at the border all of them were kept
+    close |= __popcll(kept) != A.topk_group;
     if ((S & (S - 1)) == 0 && S >= 4) {   // quads are of one group
       const int shift = 31 - __builtin_clz(S);
 #pragma unroll

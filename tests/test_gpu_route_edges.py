@@ -1,0 +1,40 @@
+"""GPU: the scored router where its fp32 order is at its limits."""
+import pytest
+import torch
+
+from tests.gpu_util import need_gpu
+from tests.test_gpu_route_ex import check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+@pytest.mark.parametrize("e,n_group,topk_group,topk", [(64, 8, 2, 8), (256, 8, 4, 8), (160, 8, 3, 6), (36, 3, 2, 7), (512, 16, 5, 4),
+                                                       (1024, 64, 9, 8), (128, 32, 1, 2)])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("t", [60, 2050])
+def test_groups_that_fp32_cannot_tell_apart(e, n_group, topk_group, topk, group_top, t):
+    """Every group's best logit one of a few neighbouring numbers, of which many have the same sigmoid in fp32: in 64 bits
+    the groups are in order, and no more than topk_group of them are open."""
+    g = torch.Generator().manual_seed(e + n_group)
+    x = -1 - torch.rand(t, n_group, e // n_group, generator=g)
+    best = 2 + torch.rand(t, 1, generator=g) + torch.randint(0, 2 * n_group, (t, n_group), generator=g) * 2.0 ** -22
+    x.scatter_(2, torch.randint(0, e // n_group, (t, n_group, 1), generator=g), best.unsqueeze(-1))
+    kw = dict(score="sigmoid", n_group=n_group, topk_group=topk_group, group_top=group_top)
+    check(x.flatten(1), topk, **kw)
+    if t > 60:
+        return
+    check(x.flatten(1), topk, bias=torch.zeros(e), **kw)
+    check(x.flatten(1) + 4, topk, renorm=False, **kw)
+
+
+def test_groups_of_a_prompt():
+    """Drawn logits, where a border between groups that close is one in thousands."""
+    for seed in range(3):
+        x = 1.5 * torch.randn(6000, 64, generator=torch.Generator().manual_seed(64 + seed))
+        check(x, 8, score="sigmoid", n_group=8, topk_group=2)
+        check(x, 6, score="sigmoid", n_group=16, topk_group=4, group_top=2, bias=torch.zeros(64))
