@@ -181,7 +181,8 @@ __device__ __forceinline__ void route_exact(const RouteArgs& A, int64_t tok, dou
 // the softmax's sum within 2^-21; together under 2^-19 s = 2 units (2^-16 s = 16 in the
 // exception).  Adding the bias and taking the distance round by 2^-24 of |c| + 16 s, one
 // unit and |c| / 16 s; the unit itself half of one.  Two keys that lie `room` = 10 (50) +
-// |c| / 4 s units apart are in the right order.
+// |c| / 4 s units apart are in the right order; where that is over 10^6, a part of the
+// range that keys have, the token goes through route_exact.
 //
 // The rounds go two past topk.  Where neighbours among them are closer than `room`, the
 // slots' own 64-bit choices settle their order; only if the one after next to the last
@@ -462,7 +463,9 @@ route_fast_kernel(RouteArgs A) {
   const float inv = __builtin_amdgcn_rcpf(s) * 0x1p20f;
   // no distances without a finite choice and a scale (every logit closed, or infinite)
   close |= !(fabsf(most) < INFINITY && inv < INFINITY && fabsf(top) < INFINITY);
-  const uint32_t room = (uint32_t)fminf(units + fabsf(most) * inv * 0x1p-22f, 1e6f);
+  const float apart = units + fabsf(most) * inv * 0x1p-22f;
+  close |= !(apart <= 1e6f);   // scores far below the choice's last bits: no distance tells them apart
+  const uint32_t room = (uint32_t)fminf(apart, 1e6f);
   uint32_t key[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {

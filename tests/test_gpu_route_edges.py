@@ -38,3 +38,19 @@ def test_groups_of_a_prompt():
         x = 1.5 * torch.randn(6000, 64, generator=torch.Generator().manual_seed(64 + seed))
         check(x, 8, score="sigmoid", n_group=8, topk_group=2)
         check(x, 6, score="sigmoid", n_group=16, topk_group=4, group_top=2, bias=torch.zeros(64))
+
+
+@pytest.mark.parametrize("e", [40, 128, 256, 400, 1000])
+@pytest.mark.parametrize("t", [50, 2100])
+def test_scores_far_below_the_bias(e, t):
+    """Scores under 1e-7 of the choice: the bias decides up to its own last bits, the scores below them."""
+    g = torch.Generator().manual_seed(e)
+    x = -17 + 0.3 * torch.randn(t, e, generator=g)
+    near = 1 + torch.randint(0, 6, (e,), generator=g) * 2.0 ** -23       # biases a few last bits apart
+    check(x, 8, score="sigmoid", bias=near)
+    if t > 50:
+        return
+    check(x - 4, 8, score="sigmoid", bias=near)
+    check(x, 8, score="sigmoid", bias=(1 + 2.0 ** -20 * torch.rand(e, generator=g)))
+    if e % 4 == 0:
+        check(x, 8, score="sigmoid", bias=near, n_group=4, topk_group=2, group_top=2)
