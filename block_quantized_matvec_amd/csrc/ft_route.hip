@@ -512,7 +512,7 @@ route_fast_kernel(RouteArgs A) {
   const bool same = !A.bias && __shfl_up(xv, 1, 64) == xv;
   const bool near = (l > 0) & (l <= A.topk) & (far - before < room) & !same;
   // ... and cannot be settled among the slots: too far to tell, or a third that close
-  close |= (far >= FAR) & ((l < A.topk) | ((l <= A.topk + 1) & (FAR - before < room)));
+  close |= (far >= FAR) & ((l < A.topk) | ((l == A.topk) & (FAR - before < room)));
   close |= (l == A.topk + 1) & (far - two_before < room);
   double w = A.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)top);
   const bool settle = __ballot(near) != 0;

@@ -54,3 +54,15 @@ def test_scores_far_below_the_bias(e, t):
     check(x, 8, score="sigmoid", bias=(1 + 2.0 ** -20 * torch.rand(e, generator=g)))
     if e % 4 == 0:
         check(x, 8, score="sigmoid", bias=near, n_group=4, topk_group=2, group_top=2)
+
+
+@pytest.mark.parametrize("t", [7, 2100])
+@pytest.mark.parametrize("e,topk,kw", [(8, 8, {}), (30, 30, {}), (32, 32, {}), (128, 8, dict(n_group=16, topk_group=1)),
+                                       (64, 16, dict(n_group=8, topk_group=2)), (512, 16, dict(n_group=32, topk_group=1)),
+                                       (1000, 25, dict(n_group=40, topk_group=1, group_top=2))])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_every_open_expert_is_chosen(e, topk, kw, t, score):
+    g = torch.Generator().manual_seed(e + t)
+    x = 1.5 * torch.randn(t, e, generator=g)
+    check(x, topk, score=score, **kw)
+    check(x.bfloat16(), topk, score=score, bias=0.1 * torch.randn(e, generator=g), **kw)
