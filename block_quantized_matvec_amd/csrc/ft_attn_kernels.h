@@ -276,9 +276,29 @@ __device__ __forceinline__ AttnSeen seen_by(const AttnArgs& A, const AttnRow& r,
   s.above = A.window > 0 ? r.pos - (int)A.window : -1;
   return s;
 }
+// What any row of a tile sees.  Slots outside may hold anything (no key, a page that a window
+// has left behind): V's scales there count as zero, since 0 * NaN would reach every row and
+// a large one would set the unit of p.  Of a sequence's rows, whose windows overlap, exactly
+// the keys some row sees; of the shared keys, which are all stored, perhaps more.  The
+// arguments are the same in all lanes.
+__device__ __forceinline__ AttnSeen seen_by_any(const AttnArgs& A, int min_pos, int max_pos, int max_len, int max_pfx, int part_hi) {
+  AttnSeen s;
+  s.below = min(max_len, part_hi);
+  s.pfx = min(max_pfx, s.below);
+  if (A.causal) s.below = min(s.below, max_pos + 1);
+  s.above = A.window > 0 ? min_pos - (int)A.window : -1;
+  return {__builtin_amdgcn_readfirstlane(s.above), __builtin_amdgcn_readfirstlane(s.below), __builtin_amdgcn_readfirstlane(s.pfx)};
+}
 // by bits, not by branches: a select per score
 __device__ __forceinline__ bool sees(const AttnSeen& s, int part_lo, int key) {
   return (key >= part_lo) & (((key > s.above) & (key < s.below)) | (key < s.pfx));
+}
+
+// eight scales of keys key .. key+7: those that `s` does not hold count as zero
+__device__ __forceinline__ void only_seen(u32x4& d, const AttnSeen& s, int part_lo, int key) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    d[k] &= (sees(s, part_lo, key + 2 * k) ? 0xFFFFu : 0u) | (sees(s, part_lo, key + 2 * k + 1) ? 0xFFFF0000u : 0u);
 }
 
 __device__ __forceinline__ int page_at(const int32_t* row, int col, int cols, int n_pages) {
@@ -442,7 +462,7 @@ attn_step_kernel(AttnArgs A) {
   f32x4 o[2 * NB];
 #pragma unroll
   for (int i = 0; i < 2 * NB; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int end = min(max_len, part_hi);   // slots from here on may hold anything
+  const AttnSeen any = seen_by_any(A, min_pos, max_pos, max_len, max_pfx, part_hi);
 
   // Each load goes out as soon as its registers are free, a step (of this wave) ahead;
   // behind the last step the last one is loaded again (a branch around the loads costs
@@ -453,16 +473,14 @@ attn_step_kernel(AttnArgs A) {
     const int kg = key0 + 16 * g;
     const bool all = key0 >= part_lo && last < min(min_len, part_hi) &&
                      (((!A.causal || last <= min_pos) && (!A.window || key0 > max_pos - (int)A.window)) || last < min_pfx);
-    // scales through LDS (the wave's own); those of slots past the sequence count as zero
+    // by some row; expected, so that the masks stay behind a branch (in every step: batch 83 us for 80)
+    const bool all_seen = key0 >= part_lo && key0 > any.above && last < any.below;
+    // scales through LDS (the wave's own); those of keys that no row sees count as zero
     uint32_t top_d = 0;
 #pragma unroll
     for (int n = 0; n < SL; ++n) {
-      const int p = lane + 64 * n, key = key0 + my_s;
-      if (last >= end) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          sc[n][k] &= (key + 2 * k < end ? 0xFFFFu : 0u) | (key + 2 * k + 1 < end ? 0xFFFF0000u : 0u);
-      }
+      const int p = lane + 64 * n;
+      if (__builtin_expect(!all_seen, 0)) only_seen(sc[n], any, part_lo, key0 + my_s);
       if (p >= NB * 8) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) top_d = max(top_d, max(sc[n][k] & 0x7FFFu, (sc[n][k] >> 16) & 0x7FFFu));
@@ -865,7 +883,7 @@ attn_tile_kernel(AttnArgs A) {
       sc = *(const u32x4*)(src + 2 * (b * A.page + (kk & page_mask)));
     }
   };
-  const int end = min(w_max_len, part_hi);   // slots from here on may hold anything
+  const AttnSeen any = seen_by_any(A, w_min_pos, w_max_pos, w_max_len, w_max_pfx, part_hi);
   const auto commit = [&](int buf, int key0) {
     const auto [tid, lane, j, kg_, vg_] = my_part();
     const int r = (j >> 4) * 4 + (j & 3), t = (j >> 2) & 3;   // key j's row and tile
@@ -925,12 +943,11 @@ attn_tile_kernel(AttnArgs A) {
     if (wave == 0) {
       const int kk = key0 + 8 * (lane & 7), b = lane >> 3;
       uint32_t top = 0;
+      const bool all_seen = key0 >= part_lo && key0 > any.above && key0 + ATTN_STEP <= any.below;   // by some row
+      if (__builtin_expect(!all_seen, 0)) only_seen(sc, any, part_lo, kk);
       if (lane < NB * 8) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sc[k] &= (kk + 2 * k < end ? 0xFFFFu : 0u) | (kk + 2 * k + 1 < end ? 0xFFFF0000u : 0u);
-          top = max(top, max(sc[k] & 0x7FFFu, (sc[k] >> 16) & 0x7FFFu));
-        }
+        for (int k = 0; k < 4; ++k) top = max(top, max(sc[k] & 0x7FFFu, (sc[k] >> 16) & 0x7FFFu));
       }
       top = wave_umax(top);
       if (lane == 0) L.vmax[buf] = top;
