@@ -8,7 +8,7 @@
 namespace ftk {
 
 // One row's parts into its output: with M = max m, o = sum exp2(m - M) o_part / sum
-// exp2(m - M) l.  A wave per row: a lane per part for m and l, then D / 4 lanes per part
+// exp2(m - M) l; a part whose l is NaN makes the row NaN.  A wave per row: a lane per part for m and l, then D / 4 lanes per part
 // and 64 / (D / 4) parts at a time for o, added up in an order of their own, so the
 // result does not depend on which part was done first.  Bound by the latency of the
 // loads: all of a row's (m, l) go out at once, then four rounds of parts (31 parts of 80
@@ -41,9 +41,9 @@ attn_join_kernel(AttnArgs A, int parts) {
   for (int p0 = 0; p0 < parts; p0 += 64) {
     const int p = p0 + lane;
     const f32x2 v = p < parts ? ml[p * A.part_rows + row] : f32x2{NO_MAX, 0.0f};
-    const float m = v[1] > 0.0f ? v[0] : NO_MAX;   // a part without keys wrote no row
+    const float m = v[1] != 0.0f ? v[0] : NO_MAX;   // a part without keys wrote no row
     const float Mn = fmaxf(M, route_val(wave_umax(route_key(m))));
-    const float back = __builtin_amdgcn_exp2f(M - Mn), f = v[1] > 0.0f ? __builtin_amdgcn_exp2f(m - Mn) : 0.0f;
+    const float back = __builtin_amdgcn_exp2f(M - Mn), f = v[1] != 0.0f ? __builtin_amdgcn_exp2f(m - Mn) : 0.0f;
     M = Mn;
     L = L * back + f * v[1];
     x *= back;
@@ -56,7 +56,7 @@ attn_join_kernel(AttnArgs A, int parts) {
         const int at = q0 + u * PG + sub;
         w[u] = __shfl(f, min(at, 63), 64);
         y[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (at < n && sub < PG && w[u] > 0.0f) y[u] = *(const f32x4*)(A.part_o + ((p0 + at) * A.part_rows + row) * D + e);
+        if (at < n && sub < PG && w[u] != 0.0f) y[u] = *(const f32x4*)(A.part_o + ((p0 + at) * A.part_rows + row) * D + e);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) x += w[u] * y[u];
@@ -72,7 +72,7 @@ attn_join_kernel(AttnArgs A, int parts) {
     x[k] = y;
   }
   if (sub != 0) return;
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const float inv = L != 0.0f ? 1.0f / L : 0.0f;
   const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
   kv_store_n<4>(A.ftype, A.out, tok * A.out_token + head * A.out_head + e, A.out_vec, y);
 }

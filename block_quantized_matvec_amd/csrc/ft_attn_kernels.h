@@ -309,18 +309,20 @@ __device__ __forceinline__ int page_at(const int32_t* row, int col, int cols, in
 // q rows as matrix operands: a power of two brings the largest element of a row to [2^10,
 // 2^11), so that an fp16 (and, for fp32 rows, a second one of the remainder) holds every
 // element to 2^-24 of the largest.  A negative scale turns q's sign, so that the scores'
-// factor is positive and their maximum can be taken before it.  Returns the factor (the
-// scale and the power back).
+// factor is positive and their maximum can be taken before it.  A row with an element that is
+// not finite becomes NaN throughout, and so its output, however its keys are split.
+// Returns the factor (the scale and the power back).
 template <int NB, bool LO>
 __device__ __forceinline__ float q_operands(const AttnArgs& A, float (&x)[NB][8], h16x8 (&hi)[NB], h16x8 (&lo)[LO ? NB : 1]) {
-  float amax = 0.0f;
+  uint32_t most = 0;   // the largest magnitude's bits: infinity lies above the numbers, NaN above that
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
-  amax = groups_max(amax);
-  const int ex = amax > 0.0f && amax < INFINITY ? min(max(11 - __builtin_amdgcn_frexp_expf(amax), -120), 120) : 0;
-  const float up = __builtin_ldexpf(A.scale < 0.0f ? -1.0f : 1.0f, ex);
+    for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(x[b][e]) & 0x7FFFFFFFu);
+  most = groups_umax(most);
+  const bool finite = most < 0x7F800000u;
+  const int ex = most > 0 && finite ? min(max(11 - __builtin_amdgcn_frexp_expf(__uint_as_float(most)), -120), 120) : 0;
+  const float up = finite ? __builtin_ldexpf(A.scale < 0.0f ? -1.0f : 1.0f, ex) : NAN;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -624,10 +626,10 @@ attn_step_kernel(AttnArgs A) {
     const int64_t at = A.step_rows ? ((int64_t)sq.seq * A.step_rows + first + r) * A.n_kv_head + hk : (int64_t)out.tok * A.n_head + oh;
     const int64_t ps = (A.split0 + (int)blockIdx.y) * A.part_rows + at;
     if (threadIdx.x % TR == 0) {
-      A.part_ml[2 * ps] = L > 0.0f ? M : NO_MAX;
+      A.part_ml[2 * ps] = L != 0.0f ? M : NO_MAX;
       A.part_ml[2 * ps + 1] = L;
     }
-    if (!(L > 0.0f)) return;   // the join skips it
+    if (L == 0.0f) return;   // no key seen: the join skips it (NaN it takes)
     for (int e = e0; e < D; e += 4 * TR) {
       f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -636,7 +638,7 @@ attn_step_kernel(AttnArgs A) {
     }
     return;
   }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const float inv = L != 0.0f ? 1.0f / L : 0.0f;
   for (int e = e0; e < D; e += 4 * TR) {
     f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -1187,12 +1189,12 @@ attn_tile_kernel(AttnArgs A) {
     if (tok < 0) continue;
     if (A.part_o) {
       const int64_t ps = (A.split0 + split) * A.part_rows + (int64_t)tok * A.n_head + oh;
-      if (g == 0) *(f32x2*)(A.part_ml + 2 * ps) = f32x2{L_ > 0.0f ? m[c] : NO_MAX, L_};
-      if (!(L_ > 0.0f)) continue;
+      if (g == 0) *(f32x2*)(A.part_ml + 2 * ps) = f32x2{L_ != 0.0f ? m[c] : NO_MAX, L_};
+      if (L_ == 0.0f) continue;
 #pragma unroll
       for (int i = 0; i < 2 * NB; ++i) *(f32x4*)(A.part_o + ps * D + 16 * i + 4 * g) = o[c][i];
     } else {
-      const float inv = L_ > 0.0f ? 1.0f / L_ : 0.0f;
+      const float inv = L_ != 0.0f ? 1.0f / L_ : 0.0f;
 #pragma unroll
       for (int i = 0; i < 2 * NB; ++i) {
         const float y[4] = {o[c][i][0] * inv, o[c][i][1] * inv, o[c][i][2] * inv, o[c][i][3] * inv};

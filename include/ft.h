@@ -347,7 +347,8 @@ ft_status ft_kv_load(const ft_kv_cache* cache, const int64_t* slots, int64_t t, 
      if j < kv_len and (j <= p, unless `bidirectional`) and (j > p - window, with a window),
      or if j < kv_len and j < prefix_len[i] (a prefix that all see: prompt or sink tokens).
    score = scale * q.k; with softcap c, c * tanh(score / c); with slopes, - slopes[head] *
-   |p - j|; out = softmax over the visible keys times v, zeros where there is none.
+   |p - j|; out = softmax over the visible keys times v, zeros where there is none.  A row of
+   q with a NaN or an infinity gives NaN (zeros where it sees no key), and no other row does.
    Tokens of no sequence (before q_start[0], from q_start[n_seq] on) are left as they were.
    n_shared > 0: the first n_shared keys (a multiple of page_size) of every sequence are
    the pages of table row 0, read once for all sequences; the result is the same up to
