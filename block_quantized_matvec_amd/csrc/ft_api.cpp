@@ -73,6 +73,16 @@ ft_status pool_get(hipStream_t st, size_t bytes, void** out) {
   return FT_OK;
 }
 
+// the pool as it is
+size_t pool_size(hipStream_t st, void** out) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 0;
+  std::lock_guard<std::mutex> lk(g_pool_mu);
+  const Pool& p = g_pools[{dev, st}];
+  *out = p.ptr;
+  return p.size;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // scratch layout of ft_moe_q_vec
@@ -404,7 +414,7 @@ size_t ft_attn_kv_scratch_bytes(const ft_kv_cache* cache, int64_t n_tok, int64_t
   size_t most = 0;
   for (const int type : {FT_F32, FT_F16, FT_BF16}) {   // the split depends on the type
     a.ftype = type;
-    most = std::max(most, ftk_attn_plan(a).scratch);
+    most = std::max(most, ftk_attn_plan(a).scratch_most);
   }
   return align256(most);
 }
@@ -452,17 +462,26 @@ ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int
   a.table = table;
   a.table_ld = table_ld;
   a.cols = (int)n_col;
-  const AttnPlan p = ftk_attn_plan(a);
+  AttnPlan p = ftk_attn_plan(a);
   // launches of under 2^32 threads (512 a tile, 64 a row of a join)
-  for (const AttnSplit& x : {p.shared, p.tile, p.step})
-    if (x.tiles * a.n_kv_head >= (1 << 23) || x.n_split > 65535) return FT_ERR_SHAPE;
-  if (p.scratch && std::max(n_tok * n_head, p.step_rows * n_seq * cache->n_kv_head) >= (1 << 26)) return FT_ERR_SHAPE;
+  const auto too_large = [&] {
+    for (const AttnSplit& x : {p.shared, p.tile, p.step})
+      if (x.tiles * a.n_kv_head >= (1 << 23) || x.n_split > 65535) return true;
+    return p.scratch && std::max(n_tok * n_head, p.step_rows * n_seq * cache->n_kv_head) >= (1 << 26);
+  };
+  if (too_large()) return FT_ERR_SHAPE;
   void* base = o.workspace;
-  if (p.scratch && base && o.workspace_bytes < p.scratch) return FT_ERR_NO_SCRATCH;
+  size_t room_bytes = o.workspace_bytes;
   if (p.scratch && !base) {
     s = pool_get(hs(stream), align256(p.scratch), &base);
-    if (s != FT_OK) return s;
+    if (s == FT_ERR_NO_SCRATCH) room_bytes = pool_size(hs(stream), &base);
+    else if (s != FT_OK) return s;
+    else room_bytes = p.scratch;
   }
+  // many rows do with fewer splits, down to none: so the size for a larger max_kv is enough
+  while (p.scratch > room_bytes && p.tile.n_split > 1) p = ftk_attn_plan(a, p.tile.n_split - 1);
+  if (p.scratch > room_bytes) return FT_ERR_NO_SCRATCH;
+  if (too_large()) return FT_ERR_SHAPE;
   return hip_status(ftk_launch_attn(a, p, base, hs(stream)));
 }
 

@@ -112,7 +112,8 @@ static AttnSplit split_keys(const AttnArgs& a, int64_t tiles, int64_t steps, int
   const int64_t n = std::max<int64_t>(1, std::min<int64_t>({(want + wgs - 1) / wgs, (steps + least - 1) / least, most}));
   int64_t per = (steps + n - 1) / n;
   per = std::max<int64_t>(least, (per + waves - 1) / waves * waves);
-  return {tiles, (int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per, 0};
+  // n grows with the steps; the splits it comes to do not always
+  return {tiles, (int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per, 0, (int)n};
 }
 
 // Time of the tile kernel with n splits of `per` steps, in steps of one CU (256 rows, 64
@@ -133,7 +134,7 @@ static double tile_cost(const AttnArgs& a, int prec, int wide, int64_t wgs, int6
   return ((double)per + 2) * std::max(load * rate, two ? 0.7 * pair : 1.0) + join;
 }
 
-AttnPlan ftk_attn_plan(const AttnArgs& a) {
+AttnPlan ftk_attn_plan(const AttnArgs& a, int most_tile) {
   using namespace ftk;
   AttnPlan p = {};
   constexpr int kStepRows = 32;
@@ -159,7 +160,7 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
       double seen = 1.0;
       if (!shared && a.causal && !a.prefix_len)
         seen -= 0.5 * std::min(n_rows / (64.0 * a.group * seqs), (double)n_steps) / n_steps;
-      for (int64_t n = 1, per; n <= n_steps; n = (n_steps + per - 2) / (per - 1)) {
+      for (int64_t n = 1, per; n <= n_steps && (shared || n <= most_tile); n = (n_steps + per - 2) / (per - 1)) {
         per = (n_steps + n - 1) / n;
         const double cost = tile_cost(a, prec, wide, filled * a.n_kv_head, n, per, seen);
         if (best.tiles == 0 || cost < best_cost) {
@@ -185,7 +186,7 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
   else if (!many) p.step = step_split(rows / 16 + a.n_seq);
   // few workgroups with a block for each of eight waves: no split, no join (one user, 250
   // keys: 9.2 us against 11.7; with two rounds, 777 keys, 13.8 against 11.2)
-  const AttnSplit whole = {rows / 16 + a.n_seq, 1, (int)steps(16), 0};
+  const AttnSplit whole = {rows / 16 + a.n_seq, 1, (int)steps(16), 0, p.step.most};
   if (!many && !a.n_shared && a.dim <= 128 && p.step.n_split > 1 && whole.tiles * a.n_kv_head <= 256 && whole.split_steps <= 9) {
     p.step = whole;
     p.eight = 1;
@@ -194,7 +195,7 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
   // launched (three prompts of 130 to 200 tokens: 23.3 us against 25.0; with 64 steps and a
   // short sequence among eight, 79 against 65 the other way)
   if (p.step_rows && a.dim <= 128 && p.step.n_split > 1 && steps(16) <= 16) {
-    p.step = {p.step.tiles, 1, (int)steps(16), 0};
+    p.step = {p.step.tiles, 1, (int)steps(16), 0, p.step.most};
     p.eight = 1;
   }
   if (a.n_shared > 0) {
@@ -202,11 +203,15 @@ AttnPlan ftk_attn_plan(const AttnArgs& a) {
     p.shared = p.shared_tile ? tiles(rows, 1, true) : split_keys(a, (rows + 15) / 16, a.n_shared / 64 + 1, 512, 4, 4);
   }
   const int64_t all = (int64_t)a.n_tok * a.n_head;
-  const int64_t parts = p.shared.n_split + (p.step_rows ? p.tile.n_split : p.tile.n_split + p.step.n_split);
-  if (parts > 1) p.scratch = (size_t)(parts * all * part);
-  p.step_at = (p.scratch + 255) & ~(size_t)255;
-  if (p.step_rows && p.step.n_split > 1)
-    p.scratch = p.step_at + (size_t)((int64_t)p.step.n_split * a.n_seq * kStepRows * a.n_kv_head * part);
+  const auto scratch = [&](int step_split) {
+    const int64_t parts = p.shared.n_split + p.tile.n_split + (p.step_rows ? 0 : step_split);
+    size_t n = parts > 1 ? (size_t)(parts * all * part) : 0;
+    p.step_at = (n + 255) & ~(size_t)255;
+    if (p.step_rows && step_split > 1) n = p.step_at + (size_t)((int64_t)step_split * a.n_seq * kStepRows * a.n_kv_head * part);
+    return n;
+  };
+  p.scratch_most = scratch(p.step.most);
+  p.scratch = scratch(p.step.n_split);   // and step_at
   return p;
 }
 

@@ -186,15 +186,18 @@ struct AttnArgs {
 struct AttnSplit {
   int64_t tiles;
   int n_split, split_steps, wide;
+  int most;                // few rows: n_split for these steps or fewer
 };
 struct AttnPlan {
   AttnSplit shared, tile, step;   // tiles 0: no such launch
   int shared_tile;         // the shared part runs on the tile kernel
   int step_rows, eight;
   size_t scratch;          // bytes of partial results; 0: none
+  size_t scratch_most;     // no smaller, and what a plan for a smaller max_kv does with (its tile kernel's splits limited)
   size_t step_at;          // byte offset of the step kernel's, with step_rows
 };
-AttnPlan ftk_attn_plan(const AttnArgs& a);
+// most_tile: a limit of the tile kernel's splits of the sequences' own keys
+AttnPlan ftk_attn_plan(const AttnArgs& a, int most_tile = INT32_MAX);
 hipError_t ftk_launch_attn(AttnArgs a, const AttnPlan& p, void* scratch, hipStream_t st);
 hipError_t ftk_attn_d64(const AttnArgs& a, hipStream_t st);
 hipError_t ftk_attn_d96(const AttnArgs& a, hipStream_t st);

@@ -467,7 +467,8 @@ def kv_load(cache: KvCache, slots: torch.Tensor, dtype=torch.float32, k: torch.T
 
 def attn_kv_scratch_bytes(cache: KvCache, n_tok: int, n_head: int, n_seq: int, max_kv: int, causal: bool = True,
                           window: int = 0, prefix: bool = False, n_shared: int = 0) -> int:
-    """Bytes of a workspace for attn_kv at these sizes (prefix: a prefix_len will be given)."""
+    """Bytes of a workspace that is enough for attn_kv at these sizes and any smaller max_kv (prefix: a prefix_len will
+    be given).  A smaller batch can take more: a workspace for several takes the largest of their sizes."""
     o = _AttnOpts(0.0, 0.0, not causal, window, None, 1 if prefix else None, n_shared, None, 0)
     return lib().ft_attn_kv_scratch_bytes(cache._ref, n_tok, n_head, n_seq, max_kv, ctypes.byref(o))
 

@@ -377,7 +377,11 @@ ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int
                      int64_t n_tok, int64_t n_head, const int32_t* q_start, const int32_t* kv_len,
                      const int32_t* table, int64_t table_ld, int64_t n_col, int64_t n_seq, int64_t max_kv, void* out,
                      int64_t out_token, int64_t out_head, const ft_attn_opts* opts, ft_stream_t stream);
-/* scratch bytes ft_attn_kv needs for these sizes and options, whatever the type */
+/* Scratch bytes that are enough for ft_attn_kv with these sizes and options, whatever the type
+   and the table's width, and with any smaller max_kv (calls of many query rows per sequence then
+   split their keys as far as the scratch goes).  Another number of tokens or sequences has a size
+   of its own, a smaller batch sometimes a larger one, as its keys are split further: scratch for
+   several batches takes the largest of their sizes. */
 size_t ft_attn_kv_scratch_bytes(const ft_kv_cache* cache, int64_t n_tok, int64_t n_head, int64_t n_seq, int64_t max_kv,
                                 const ft_attn_opts* opts);
 
