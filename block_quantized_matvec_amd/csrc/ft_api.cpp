@@ -42,23 +42,38 @@ ft_status hip_status(hipError_t e) { return e == hipSuccess ? FT_OK : FT_ERR_HIP
 // scratch pool
 // --------------------------------------------------------------------------
 struct Pool {
+  std::mutex use;   // held from a call's look-up until its last launch is enqueued
   void* ptr = nullptr;
   size_t size = 0;
   std::vector<void*> retired;
 };
+// A stream orders what is enqueued on it, but two host threads that call on one stream may
+// enqueue their launches in turn, and one would read what the other's wrote to the pool.  So a
+// call that uses the pool holds it until it has enqueued everything.
+using PoolUse = std::unique_lock<std::mutex>;
 std::mutex g_pool_mu;
 // by device too: every device has the null stream
 std::map<std::pair<int, hipStream_t>, Pool> g_pools;
 
-ft_status pool_get(hipStream_t st, size_t bytes, void** out) {
+Pool* pool_hold(hipStream_t st, PoolUse& use) {
   int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return FT_ERR_HIP;
-  std::lock_guard<std::mutex> lk(g_pool_mu);
-  Pool& p = g_pools[{dev, st}];
-  if (p.size >= bytes) {
-    *out = p.ptr;
-    return FT_OK;
+  if (hipGetDevice(&dev) != hipSuccess) return nullptr;
+  Pool* p;
+  {
+    std::lock_guard<std::mutex> lk(g_pool_mu);
+    p = &g_pools[{dev, st}];   // entries stay where they are
   }
+  use = PoolUse(p->use);
+  return p;
+}
+
+ft_status pool_get(hipStream_t st, size_t bytes, void** out, PoolUse& use, size_t* held = nullptr) {
+  Pool* pool = pool_hold(st, use);
+  if (!pool) return FT_ERR_HIP;
+  Pool& p = *pool;
+  *out = p.ptr;
+  if (held) *held = p.size;
+  if (p.size >= bytes) return FT_OK;
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
   if (hipStreamIsCapturing(st, &cs) != hipSuccess) return FT_ERR_HIP;
   if (cs != hipStreamCaptureStatusNone) return FT_ERR_NO_SCRATCH;
@@ -70,17 +85,8 @@ ft_status pool_get(hipStream_t st, size_t bytes, void** out) {
   p.ptr = np;
   p.size = want;
   *out = np;
+  if (held) *held = want;
   return FT_OK;
-}
-
-// the pool as it is
-size_t pool_size(hipStream_t st, void** out) {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 0;
-  std::lock_guard<std::mutex> lk(g_pool_mu);
-  const Pool& p = g_pools[{dev, st}];
-  *out = p.ptr;
-  return p.size;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -294,10 +300,11 @@ ft_status ft_mul_mat_vec_q(ft_type w, const void* W, int64_t n, int64_t k, ft_ty
   if (!W || !xq || !y) return FT_ERR_INVALID_ARG;
   if (k == 0) return FT_ERR_SHAPE;
   if (!aligned16(W) || !aligned16(xq) || !aligned16(y)) return FT_ERR_ALIGNMENT;
+  PoolUse use;
   if (act == FT_Q8_0) {   // the Q8_1 layout of the same blocks, in the stream's pool
     void* rp = nullptr;
     const int64_t nblk = t * (k / 32);
-    const ft_status ps = pool_get(hs(stream), align256((size_t)nblk * 36), &rp);
+    const ft_status ps = pool_get(hs(stream), align256((size_t)nblk * 36), &rp, use);
     if (ps != FT_OK) return ps;
     const hipError_t e = ftk_launch_repack_q8_0(xq, nblk, rp, hs(stream));
     if (e != hipSuccess) return FT_ERR_HIP;
@@ -472,11 +479,10 @@ ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int
   if (too_large()) return FT_ERR_SHAPE;
   void* base = o.workspace;
   size_t room_bytes = o.workspace_bytes;
+  PoolUse use;
   if (p.scratch && !base) {
-    s = pool_get(hs(stream), align256(p.scratch), &base);
-    if (s == FT_ERR_NO_SCRATCH) room_bytes = pool_size(hs(stream), &base);
-    else if (s != FT_OK) return s;
-    else room_bytes = p.scratch;
+    s = pool_get(hs(stream), align256(p.scratch), &base, use, &room_bytes);
+    if (s != FT_OK && s != FT_ERR_NO_SCRATCH) return s;
   }
   // many rows do with fewer splits, down to none: so the size for a larger max_kv is enough
   while (p.scratch > room_bytes && p.tile.n_split > 1) p = ftk_attn_plan(a, p.tile.n_split - 1);
@@ -674,13 +680,13 @@ ft_status moe_run(ft_type w, const void* w_gate, const void* w_up, const void* w
 static __device__ __align__(256) uint8_t scratch[FT_NOALLOC_SCRATCH_BYTES];
 
 constexpr int kMaxDevices = 64;
-std::mutex g_static_mu;
+std::mutex g_static_use[kMaxDevices];   // held as a pool's is
 void* g_static_ptr[kMaxDevices] = {};
 
-ft_status static_scratch(void** out) {
+ft_status static_scratch(void** out, PoolUse& use) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return FT_ERR_HIP;
-  std::lock_guard<std::mutex> lk(g_static_mu);
+  use = PoolUse(g_static_use[dev]);
   if (!g_static_ptr[dev]) {
     void* p = nullptr;
     if (hipGetSymbolAddress(&p, HIP_SYMBOL(scratch)) != hipSuccess || !p) return FT_ERR_HIP;
@@ -707,7 +713,8 @@ ft_status ft_moe_q_vec(ft_type w, const void* w_gate, const void* w_up, const vo
   if (s != FT_OK || t == 0) return s;
   hipStream_t st = hs(stream);
   void* base = nullptr;
-  s = pool_get(st, need, &base);
+  PoolUse use;
+  s = pool_get(st, need, &base, use);
   if (s != FT_OK) return s;
   return moe_run(w, w_gate, w_up, w_down, n_expert, hidden, inter, act, x, t, expert_ids, expert_w, topk, y, o,
                  tiles, (uint8_t*)base, st);
@@ -726,7 +733,8 @@ ft_status ft_moe_q_vec_noalloc(ft_type w, const void* w_gate, const void* w_up, 
   if (s != FT_OK || t == 0) return s;
   if (need > (size_t)FT_NOALLOC_SCRATCH_BYTES) return FT_ERR_SHAPE;
   void* base = nullptr;
-  s = static_scratch(&base);
+  PoolUse use;
+  s = static_scratch(&base, use);
   if (s != FT_OK) return s;
   return moe_run(w, w_gate, w_up, w_down, n_expert, hidden, inter, act, x, t, expert_ids, expert_w, topk, y, o,
                  tiles, (uint8_t*)base, hs(stream));
@@ -745,7 +753,8 @@ ft_status ft_grouped_gemm_q(ft_type w, const void* W, int64_t n_expert, int64_t 
   hipStream_t st = hs(stream);
   const SortScratch L = sort_layout(n_expert, t, topk, xf8_bytes_of(w, x_per_pair ? t * topk : t, k));
   void* base = nullptr;
-  ft_status s = pool_get(st, L.total, &base);
+  PoolUse use;
+  ft_status s = pool_get(st, L.total, &base, use);
   if (s != FT_OK) return s;
   uint8_t* b = (uint8_t*)base;
   GroupedArgs a = {};
@@ -779,10 +788,11 @@ ft_status ft_debug_block_dots(ft_type w, const void* W, int64_t n, int64_t k, ft
   if (n == 0 || t == 0 || k == 0) return FT_OK;
   if (!W || !xq || !partials) return FT_ERR_INVALID_ARG;
   if (!aligned16(W) || !aligned16(xq)) return FT_ERR_ALIGNMENT;
+  PoolUse use;
   if (act == FT_Q8_0) {   // as the matvec: the Q8_1 layout of the same blocks
     void* rp = nullptr;
     const int64_t nblk = t * (k / 32);
-    const ft_status ps = pool_get(hs(stream), align256((size_t)nblk * 36), &rp);
+    const ft_status ps = pool_get(hs(stream), align256((size_t)nblk * 36), &rp, use);
     if (ps != FT_OK) return ps;
     const hipError_t e = ftk_launch_repack_q8_0(xq, nblk, rp, hs(stream));
     if (e != hipSuccess) return FT_ERR_HIP;
@@ -805,7 +815,8 @@ ft_status ft_debug_ceiling(int which, const void* buf, int64_t bytes, int64_t it
 
 ft_status ft_scratch_reserve(ft_stream_t stream, size_t bytes) {
   void* p = nullptr;
-  return pool_get(hs(stream), bytes, &p);
+  PoolUse use;
+  return pool_get(hs(stream), bytes, &p, use);
 }
 
 void ft_shutdown(void) {

@@ -37,7 +37,9 @@
  *    is enqueued.  Out-of-range expert ids and non-finite inputs are outside
  *    the contract (results undefined, never a memory fault: ids are clamped).
  *  - Calls on different streams may run concurrently; calls that share a
- *    stream's scratch pool are ordered by that stream.
+ *    stream's scratch pool are ordered by that stream, from however many host
+ *    threads they come (a call holds the pool until it has enqueued its work).
+ *    Scratch that a caller gives (ft_attn_opts.workspace) is the caller's to order.
  */
 #ifndef FT_H
 #define FT_H
