@@ -1182,6 +1182,7 @@ attn_tile_kernel(AttnArgs A) {
     }
   }
 
+  wave_lds_sync();   // s_tok and s_head, also of a workgroup that has no step and so no barrier
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     const float L_ = groups_sum(l[c]);
