@@ -90,7 +90,7 @@ __device__ __forceinline__ uint32_t kv_quantize(const float (&v)[8], int l4, uin
     d = h2f(dh);
     kv_codes<-127, 127>(v, d, a, u);
   } else {
-    float m = v[0];
+    float m = v[0] == v[0] ? v[0] : 0.0f;   // a NaN has no magnitude; behind the first it is never the larger
 #pragma unroll
     for (int j = 1; j < 8; ++j) m = fabsf(v[j]) > fabsf(m) ? v[j] : m;
     // of two of equal magnitude the lower lane's stands first
