@@ -66,11 +66,11 @@ __device__ __forceinline__ float capped_score(float x, float cap) {
 }
 
 // from a product of operands to what capped_score takes, or to the score in powers of two;
-// finite, as a product may be 0
+// finite, as a product may be 0, and not 0, as a masked score is -inf
 template <bool EXACT>
 __device__ __forceinline__ float score_factor(float c, float softcap) {
   const float f = softcap > 0.0f ? c / softcap * (EXACT ? 1.0f : 2.0f * LOG2E) : c * LOG2E;
-  return fminf(f, 3.0e38f);
+  return fminf(fmaxf(f, 0x1p-126f), 3.0e38f);
 }
 
 // two fp16 numbers of a word (by value: a bit cast of a vector's element would read the
