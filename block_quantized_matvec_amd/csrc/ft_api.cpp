@@ -225,7 +225,7 @@ ft_status attn_sizes(const ft_kv_cache* c, int64_t n_tok, int64_t n_head, int64_
   a->n_seq = (int)n_seq;
   a->max_kv = (int)max_kv;
   a->scale = o.scale != 0.0f ? o.scale : 1.0f / std::sqrt((float)c->head_dim);
-  a->softcap = o.softcap;
+  a->softcap = std::min(o.softcap, 1e30f);   // in powers of two it stays finite; no score comes near it
   a->causal = !o.bidirectional;
   a->window = std::min<int64_t>(o.window, 1 << 30);
   a->slopes = o.slopes;

@@ -139,7 +139,7 @@ AttnPlan ftk_attn_plan(const AttnArgs& a, int most_tile) {
   AttnPlan p = {};
   constexpr int kStepRows = 32;
   const int64_t rows = (int64_t)a.n_tok * a.group;
-  const int prec = a.ftype == FT_F32 ? PREC_F32 : a.ftype == FT_F16 ? PREC_F16 : PREC_BF16;
+  const int prec = attn_prec(a);
   // under a causal window a tile sees the window of its tokens only
   const auto steps = [&](int64_t tile) {
     int64_t span = a.max_kv - a.n_shared;

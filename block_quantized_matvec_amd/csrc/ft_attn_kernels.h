@@ -46,9 +46,9 @@ __device__ __forceinline__ int row_max(int v) { return -row_min(-v); }
 
 // c * tanh(x / c) in the units of `cap`; x comes divided by c, without EXACT times 2 log2(e).
 // EXACT: an odd series below 0.35 (its next term is under 2^-26 of the result), else
-// 1 - 2 / (exp(2x) + 1), within 2^-22.6 absolute; without EXACT the latter throughout
-// (its absolute error is what matters to a score, and 2^-22 * c is far below the
-// rounding of 16-bit probabilities).
+// 1 - 2 / (exp(2x) + 1), within 2^-22.6 absolute; without EXACT the latter throughout,
+// which takes 2^-22 c from a score: up to WIDE_CAP under a quarter of what rounding a
+// probability to fp16 does.
 template <bool EXACT>
 __device__ __forceinline__ float capped_score(float x, float cap) {
   const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(EXACT ? x * (2.0f * LOG2E) : x) + 1.0f);
@@ -688,6 +688,12 @@ __device__ __forceinline__ h16x8 times(h16x8 a, h16x2 f) {   // by pairs
 }
 
 constexpr int PREC_BF16 = 0, PREC_F16 = 1, PREC_F32 = 2;
+// 16-bit rows under a cap above 512 take the fp32 rows' kernels (both forms of the cap in the
+// 16-bit kernels cost them registers, and all their calls 2 to 5 %: fp16 prompts 501 -> 526 us)
+constexpr float WIDE_CAP = 512.0f;
+inline int attn_prec(const AttnArgs& a) {
+  return a.ftype == FT_F32 || a.softcap > WIDE_CAP ? PREC_F32 : a.ftype == FT_F16 ? PREC_F16 : PREC_BF16;
+}
 
 // Where lane (g, r) of an operand lies in its 1 KB.  LDS serves a 16-byte access in
 // groups of 16 lanes that take quads 0, 3 of lane group 0 with quads 1, 2 of group 1
@@ -1225,19 +1231,20 @@ static hipError_t tile_launch(const AttnArgs& a, hipStream_t st) {
 
 template <int TK, int TV, int NB>
 static hipError_t attn_launch(const AttnArgs& a, hipStream_t st) {
+  const int prec = attn_prec(a);
   if (a.tile_kernel) {
-    if (a.ftype == FT_F32) return tile_launch<TK, TV, NB, PREC_F32>(a, st);
-    if (a.ftype == FT_F16) return tile_launch<TK, TV, NB, PREC_F16>(a, st);
+    if (prec == PREC_F32) return tile_launch<TK, TV, NB, PREC_F32>(a, st);
+    if (prec == PREC_F16) return tile_launch<TK, TV, NB, PREC_F16>(a, st);
     return tile_launch<TK, TV, NB, PREC_BF16>(a, st);
   }
   const dim3 grid((unsigned)(a.tiles * a.n_kv_head), a.n_split);
   if (NB <= 4 && a.eight) {   // eight waves for a few blocks of keys: one launch, nothing to join
     constexpr int B = NB <= 4 ? NB : 4;
-    if (a.ftype == FT_F32) attn_step_kernel<TK, TV, B, 8, true><<<grid, 512, 0, st>>>(a);
+    if (prec == PREC_F32) attn_step_kernel<TK, TV, B, 8, true><<<grid, 512, 0, st>>>(a);
     else attn_step_kernel<TK, TV, B, 8, false><<<grid, 512, 0, st>>>(a);
     return hipGetLastError();
   }
-  if (a.ftype == FT_F32) attn_step_kernel<TK, TV, NB, 4, true><<<grid, 256, 0, st>>>(a);
+  if (prec == PREC_F32) attn_step_kernel<TK, TV, NB, 4, true><<<grid, 256, 0, st>>>(a);
   else attn_step_kernel<TK, TV, NB, 4, false><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }

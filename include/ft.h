@@ -357,7 +357,8 @@ ft_status ft_kv_load(const ft_kv_cache* cache, const int64_t* slots, int64_t t, 
    fp32 rounding.
    fp32: products of fp16 pairs summed in fp32, about fp32 accuracy; fp16: the
    probabilities times V's scales are rounded to fp16, everything else as for fp32; bf16:
-   with many query tokens the keys and the probabilities are rounded to fp16 too.
+   with many query tokens the keys and the probabilities are rounded to fp16 too.  With a cap
+   above 512 every type is computed as fp32 is; a cap above 1e30 counts as 1e30.
    Page ids outside the pool are clamped.  Refused as too large: n_tok > 2^24, n_seq > 2^20,
    n_head > 1024, max_kv > 2^30, n_tok * G >= 2^30, and more rows than one launch takes
    (n_tok * n_head past 2^30, less where the keys are split).  opts NULL: causal, scale 1/sqrt(head_dim).
