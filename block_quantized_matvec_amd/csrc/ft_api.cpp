@@ -80,7 +80,10 @@ ft_status pool_get(hipStream_t st, size_t bytes, void** out, PoolUse& use, size_
   size_t want = std::max(bytes, 2 * p.size);
   want = (want + ((size_t)1 << 20) - 1) & ~(((size_t)1 << 20) - 1);
   void* np = nullptr;
-  if (hipMalloc(&np, want) != hipSuccess) return FT_ERR_HIP;
+  if (hipMalloc(&np, want) != hipSuccess) {
+    (void)hipGetLastError();   // told by the status; the next launch's check would find it again
+    return FT_ERR_HIP;
+  }
   if (p.ptr) p.retired.push_back(p.ptr);  // work already enqueued may still use it
   p.ptr = np;
   p.size = want;
