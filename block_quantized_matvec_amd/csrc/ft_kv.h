@@ -40,10 +40,6 @@ __host__ __device__ constexpr int kv_head_bytes(int type, int dim, int page) {
 template <int T> struct KvCodes;
 template <> struct KvCodes<FT_Q8_0> { static constexpr int GROUP = 2, CB = 8; };   // blocks per group, bytes per 8 codes
 template <> struct KvCodes<FT_Q4_0> { static constexpr int GROUP = 4, CB = 4; };
-template <int T, int NB>
-__host__ __device__ constexpr int kv_group_blocks(int p) {
-  return NB - p * KvCodes<T>::GROUP < KvCodes<T>::GROUP ? NB - p * KvCodes<T>::GROUP : KvCodes<T>::GROUP;
-}
 // byte of the first of codes 8g .. 8g+7 of block b of key j
 template <int T, int NB>
 __host__ __device__ inline int kv_k_at(int page, int j, int b, int g) {
