@@ -339,13 +339,17 @@ __device__ __forceinline__ float q_operands(const AttnArgs& A, float (&x)[NB][8]
 // meet in LDS at the end, those of splits in attn_join_kernel.  The rows are the query
 // heads of a KV head (and the few tokens of its sequence), so that each code is read once:
 // bound by HBM on long contexts (32 ragged sequences of 512 to 8192 keys, 8 KV heads of
-// 128 in Q8_0: 78 us, 3.9 TB/s; 2 of 100000 to 131071, V in Q4_0: 84 us, 4.6 TB/s, a
-// large copy 5.0), by latency on short ones (777 keys: 8 us and the join's 2.7).  Codes
+// 128 in Q8_0: 79 us with the join, 3.8 TB/s; 2 of 100000 to 131071, V in Q4_0: 84 us, 4.6
+// TB/s; a large copy 5.0), by latency on short ones (777 keys: 8 us and the join's 3).  Codes
 // go from memory to registers in the order of a matrix operand, one step ahead, with no
 // pass through LDS: each is used by one wave only.  K's scale multiplies a block's
 // product, V's the probability, so the codes are exact operands.  Where a load was issued
 // by a branch the compiler spilled and waited (batch 112 -> 176 us): loads past the last
 // step repeat it.
+// Rows of 16 bits round p times V's scale to one fp16: half a step of 2^-11 per term, against
+// the output's own (errors against 64 bits, fp16 outputs: 2.7e-4 of the root mean square, where
+// products in fp32 throughout leave 2.1e-4; bf16 ones 1.7e-3 both).  A pair as fp32 rows have
+// costs 5 to 10 % (batch 72.5 -> 78.4 us, head size 256 186 -> 205).
 // ---------------------------------------------------------------------------
 template <int TK, int TV, int NB, int NW, bool LO>
 __global__ void __launch_bounds__(64 * NW, NB <= 4 || NW > 4 ? 2 : 1)
@@ -654,14 +658,17 @@ attn_step_kernel(AttnArgs A) {
 // The same sums as above; a step's codes become fp16 operands in LDS once for all rows of
 // the workgroup, double buffered, laid out as the matrix unit takes them (operand_slot).
 //   fp32 rows: q and p as pairs of fp16, four products in place of two;
-//   fp16 rows: K's scales on the products, p times V's scale rounded to fp16;
+//   fp16 rows: K's scales on the products, p times V's scale rounded to fp16, as above (a
+//     pair: prompts 513 -> 620 us, head size 256 1020 -> 1240);
 //   bf16 rows: K's scales in the operand (fp16, a power of two per key apart), p and its
-//     product with V's scale in fp16: no fp32 work per block.
-// Bound by vector instructions, not by the matrix unit (busy a quarter of the time): 4096
-// bf16 rows over 16384 keys of 8 heads of 128 take 1318 us, 835 TFLOP/s; ragged causal
-// prompts of 2239 to 4096 tokens 395 us, with a cap 477 us (two exponentials and a
-// reciprocal per score); an fp32 chunk of 1000 tokens over 7000 keys 332 us, 320 TFLOP/s of
-// the result and twice that of fp16 products.
+//     product with V's scale in fp16: no fp32 work per block, and an eighth of the output's
+//     own rounding each.  V's scales are held to 2^-25 of the largest of the 64 keys.
+// Bound by vector instructions, not by the matrix unit (busy a quarter to a third of the
+// time): 4096 bf16 tokens over 16384 keys of 8 heads of 128 take 1290 us, 850 TFLOP/s; ragged
+// causal prompts of 2239 to 4096 tokens 380 to 400 us, with a cap 475 us (two exponentials and
+// a reciprocal per score); an fp32 chunk of 1000 tokens over 7000 keys 300 to 315 us, 345
+// TFLOP/s of the result and twice that of fp16 products.  Figures of two forms below were
+// taken in turn in one run; from run to run these kernels differ by up to 8 %.
 // Two row operands per wave (CT = 2) halve the layout's share for bf16 at head size 128
 // (423 us against 461); fp16 and fp32 rows then spill (1066 us against 535), other head
 // sizes gain nothing.

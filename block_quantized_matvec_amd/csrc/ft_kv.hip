@@ -19,10 +19,11 @@
 //
 // At a decode step both are launch and latency (4 us each).  8192 bf16 tokens of 8 heads
 // of 128, K in Q8_0 and V in Q4_0 (33 MB of rows, 14 MB of cache): reading back 9.3 us,
-// at the rate of a copy; writing 15 us, bound by vector instructions, 170 per eight
-// elements and wave (208, and 18 us, while every value near a half-integer divided; byte
-// writes to LDS in place of the exchange between lanes: 17.6 and 12.6 us).  fp32 rows, twice
-// the bytes: 36 us together, 4.5 TB/s.
+// at the rate of a copy; writing 15 us, of which vector instructions issue for 9, 170 per
+// eight elements and wave, while the waves wait for half of their time (208 instructions, and
+// 18 us, while every value near a half-integer divided; byte writes to LDS in place of the
+// exchange between lanes: 17.6 and 12.6 us).  fp32 rows, twice the bytes: 36 us together,
+// 4.5 TB/s.
 #include "ft_device.h"
 #include "ft_internal.h"
 #include "ft_kv.h"

@@ -10,16 +10,16 @@
 // the last bits of an exponential, and in fp64 it depends on the formula alone (fp32
 // would reorder neighbours by its own rounding).  Almost always fp32 is enough to know
 // that order: route_fast_kernel works in fp32 with a bound of its error, and where two
-// neighbours in the order lie closer than the bound (ties among them) the wave decides
-// that token again in fp64 (route_exact).
+// neighbours in the order lie closer than the bound (ties among them, groups that are equal
+// in fp32) the wave decides that token again in fp64 (route_exact).
 //
 // Bound by instruction issue and the length of a token's chain, not by HBM: 16384 tokens
-// x 256 experts, sigmoid, bias, 8 groups, top 8 (16.8 MB in) take 18.6 us (10.8 us without
-// bias and groups), of which 4 us are the tail of the few tokens that fp64 decides (bf16
-// logits without a bias, where one token in a hundred has three equal ones at the last
-// slot: 17 us); with every exponential in fp64 and a wave per token 33 us.  3 tokens x 128
+// x 256 experts, sigmoid, bias, 8 groups, top 8 (16.8 MB in) take 17 to 18.5 us (10.2 us
+// without bias and groups), of which 4 us are the tail of the few tokens that fp64 decides
+// (bf16 logits without a bias, where one token in a hundred has three equal ones at the last
+// slot: 16.4 us); with every exponential in fp64 and a wave per token 33 us.  3 tokens x 128
 // experts: 4.7 us.  More than 14 slots go to the kernels with more lanes per token (top 16
-// of 1024, 16384 tokens: 43 us; every token in fp64: 126).
+// of 1024, 16384 tokens: 45 us; every token in fp64: 126).
 #include "ft_device.h"
 #include "ft_internal.h"
 #include "ft_kv.h"

@@ -281,7 +281,9 @@ ft_status ft_debug_ceiling(int which, const void* buf, int64_t bytes, int64_t it
    w is rounded to fp32 once.  A logit of -inf has score 0; NaN logits count as -inf
    when experts are chosen.  t <= 2^25, 1 <= topk <= min(32, topk_group * n_expert / n_group),
    n_expert <= 1024, n_group <= 64 and a divisor of n_expert, 1 <= topk_group <=
-   n_group.  opts NULL: softmax, no bias, one group, renorm, scale 1. */
+   n_group.  opts NULL: softmax, no bias, one group, renorm, scale 1.
+   The library's own calls that take ids (ft_moe_sort, ft_moe_q_vec, ft_grouped_gemm_q)
+   take topk up to 8. */
 typedef struct {
   int sigmoid;        /* 0 softmax, 1 sigmoid */
   const float* bias;  /* nullable [n_expert] */
@@ -353,11 +355,13 @@ ft_status ft_kv_load(const ft_kv_cache* cache, const int64_t* slots, int64_t t, 
    q with a NaN or an infinity gives NaN (zeros where it sees no key), and no other row does.
    Tokens of no sequence (before q_start[0], from q_start[n_seq] on) are left as they were.
    n_shared > 0: the first n_shared keys (a multiple of page_size) of every sequence are
-   the pages of table row 0, read once for all sequences; the result is the same up to
-   fp32 rounding.
+   the pages of table row 0, read once for all sequences.  The result is the same up to the
+   roundings of its type named here; which of the kernels (few or many query tokens) reads
+   the shared keys depends on the rows of all sequences together.
    fp32: products of fp16 pairs summed in fp32, about fp32 accuracy; fp16: the
    probabilities times V's scales are rounded to fp16, everything else as for fp32; bf16:
-   with many query tokens the keys and the probabilities are rounded to fp16 too.  With a cap
+   with many query tokens the keys and the probabilities are rounded to fp16 too, and V's
+   scales are held to 2^-25 of the largest of 64 keys.  With a cap
    above 512 every type is computed as fp32 is; a cap above 1e30 counts as 1e30.
    Page ids outside the pool are clamped.  Refused as too large: n_tok > 2^24, n_seq > 2^20,
    n_head > 1024, max_kv > 2^30, n_tok * G >= 2^30, and more rows than one launch takes
