@@ -394,7 +394,12 @@ attn_step_kernel(AttnArgs A) {
   const int min_pfx = row_min(row.pfx), max_pfx = row_max(row.pfx);
   const int part_lo = shared ? 0 : A.n_shared, part_hi = shared ? A.n_shared : A.max_kv;
   const AttnSeen seen = seen_by(A, row, part_hi);
-  const AttnSteps steps = attn_steps(A, part_lo, part_hi, min_pos, max_pos, max_len, max_pfx);
+  AttnSteps steps = attn_steps(A, part_lo, part_hi, min_pos, max_pos, max_len, max_pfx);
+  // the same in all lanes: in scalar registers, which takes back what the masks of unseen keys
+  // cost short calls (16 drafts 17.1 us against 17.6, head size 64 batch in Q4_0 42.0 against
+  // 43.7; the other kernel spills for it: fp16 prompts 514 against 502)
+  steps = {__builtin_amdgcn_readfirstlane(steps.a), __builtin_amdgcn_readfirstlane(steps.n1), __builtin_amdgcn_readfirstlane(steps.c),
+           __builtin_amdgcn_readfirstlane(steps.total)};
   const int s_end = min(steps.total, (split + 1) * per_split);
   const int s0 = split * per_split + wave;
   const int s_last = s0 + (s_end - 1 - s0) / NW * NW;   // this wave's last step (where there is one)
