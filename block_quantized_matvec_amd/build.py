@@ -23,7 +23,7 @@ ARCH = "gfx950"
 SOURCES = ["ft_mmvq_kq.hip", "ft_mmvq_kq_b.hip", "ft_mmvq_kq_c.hip", "ft_mmvq_kq_d.hip", "ft_mmvq_q8k.hip", "ft_mmvq.hip",
            "ft_api.cpp", "ft_quant.hip", "ft_mmvq_mfma.hip", "ft_moe.hip", "ft_moe_fused.hip", "ft_moe_fp4.hip", "ft_grouped.hip",
            "ft_probe.hip", "ft_kv.hip", "ft_attn.hip", "ft_attn_d64.hip", "ft_attn_d96.hip", "ft_attn_d128.hip",
-           "ft_attn_d256.hip", "ft_route.hip"]
+           "ft_attn_d256.hip", "ft_route.hip", "ft_rope.hip", "ft_norm.hip", "ft_lora.hip"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -37,11 +37,14 @@ CFLAGS = [
     "-I" + os.path.join(ROOT, "include"), "-I" + CSRC,
 ]
 
+# every fp32 operation rounded by itself (the quantized code of a normed or turned element hangs on no pairing)
+EXTRA = {"ft_rope.hip": ["-ffp-contract=off"], "ft_norm.hip": ["-ffp-contract=off"]}
+
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
-    cmd = [HIPCC] + CFLAGS + lang + ["-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC] + CFLAGS + EXTRA.get(src, []) + lang + ["-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")

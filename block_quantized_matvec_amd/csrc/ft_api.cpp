@@ -206,6 +206,34 @@ KvArgs kv_args(const ft_kv_cache* c, ft_float type, void* k, int64_t k_token, in
   return a;
 }
 
+// positions and table of a rotation, and the sizes that its kernels take
+ft_status rope_check(const ft_rotation* r, int64_t t, int64_t heads, int64_t dim, double eps) {
+  if (!r || t < 0 || r->n_pos < 1 || !r->table) return FT_ERR_INVALID_ARG;
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return FT_ERR_INVALID_ARG;
+  if (r->rot_dim < 2 || r->rot_dim > dim || r->rot_dim % 2) return FT_ERR_SHAPE;
+  if (t > ((int64_t)1 << 24) || heads > 1024 || t * heads > ((int64_t)1 << 30) || r->n_pos > ((int64_t)1 << 32)) return FT_ERR_SHAPE;
+  return ((uintptr_t)r->table & 3) ? FT_ERR_ALIGNMENT : FT_OK;
+}
+RopeArgs rope_args(const ft_rotation* r, ft_float type, int64_t t, int64_t dim, double eps) {
+  RopeArgs a = {};
+  a.pos = r->positions;
+  a.table = r->table;
+  a.n_pos = r->n_pos;
+  a.t = t;
+  a.dim = (int)dim;
+  a.rot = (int)r->rot_dim;
+  a.interleaved = r->interleaved != 0;
+  a.ftype = type;
+  a.eps = eps;
+  return a;
+}
+
+ft_status lora_sizes(int64_t t, int64_t k, int64_t n, int64_t n_adapter, int64_t rank) {
+  if (t < 0 || k < 1 || n < 0 || n_adapter < 1 || rank < 1) return FT_ERR_INVALID_ARG;
+  const int64_t most = (int64_t)1 << 20;
+  return t > most || k > most || n > most || rank > 256 || n_adapter > 8192 ? FT_ERR_SHAPE : FT_OK;
+}
+
 // Sizes and options of ft_attn_kv into the arguments that the planner needs.
 ft_status attn_sizes(const ft_kv_cache* c, int64_t n_tok, int64_t n_head, int64_t n_seq, int64_t max_kv,
                      const ft_attn_opts& o, AttnArgs* a) {
@@ -413,6 +441,186 @@ ft_status ft_kv_load(const ft_kv_cache* cache, const int64_t* slots, int64_t t, 
   if (!float_aligned(k, type) || !float_aligned(v, type) || ((uintptr_t)slots & 7)) return FT_ERR_ALIGNMENT;
   const KvArgs a = kv_args(cache, type, k, k_token, k_head, v, v_token, v_head, slots, t);
   return hip_status(ftk_launch_kv(a, true, hs(stream)));
+}
+
+ft_status ft_rope_table(const double* freqs, int64_t half, int64_t n_pos, double scale, float* table,
+                        ft_stream_t stream) {
+  if (half < 1 || n_pos < 0) return FT_ERR_INVALID_ARG;
+  if (half > (1 << 15) || n_pos > ((int64_t)1 << 30) / half) return FT_ERR_SHAPE;
+  if (n_pos == 0) return FT_OK;
+  if (!freqs || !table) return FT_ERR_INVALID_ARG;
+  if (((uintptr_t)freqs & 7) || ((uintptr_t)table & 3)) return FT_ERR_ALIGNMENT;
+  return hip_status(ftk_launch_rope_table(freqs, half, n_pos, scale, table, hs(stream)));
+}
+
+ft_status ft_rope(const ft_rotation* rot, ft_float type, const void* x, int64_t x_token, int64_t x_head, int64_t t,
+                  int64_t n_head, int64_t dim, const float* weight, double eps, void* out, int64_t out_token,
+                  int64_t out_head, ft_stream_t stream) {
+  if (!is_float(type)) return FT_ERR_UNSUPPORTED;
+  if (n_head < 0) return FT_ERR_INVALID_ARG;
+  if (dim < 2 || dim > 512) return FT_ERR_SHAPE;
+  const ft_status s = rope_check(rot, t, n_head, dim, eps);
+  if (s != FT_OK) return s;
+  if (!strides_ok(t, n_head, dim, x_token, x_head) || !strides_ok(t, n_head, dim, out_token, out_head))
+    return FT_ERR_INVALID_ARG;
+  if (t == 0 || n_head == 0) return FT_OK;
+  if (!x || !out || !rot->positions) return FT_ERR_INVALID_ARG;
+  if (x == out && (x_token != out_token || x_head != out_head)) return FT_ERR_INVALID_ARG;
+  if (!float_aligned(x, type) || !float_aligned(out, type) || ((uintptr_t)rot->positions & 3) || ((uintptr_t)weight & 3))
+    return FT_ERR_ALIGNMENT;
+  RopeArgs a = rope_args(rot, type, t, dim, eps);
+  a.q = x;
+  a.q_token = x_token;
+  a.q_head = x_head;
+  a.n_head = (int)n_head;
+  a.q_weight = weight;
+  a.out = out;
+  a.out_token = out_token;
+  a.out_head = out_head;
+  return hip_status(ftk_launch_rope(a, hs(stream)));
+}
+
+ft_status ft_kv_store_rope(const ft_kv_cache* cache, const ft_rotation* rot, ft_float type, const ft_qkv_rows* rows,
+                           const int64_t* slots, int64_t t, ft_stream_t stream) {
+  ft_status s = kv_check(cache);
+  if (s != FT_OK) return s;
+  if (!is_float(type)) return FT_ERR_UNSUPPORTED;
+  if (!rows || rows->n_head < 0) return FT_ERR_INVALID_ARG;
+  const ft_qkv_rows& r = *rows;
+  const int64_t H = cache->n_kv_head, D = cache->head_dim;
+  s = rope_check(rot, t, std::max(H, r.n_head), D, r.eps);
+  if (s != FT_OK) return s;
+  if (!strides_ok(t, H, D, r.k_token, r.k_head) || !strides_ok(t, H, D, r.v_token, r.v_head) ||
+      (r.n_head && (!strides_ok(t, r.n_head, D, r.q_token, r.q_head) || !strides_ok(t, r.n_head, D, r.out_token, r.out_head))))
+    return FT_ERR_INVALID_ARG;
+  if (t == 0) return FT_OK;
+  if (!r.k || !r.v || !slots || !rot->positions || (r.n_head && (!r.q || !r.q_out))) return FT_ERR_INVALID_ARG;
+  if (r.n_head && r.q == r.q_out && (r.q_token != r.out_token || r.q_head != r.out_head)) return FT_ERR_INVALID_ARG;
+  if (!float_aligned(r.k, type) || !float_aligned(r.v, type) || ((uintptr_t)slots & 7) || ((uintptr_t)rot->positions & 3) ||
+      (((uintptr_t)r.q_weight | (uintptr_t)r.k_weight) & 3) || (r.n_head && (!float_aligned(r.q, type) || !float_aligned(r.q_out, type))))
+    return FT_ERR_ALIGNMENT;
+  RopeArgs a = rope_args(rot, type, t, D, r.eps);
+  a.q = r.q;
+  a.q_token = r.q_token;
+  a.q_head = r.q_head;
+  a.n_head = (int)r.n_head;
+  a.q_weight = r.q_weight;
+  a.out = r.q_out;
+  a.out_token = r.out_token;
+  a.out_head = r.out_head;
+  a.kv = kv_args(cache, type, (void*)r.k, r.k_token, r.k_head, (void*)r.v, r.v_token, r.v_head, slots, t);
+  a.k_weight = r.k_weight;
+  return hip_status(ftk_launch_kv_store_rope(a, hs(stream)));
+}
+
+ft_status ft_norm(ft_float type, const void* x, int64_t ldx, int64_t rows, int64_t width, const ft_norm_opts* opts,
+                  ft_stream_t stream) {
+  if (!is_float(type)) return FT_ERR_UNSUPPORTED;
+  if (!opts || rows < 0 || width < 1) return FT_ERR_INVALID_ARG;
+  const ft_norm_opts& o = *opts;
+  const bool quantizes = o.xq != nullptr;
+  if (quantizes && !is_act(o.act)) return FT_ERR_UNSUPPORTED;
+  if (!(o.eps >= 0.0) || !std::isfinite(o.eps) || !std::isfinite(o.scale)) return FT_ERR_INVALID_ARG;
+  if (width > 32768 || rows > ((int64_t)1 << 24) || (quantizes && width % kElems[o.act])) return FT_ERR_SHAPE;
+  if (rows > 0 && !o.r && !o.out && !o.xq) return FT_ERR_INVALID_ARG;
+  if (!o.post && (o.post_weight || o.post_bias)) return FT_ERR_INVALID_ARG;
+  const struct { const void* p; int64_t ld; } side[] = {{x, ldx}, {o.residual, o.ld_residual}, {o.r, o.ld_r}, {o.out, o.ld_out}};
+  for (const auto& a : side)
+    if ((&a == side || a.p) && ((rows > 1 && a.ld < width) || a.ld < 0 || a.ld > ((int64_t)1 << 40))) return FT_ERR_INVALID_ARG;
+  if (o.gate && o.ld_gate != 0 && ((rows > 1 && o.ld_gate < width) || o.ld_gate < 0 || o.ld_gate > ((int64_t)1 << 40)))
+    return FT_ERR_INVALID_ARG;
+  // in place: the row that is written is the row that was read
+  for (int i = 2; i < 4; ++i)
+    for (int j = 0; j < 2; ++j)
+      if (rows > 1 && side[i].p && side[i].p == side[j].p && side[i].ld != side[j].ld) return FT_ERR_INVALID_ARG;
+  if (o.r && o.r == o.out) return FT_ERR_INVALID_ARG;
+  if (rows == 0) return FT_OK;
+  if (!x) return FT_ERR_INVALID_ARG;
+  for (const auto& a : side)
+    if (!float_aligned(a.p, type)) return FT_ERR_ALIGNMENT;
+  if (!float_aligned(o.gate, type) ||
+      (((uintptr_t)o.post_weight | (uintptr_t)o.post_bias | (uintptr_t)o.weight | (uintptr_t)o.bias) & 3) || !aligned16(o.xq))
+    return FT_ERR_ALIGNMENT;
+  NormArgs a = {};
+  a.ftype = type;
+  a.rows = rows;
+  a.width = width;
+  a.x = x;
+  a.ldx = ldx;
+  a.residual = o.residual;
+  a.ld_residual = o.ld_residual;
+  a.gate = o.gate;
+  a.ld_gate = o.ld_gate;
+  a.post = o.post != 0;
+  a.post_weight = o.post_weight;
+  a.post_bias = o.post_bias;
+  a.scale = o.scale == 0.0f ? 1.0f : o.scale;
+  a.layer = o.layer != 0;
+  a.eps = o.eps;
+  a.weight = o.weight;
+  a.bias = o.bias;
+  a.r = o.r;
+  a.ld_r = o.ld_r;
+  a.out = o.out;
+  a.ld_out = o.ld_out;
+  a.act = o.act;
+  a.xq = o.xq;
+  a.xq_row = quantizes ? row_bytes_of(o.act, width) : 0;
+  return hip_status(ftk_launch_norm(a, hs(stream)));
+}
+
+size_t ft_lora_scratch_bytes(int64_t t, int64_t k, int64_t n_adapter, int64_t rank) {
+  if (t < 1 || lora_sizes(t, k, 1, n_adapter, rank) != FT_OK) return 0;
+  return ftk_lora_scratch(t, k, (int)rank, n_adapter);
+}
+
+ft_status ft_lora(ft_float x_type, const void* x, int64_t ldx, int64_t t, int64_t k, ft_float w_type, const void* A,
+                  const void* B, int64_t n_adapter, int64_t rank, int64_t n, const int32_t* ids, const float* y,
+                  int64_t ldy, float* out, int64_t ldo, const ft_lora_opts* opts, ft_stream_t stream) {
+  if (!is_float(x_type) || !is_float(w_type)) return FT_ERR_UNSUPPORTED;
+  ft_status s = lora_sizes(t, k, n, n_adapter, rank);
+  if (s != FT_OK) return s;
+  const int64_t lim = (int64_t)1 << 40;
+  if ((t > 1 && (ldx < k || ldo < n || (y && ldy < n))) || ldx < 0 || ldo < 0 || ldx > lim || ldo > lim ||
+      (y && (ldy < 0 || ldy > lim)))
+    return FT_ERR_INVALID_ARG;
+  if (t > 1 && y && y == out && ldy != ldo) return FT_ERR_INVALID_ARG;
+  ft_lora_opts o = {};
+  if (opts) o = *opts;
+  if (t == 0 || n == 0) return FT_OK;
+  if (!x || !A || !B || !ids || !out) return FT_ERR_INVALID_ARG;
+  if (!float_aligned(x, x_type) || !float_aligned(A, w_type) || !float_aligned(B, w_type) ||
+      (((uintptr_t)ids | (uintptr_t)o.ranks | (uintptr_t)o.scales | (uintptr_t)y | (uintptr_t)out) & 3) || !aligned16(o.workspace))
+    return FT_ERR_ALIGNMENT;
+  const size_t need = ftk_lora_scratch(t, k, (int)rank, n_adapter);
+  void* scratch = o.workspace;
+  PoolUse use;
+  if (scratch) {
+    if (o.workspace_bytes < need) return FT_ERR_NO_SCRATCH;
+  } else {
+    s = pool_get(hs(stream), need, &scratch, use);
+    if (s != FT_OK) return s;
+  }
+  LoraArgs a = {};
+  a.xtype = x_type;
+  a.wtype = w_type;
+  a.x = x;
+  a.ldx = ldx;
+  a.y = y;
+  a.ldy = ldy;
+  a.out = out;
+  a.ldo = ldo;
+  a.a = A;
+  a.b = B;
+  a.ids = ids;
+  a.ranks = o.ranks;
+  a.scales = o.scales;
+  a.t = t;
+  a.k = k;
+  a.n = n;
+  a.adapters = n_adapter;
+  a.rank = (int)rank;
+  return hip_status(ftk_launch_lora(a, scratch, hs(stream)));
 }
 
 size_t ft_attn_kv_scratch_bytes(const ft_kv_cache* cache, int64_t n_tok, int64_t n_head, int64_t n_seq, int64_t max_kv,

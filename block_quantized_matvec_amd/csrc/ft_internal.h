@@ -220,3 +220,67 @@ struct RouteArgs {
   int vec, vec_bias;       // set by the launcher: rows (the bias) in aligned quads
 };
 hipError_t ftk_launch_route_ex(const RouteArgs& a, hipStream_t st);
+
+// rotary positions (ft_rope.hip): rows turned, alone or on the way into the cache
+struct RopeArgs {
+  const int32_t* pos;
+  const float* table;      // [n_pos][rot]
+  int64_t n_pos, t;
+  int dim, rot, interleaved, ftype;
+  double eps;
+  const void* q;           // n_head 0: no rows beside the keys
+  int64_t q_token, q_head;
+  int n_head;
+  const float* q_weight;   // nullable, as k_weight: rows are normed first
+  void* out;
+  int64_t out_token, out_head;
+  KvArgs kv;               // the store's keys, values and cache
+  const float* k_weight;
+};
+hipError_t ftk_launch_rope_table(const double* freqs, int64_t half, int64_t n_pos, double scale, float* table, hipStream_t st);
+hipError_t ftk_launch_rope(const RopeArgs& a, hipStream_t st);
+hipError_t ftk_launch_kv_store_rope(const RopeArgs& a, hipStream_t st);
+
+// norms around a block (ft_norm.hip)
+struct NormArgs {
+  int ftype;
+  int64_t rows, width;     // width <= 32768
+  const void* x;
+  int64_t ldx;
+  const void* residual;    // nullable, as all pointers below
+  int64_t ld_residual;
+  const void* gate;
+  int64_t ld_gate;
+  int post;
+  const float *post_weight, *post_bias;
+  float scale;
+  int layer;
+  double eps;
+  const float *weight, *bias;
+  void* r;
+  int64_t ld_r;
+  void* out;
+  int64_t ld_out;
+  int act;                 // Q8_1, Q8_0 or Q8_K, with xq
+  void* xq;
+  int64_t xq_row;          // bytes
+};
+hipError_t ftk_launch_norm(const NormArgs& a, hipStream_t st);
+
+// low-rank adapters (ft_lora.hip)
+struct LoraArgs {
+  int xtype, wtype;        // ft_float
+  const void* x;
+  int64_t ldx;
+  const float* y;          // nullable
+  int64_t ldy;
+  float* out;              // may be y
+  int64_t ldo;
+  const void *a, *b;
+  const int32_t *ids, *ranks;   // ranks, scales nullable
+  const float* scales;
+  int64_t t, k, n, adapters;
+  int rank;
+};
+size_t ftk_lora_scratch(int64_t t, int64_t k, int rank, int64_t adapters);
+hipError_t ftk_launch_lora(const LoraArgs& a, void* scratch, hipStream_t st);

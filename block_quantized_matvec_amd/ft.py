@@ -8,6 +8,7 @@ fallback: if libft.so is missing or cannot load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch  # loaded first so libft.so binds to the same HIP runtime as torch
@@ -52,6 +53,32 @@ class _AttnOpts(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("bidirectional", ctypes.c_int),
                 ("window", ctypes.c_int64), ("slopes", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
                 ("n_shared", ctypes.c_int64), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int64),
+                ("interleaved", ctypes.c_int)]
+
+
+class _QkvRows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64), ("n_head", ctypes.c_int64),
+                ("q_weight", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("out_token", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("k", ctypes.c_void_p), ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("k_weight", ctypes.c_void_p), ("v", ctypes.c_void_p), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("eps", ctypes.c_double)]
+
+
+class _NormOpts(ctypes.Structure):
+    _fields_ = [("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                ("ld_gate", ctypes.c_int64), ("post", ctypes.c_int), ("post_weight", ctypes.c_void_p),
+                ("post_bias", ctypes.c_void_p), ("scale", ctypes.c_float), ("layer", ctypes.c_int), ("eps", ctypes.c_double),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("r", ctypes.c_void_p), ("ld_r", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("act", ctypes.c_int), ("xq", ctypes.c_void_p)]
+
+
+class _LoraOpts(ctypes.Structure):
+    _fields_ = [("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 _P, _I64 = ctypes.c_void_p, ctypes.c_int64
@@ -102,6 +129,15 @@ EXPORTS = {
                                   _I64, _I64, _I64, _P, _I64, _I64, ctypes.POINTER(_AttnOpts), _P]),
     "ft_attn_kv_scratch_bytes": (ctypes.c_size_t, [ctypes.POINTER(_KvCache), _I64, _I64, _I64, _I64,
                                                    ctypes.POINTER(_AttnOpts)]),
+    "ft_rope_table": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_double, _P, _P]),
+    "ft_rope": (ctypes.c_int, [ctypes.POINTER(_Rotation), ctypes.c_int, _P, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_double, _P,
+                               _I64, _I64, _P]),
+    "ft_kv_store_rope": (ctypes.c_int, [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rotation), ctypes.c_int,
+                                        ctypes.POINTER(_QkvRows), _P, _I64, _P]),
+    "ft_norm": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, ctypes.POINTER(_NormOpts), _P]),
+    "ft_lora": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, ctypes.c_int, _P, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64,
+                               ctypes.POINTER(_LoraOpts), _P]),
+    "ft_lora_scratch_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
     "ft_scratch_reserve": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t]),
     "ft_moe_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                                                ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
@@ -513,4 +549,229 @@ def attn_kv(cache: KvCache, q: torch.Tensor, table: torch.Tensor, kv_len: torch.
           _plain(q_start, "q_start", torch.int32, (n_seq + 1,), dev), _plain(kv_len, "kv_len", torch.int32, (n_seq,), dev),
           table.data_ptr(), ld if n_seq > 1 else cols, cols, n_seq,
           cols * cache.page_size if max_kv is None else max_kv, out.data_ptr(), os_[0], os_[1], ctypes.byref(o))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+               original: int = 8192, low: float = 1.0, high: float = 32.0):
+    """(freqs, scale) for rope_table: the angles per position of rot_dim / 2 pairs, a list of floats, and the factor of
+    their cosines and sines.  scaling stretches positions past the `original` ones that a model was trained on by
+    `factor`: "linear" (all pairs alike), "ntk" (by the base), "blend" (pairs that turn fewer than `low` times over the
+    original positions stretch, those of more than `high` times do not, linear between: by turns), "ramp" (the same,
+    linear by the pair's number, with the cosines and sines scaled by 0.1 ln(factor) + 1)."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    if not base > 1 or not factor > 0:
+        raise ValueError("base must be above 1 and factor above 0")
+    half = rot_dim // 2
+    if scaling == "ntk" and half > 1:
+        base *= factor ** (half / (half - 1))
+    f = [base ** (-j / half) for j in range(half)]
+    if scaling in (None, "ntk"):
+        return f, 1.0
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling not in ("blend", "ramp"):
+        raise ValueError(f"scaling must be linear, ntk, blend or ramp, not {scaling}")
+    if not 0 < low < high:
+        raise ValueError("low must be above 0 and below high")
+    if scaling == "blend":
+        keep = [(x * original / (2 * math.pi) - low) / (high - low) for x in f]
+    else:  # the pair's number at which a pair turns so many times
+        first, last = (half * math.log(original / (n * 2 * math.pi)) / math.log(base) for n in (high, low))
+        first, last = max(math.floor(first), 0), min(math.ceil(last), rot_dim - 1)
+        keep = [1 - (j - first) / (max(last - first, 0.001)) for j in range(half)]
+    keep = [min(1.0, max(0.0, x)) for x in keep]
+    scale = 0.1 * math.log(factor) + 1.0 if scaling == "ramp" and factor > 1 else 1.0
+    return [x * k + x / factor * (1 - k) for x, k in zip(f, keep)], scale
+
+
+def rope_table(n_pos: int, freqs, scale: float = 1.0, device="cuda", out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """The table of rope and kv_store_rope, float32 (n_pos, 2 * len(freqs)): row p the cosines, then the sines of
+    p * freqs, times scale, computed in 64 bits.  freqs: a list, or a float64 tensor on the device."""
+    if not isinstance(freqs, torch.Tensor):
+        freqs = torch.tensor(freqs, dtype=torch.float64, device=device)
+    dev, half = freqs.device, freqs.numel()
+    if not freqs.is_cuda:
+        raise ValueError("freqs must be a list or a device tensor")
+    if out is None:
+        out = torch.empty((n_pos, 2 * half), dtype=torch.float32, device=dev)
+    _call("ft_rope_table", dev, stream, _plain(freqs, "freqs", torch.float64, (half,), dev), half, n_pos, scale,
+          _plain(out, "out", torch.float32, (n_pos, 2 * half), dev))
+    return out
+
+
+def _rotation(table: torch.Tensor, positions: torch.Tensor, t: int, interleaved: bool, device) -> _Rotation:
+    if table.dim() != 2:
+        raise ValueError("table must be (n_pos, rot_dim)")
+    n_pos, rot = table.shape
+    return _Rotation(_plain(table, "table", torch.float32, (n_pos, rot), device),
+                     _plain(positions, "positions", torch.int32, (t,), device), n_pos, rot, interleaved)
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
+         weight: torch.Tensor | None = None, eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The rows of x ((t, heads, dim), strided tokens and heads) turned by their token's position (int32 (t,)): pairs
+    (j, j + rot_dim / 2), or neighbours with interleaved; elements from the table's width on stay.  weight (float32
+    (dim,)): each row is first divided by its root mean square (with eps) and multiplied by weight.  out may be x."""
+    if not x.is_cuda or x.dim() != 3:
+        raise ValueError("x must be a device tensor (t, heads, dim)")
+    ty, dev, shape = _float_type(x, "x"), x.device, x.shape
+    t, heads, dim = shape
+    if out is None:
+        out = x.new_empty(shape)
+    xs, os_ = _rows(x, "x", shape, x.dtype, dev), _rows(out, "out", shape, x.dtype, dev)
+    r = _rotation(table, positions, t, interleaved, dev)
+    _call("ft_rope", dev, stream, ctypes.byref(r), ty, x.data_ptr(), xs[0], xs[1], t, heads, dim,
+          None if weight is None else _plain(weight, "weight", torch.float32, (dim,), dev), eps, out.data_ptr(), os_[0], os_[1])
+    return out
+
+
+def kv_store_rope(cache: KvCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                  positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False, q_weight: torch.Tensor | None = None,
+                  k_weight: torch.Tensor | None = None, eps: float = 1e-6, q_out: torch.Tensor | None = None, stream=None):
+    """kv_store with the keys turned (and normed, with k_weight) on the way, and the queries q ((t, heads, head_dim),
+    any number of heads, or None) turned in the same launch, as rope does: returns them (in q_out, which may be q)."""
+    t, dev, dim = k.shape[0], cache.device, cache.head_dim
+    ty, shape = _float_type(k, "k"), (t, cache.n_kv_head, dim)
+    ks, vs = _rows(k, "k", shape, k.dtype, dev), _rows(v, "v", shape, k.dtype, dev)
+    r = _rotation(table, positions, t, interleaved, dev)
+    o = _QkvRows(None, 0, 0, 0, None, None, 0, 0, k.data_ptr(), ks[0], ks[1], None, v.data_ptr(), vs[0], vs[1], eps)
+    if k_weight is not None:
+        o.k_weight = _plain(k_weight, "k_weight", torch.float32, (dim,), dev)
+    if q is not None:
+        heads = q.shape[1]
+        qshape = (t, heads, dim)
+        qs = _rows(q, "q", qshape, k.dtype, dev)
+        if q_out is None:
+            q_out = q.new_empty(qshape)
+        os_ = _rows(q_out, "q_out", qshape, k.dtype, dev)
+        o.q, o.q_token, o.q_head, o.n_head = q.data_ptr(), qs[0], qs[1], heads
+        o.q_out, o.out_token, o.out_head = q_out.data_ptr(), os_[0], os_[1]
+        if q_weight is not None:
+            o.q_weight = _plain(q_weight, "q_weight", torch.float32, (dim,), dev)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight are q's")
+    _call("ft_kv_store_rope", dev, stream, cache._ref, ctypes.byref(r), ty, ctypes.byref(o),
+          _plain(slots, "slots", torch.int64, (t,), dev), t)
+    return q_out
+
+
+# ---------------------------------------------------------------------------
+# the norm around a block
+# ---------------------------------------------------------------------------
+def _line(t: torch.Tensor, name: str, shape: tuple, dtype, device) -> int:
+    """Row stride of a (rows, width) tensor."""
+    ld, step = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != shape or t.dtype is not dtype or t.device != device or (step != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be {shape} {dtype} on {device} with unit element stride, "
+                         f"not {tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
+    return ld if shape[0] > 1 else shape[1]
+
+
+def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+         residual: torch.Tensor | None = None, post_weight: torch.Tensor | None = None, post_bias: torch.Tensor | None = None,
+         post: bool | None = None, gate: torch.Tensor | None = None, scale: float = 1.0, kind: str = "rms", eps: float = 1e-6,
+         act: str | None = None, rows: bool | None = None, r: torch.Tensor | None = None, out: torch.Tensor | None = None,
+         xq: torch.Tensor | None = None, stream=None):
+    """(r, n, xq) of x ((t, width), rows may be strided, as those of all others): r = residual + scale * gate * x, x first
+    normed with `post` (by default where there is a post_weight); n = norm(r) * weight + bias.  gate: (t, width), or
+    (1, width) or (width,) for all rows.  kind: "rms" or "layer".  act ("Q8_1", "Q8_0", "Q8_K"): n as quantized blocks,
+    xq, and as rows only with rows=True; without act n is rows.  r is x where nothing is done to it.  What is not
+    computed is None.  r and out may be x or residual."""
+    if not x.is_cuda or x.dim() != 2:
+        raise ValueError("x must be a device tensor (t, width)")
+    ty, dev, dt, shape = _float_type(x, "x"), x.device, x.dtype, x.shape
+    t, width = shape
+    if kind not in ("rms", "layer"):
+        raise ValueError(f"kind must be rms or layer, not {kind}")
+    if act not in (None, "Q8_1", "Q8_0", "Q8_K"):
+        raise ValueError(f"act must be Q8_1, Q8_0 or Q8_K, not {act}")
+    if not scale:
+        raise ValueError("scale must not be 0")
+    if post is None:
+        post = post_weight is not None or post_bias is not None
+    o = _NormOpts(None, 0, None, 0, post, None, None, scale, kind == "layer", eps, None, None, None, 0, None, 0, 0, None)
+    for w, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias")):
+        if w is not None:
+            setattr(o, name, _plain(w, name, torch.float32, (width,), dev))
+    if residual is not None:
+        o.residual, o.ld_residual = residual.data_ptr(), _line(residual, "residual", shape, dt, dev)
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate.unsqueeze(0)
+        if gate.shape[0] == 1 or gate.stride(0) == 0:
+            _line(gate[:1], "gate", (1, width), dt, dev)
+            if gate.shape[0] not in (1, t):
+                raise ValueError(f"gate must be (1 or {t}, {width})")
+        else:
+            o.ld_gate = _line(gate, "gate", shape, dt, dev)
+        o.gate = gate.data_ptr()
+    if r is None:
+        if post or residual is not None or gate is not None or scale != 1.0:
+            r = torch.empty(shape, dtype=dt, device=dev)
+            o.r, o.ld_r = r.data_ptr(), width
+        else:
+            r = x
+    else:
+        o.r, o.ld_r = r.data_ptr(), _line(r, "r", shape, dt, dev)
+    if out is None:
+        if rows or act is None and rows is None:
+            out = torch.empty(shape, dtype=dt, device=dev)
+            o.out, o.ld_out = out.data_ptr(), width
+    else:
+        o.out, o.ld_out = out.data_ptr(), _line(out, "out", shape, dt, dev)
+    if act is not None:
+        size = (t, row_bytes(act, width))
+        if xq is None:
+            xq = torch.empty(size, dtype=torch.uint8, device=dev)
+        o.act, o.xq = TYPES[act], _plain(xq, "xq", torch.uint8, size, dev)
+    elif xq is not None:
+        raise ValueError("xq needs an act")
+    _call("ft_norm", dev, stream, ty, x.data_ptr(), _line(x, "x", shape, dt, dev), t, width, ctypes.byref(o))
+    return r, out, xq
+
+
+# ---------------------------------------------------------------------------
+# low-rank adapters
+# ---------------------------------------------------------------------------
+def lora_scratch_bytes(t: int, k: int, n_adapter: int, rank: int) -> int:
+    """Bytes of a workspace that is enough for lora at these sizes and any smaller t."""
+    n = lib().ft_lora_scratch_bytes(t, k, n_adapter, rank)
+    if not n:
+        raise FtError(3, f"no adapters for {t} rows of {k}, {n_adapter} of rank {rank}")
+    return n
+
+
+def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, y: torch.Tensor | None = None,
+         scales: torch.Tensor | None = None, ranks: torch.Tensor | None = None, out: torch.Tensor | None = None,
+         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y + scales[i] * b[i] (a[i] x) for every row of x ((t, k), rows may be strided) with the adapter i = ids (int32
+    (t,)) of a (n_adapter, rank, k) and b (n_adapter, n, rank), which share a type; an id outside them leaves y's row.  y
+    (default: zeros) and out are float32 (t, n); out may be y.  scales float32, ranks int32 (n_adapter,): an
+    adapter's own rank, what a and b hold beyond is not used.  workspace: uint8, lora_scratch_bytes (default: the
+    stream's pool)."""
+    if not x.is_cuda or x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be a device tensor (t, k), a (n_adapter, rank, k), b (n_adapter, n, rank)")
+    tx, tw, dev = _float_type(x, "x"), _float_type(a, "a"), x.device
+    t, k = shape = x.shape
+    many, rank, _ = a.shape
+    n = b.shape[1]
+    if out is None:
+        out = torch.empty((t, n), dtype=torch.float32, device=dev)
+    o = _LoraOpts(None if ranks is None else _plain(ranks, "ranks", torch.int32, (many,), dev),
+                  None if scales is None else _plain(scales, "scales", torch.float32, (many,), dev), None, 0)
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        o.workspace, o.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    yp, ldy = (None, 0) if y is None else (y.data_ptr(), _line(y, "y", (t, n), torch.float32, dev))
+    _call("ft_lora", dev, stream, tx, x.data_ptr(), _line(x, "x", shape, x.dtype, dev), t, k, tw,
+          _plain(a, "a", a.dtype, (many, rank, k), dev), _plain(b, "b", a.dtype, (many, n, rank), dev), many, rank, n,
+          _plain(ids, "ids", torch.int32, (t,), dev), yp, ldy, out.data_ptr(), _line(out, "out", (t, n), torch.float32, dev),
+          ctypes.byref(o))
     return out

@@ -392,6 +392,109 @@ ft_status ft_attn_kv(const ft_kv_cache* cache, ft_float type, const void* q, int
 size_t ft_attn_kv_scratch_bytes(const ft_kv_cache* cache, int64_t n_tok, int64_t n_head, int64_t n_seq, int64_t max_kv,
                                 const ft_attn_opts* opts);
 
+/* Rotary positions.  A pair (a, b) of a row at position p turns by the angle p * f_j:
+     a' = a cos - b sin,  b' = b cos + a sin,
+   pair j of rot_dim / 2 being elements (j, j + rot_dim / 2), or (2j, 2j + 1) with
+   `interleaved`; elements from rot_dim on stay as they are.  cos and sin are read from a table
+   [n_pos][rot_dim] fp32, row p the cosines, then the sines: ft_rope_table's, or the caller's.
+   positions [t] int32; one outside the table counts as its nearest row.  Products and sums
+   are single fp32 operations. */
+typedef struct {
+  const float* table;
+  const int32_t* positions;
+  int64_t n_pos;
+  int64_t rot_dim;   /* even, 2 .. head_dim */
+  int interleaved;
+} ft_rotation;
+/* Row p of the table: cos(p * f_j) * scale and sin(p * f_j) * scale, computed in 64 bits and
+   rounded once.  freqs [half] double (every scaling for long contexts is a choice of f and
+   scale; negative f turns back), table [n_pos][2 * half].  half <= 2^15, n_pos <= 2^30 / half. */
+ft_status ft_rope_table(const double* freqs, int64_t half, int64_t n_pos, double scale, float* table, ft_stream_t stream);
+/* Turn the rows of x, [t][n_head][dim] of `type`, into out (which may be x itself, with its
+   strides; otherwise they must not overlap).  Element stride 1, token and head strides in
+   elements.  With weight ([dim] fp32) each row is first x * rstd * weight, rstd = 1 / sqrt(mean x^2 + eps)
+   (mean in 64 bits, rstd rounded to fp32).  dim 2 .. 512, t <= 2^24, n_head <= 1024, t * n_head <= 2^30. */
+ft_status ft_rope(const ft_rotation* rot, ft_float type, const void* x, int64_t x_token, int64_t x_head, int64_t t,
+                  int64_t n_head, int64_t dim, const float* weight, double eps, void* out, int64_t out_token,
+                  int64_t out_head, ft_stream_t stream);
+/* ft_kv_store with the keys normed (k_weight, nullable) and turned on the way, and the queries
+   turned into q_out as ft_rope does, in the same launch.  q: [t][n_head][head_dim], n_head >= 0 (0:
+   none, q and q_out may be NULL; otherwise n_head need not fit the cache's).  A token whose slot is
+   negative or past the pool stores nothing; its query is turned all the same.  The keys' codes are
+   those of ft_rope's fp32 rows given to ft_kv_store.  q_out may be q itself, and must not overlap k or v. */
+typedef struct {
+  const void* q;
+  int64_t q_token, q_head, n_head;
+  const float* q_weight;   /* nullable [head_dim] */
+  void* q_out;
+  int64_t out_token, out_head;
+  const void* k;
+  int64_t k_token, k_head;
+  const float* k_weight;   /* nullable [head_dim] */
+  const void* v;
+  int64_t v_token, v_head;
+  double eps;
+} ft_qkv_rows;
+ft_status ft_kv_store_rope(const ft_kv_cache* cache, const ft_rotation* rot, ft_float type, const ft_qkv_rows* rows,
+                           const int64_t* slots, int64_t t, ft_stream_t stream);
+
+/* The norm around a block.  For rows of x, [rows][width] of `type`:
+     b = x;  with `post`: b = norm(b) * post_weight + post_bias;
+     with gate: b = b * gate;  b = b * scale;
+     r = residual + b (b without a residual);
+     n = norm(r) * weight + bias
+   norm(v) = v / sqrt(mean v^2 + eps), or with `layer` (v - mean) / sqrt(variance + eps).  Written are
+   r, n (`out`, of `type`) and n's blocks of `act` (`xq`, [rows][width / blk], ft_quantize_act's of n in
+   fp32), whichever are not NULL, at least one.  n is the norm of r before r is rounded to its type.
+   Means are summed in 64 bits, 1 / sqrt is rounded to fp32, every further step is one fp32 operation.
+   Weights and biases are fp32, NULL for ones and zeros.  Row strides in elements, at least width;
+   ld_gate 0: one row of gates for all.  r and out may each be x or the residual itself (same
+   stride).  width <= 32768, rows <= 2^24; blocks need a width of whole blocks. */
+typedef struct {
+  const void* residual;     /* nullable [rows][width] */
+  int64_t ld_residual;
+  const void* gate;         /* nullable */
+  int64_t ld_gate;
+  int post;                 /* 1: x is normed first */
+  const float* post_weight;
+  const float* post_bias;
+  float scale;              /* 0 = 1 */
+  int layer;                /* 0: root mean square, 1: mean and variance */
+  double eps;
+  const float* weight;
+  const float* bias;
+  void* r;
+  int64_t ld_r;
+  void* out;
+  int64_t ld_out;
+  ft_type act;              /* FT_Q8_1, FT_Q8_0 or FT_Q8_K; read with xq only */
+  void* xq;
+} ft_norm_opts;
+ft_status ft_norm(ft_float type, const void* x, int64_t ldx, int64_t rows, int64_t width, const ft_norm_opts* opts,
+                  ft_stream_t stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+     out_i = y_i + scales[a] * B[a] (A[a] x_i),  a = ids[i], i < t.
+   x: [t][k] of x_type; y (nullable: zeros) and out: [t][n] fp32, row strides in elements; out may be y
+   itself (same stride).  A: [n_adapter][rank][k], B: [n_adapter][n][rank], both of w_type.  ids [t] int32:
+   one outside 0 .. n_adapter-1 names no adapter, and its row of out is y's.  ranks (nullable) [n_adapter]
+   int32: only that many ranks of an adapter count (0: none; at most rank), what A and B hold beyond is
+   not used.  scales (nullable: 1) [n_adapter] fp32.  About fp32 accuracy for every type; A x is held in fp32.  A
+   row of x with a NaN or an infinity gives NaN in its own row of out only.  t, k, n <= 2^20, rank 1 .. 256,
+   n_adapter <= 8192.  Scratch: the stream's pool, or the caller's `workspace` (16-byte aligned,
+   ft_lora_scratch_bytes). */
+typedef struct {
+  const int32_t* ranks;
+  const float* scales;
+  void* workspace;          /* nullable */
+  size_t workspace_bytes;
+} ft_lora_opts;
+ft_status ft_lora(ft_float x_type, const void* x, int64_t ldx, int64_t t, int64_t k, ft_float w_type, const void* A,
+                  const void* B, int64_t n_adapter, int64_t rank, int64_t n, const int32_t* ids, const float* y,
+                  int64_t ldy, float* out, int64_t ldo, const ft_lora_opts* opts, ft_stream_t stream);
+/* Scratch bytes that are enough for these sizes and any smaller t; 0 for sizes that are refused. */
+size_t ft_lora_scratch_bytes(int64_t t, int64_t k, int64_t n_adapter, int64_t rank);
+
 /* Grow the stream's scratch pool to at least `bytes` [P3 review: grow-only
    per-stream pool].  Call before capturing a graph.  The pool is never shrunk;
    retired buffers are released by ft_shutdown(). */
