@@ -25,6 +25,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int LORA_TILE = 64;    // tokens per tile
 constexpr int LORA_RANKS = 64;   // ranks per workgroup of the first product
+constexpr int LORA_FEW = 1024;   // adapters up to which a workgroup finds its tile by itself
 
 struct LoraIo {
   const void* x;
@@ -38,34 +39,39 @@ struct LoraIo {
   const float* scales;
   int64_t k, n;
   int t, rank, adapters, rank_pad;   // rank_pad: rank, rounded up to 16
-  int vec_x, vec_a, vec_b, vec_y, copies;   // copies: out is not y, rows without an adapter are copied
+  int copies;                        // out is not y: rows without an adapter are copied
   int parts, part_k;                 // shares of the long axis
   float* h;            // [parts][t][rank_pad]
   const int32_t* order;              // null: tiles from the ids
   const int4* tiles;                 // adapter, first place in order, tokens
   const int32_t* n_tiles;
+  int words;                         // bytes of LDS for finding tiles
 };
 
-// eight elements of a row from e on, those from `end` on as zeros; vec: 16-byte aligned and no end within
+// Loads and stores below are whole whatever their address: rows need only their elements' alignment.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+template <int T> constexpr int LORA_WORDS = T == FT_F32 ? 2 : 1;   // of 16 bytes for eight elements
+
+// eight elements, and the same of which those from `end` on count as zeros (e: the first's number in its row)
 template <int T>
-__device__ __forceinline__ void lora_load(const void* base, int64_t at, int e, int end, bool vec, u32x4 (&r)[T == FT_F32 ? 2 : 1]) {
-  if (vec && e + 8 <= end) {
-    if constexpr (T == FT_F32) {
-      const u32x4* p = (const u32x4*)((const float*)base + at);
-      r[0] = p[0];
-      r[1] = p[1];
-    } else {
-      r[0] = *(const u32x4*)((const uint16_t*)base + at);
-    }
+__device__ __forceinline__ void lora_load(const void* base, int64_t at, u32x4 (&r)[LORA_WORDS<T>]) {
+  const u32x4_any* p = (const u32x4_any*)((const uint8_t*)base + at * (T == FT_F32 ? 4 : 2));
+#pragma unroll
+  for (int i = 0; i < LORA_WORDS<T>; ++i) r[i] = p[i];
+}
+template <int T>
+__device__ __forceinline__ void lora_load_end(const void* base, int64_t at, int e, int end, u32x4 (&r)[LORA_WORDS<T>]) {
+  if (e + 8 <= end) {
+    lora_load<T>(base, at, r);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < (T == FT_F32 ? 2 : 1); ++i) r[i] = u32x4{0, 0, 0, 0};
-#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (e + i >= end) break;
-    if constexpr (T == FT_F32) r[i >> 2][i & 3] = ((const uint32_t*)base)[at + i];
-    else r[0][i >> 1] |= (uint32_t)((const uint16_t*)base)[at + i] << (16 * (i & 1));
+    uint32_t u = 0;
+    if (e + i < end) u = T == FT_F32 ? ((const uint32_t*)base)[at + i] : ((const uint16_t*)base)[at + i];
+    if constexpr (T == FT_F32) r[i >> 2][i & 3] = u;
+    else r[0][i >> 1] = i & 1 ? r[0][i >> 1] | (u << 16) : u;
   }
 }
 
@@ -91,7 +97,7 @@ __device__ __forceinline__ void lora_pieces(const float (&v)[8], bf16x8 (&o)[P])
 // of eight loaded elements; WITH: the other operand's type (two fp16 operands stay as they are)
 template <int T, int WITH> constexpr int LORA_PIECES = T == FT_F32 ? 3 : T == FT_F16 && WITH != FT_F16 ? 2 : 1;
 template <int T, int P>
-__device__ __forceinline__ void lora_operand(const u32x4 (&r)[T == FT_F32 ? 2 : 1], bf16x8 (&o)[P]) {
+__device__ __forceinline__ void lora_operand(const u32x4 (&r)[LORA_WORDS<T>], bf16x8 (&o)[P]) {
   if constexpr (P == 1) {
     o[0] = __builtin_bit_cast(bf16x8, r[0]);
   } else {
@@ -120,194 +126,294 @@ __device__ __forceinline__ f32x4 lora_mfma(const bf16x8 (&a)[PA], const bf16x8 (
   }
 }
 
-// A tile: its adapter (or -1), how many tokens, and which.
+// A tile: its adapter (or -1), that adapter's rank, how many tokens, and which.
 struct LoraTile {
-  int adapter, count, rank;
-  int groups, ways;   // groups of 16 tokens (1, 2 or 4), waves per group
-  int token;          // the lane's, in lane l of all waves the tile's token l
+  int adapter, rank, count;
+  int first;          // the first token of the 16 that are asked for
+  int token;          // lane l of every wave: the tile's token l
 };
-__device__ __forceinline__ bool lora_tile(const LoraIo& io, int index, LoraTile& t) {
+// Tile `index` of the plan's, or of those that up to 64 ids make; with SIXTEENS the index counts
+// groups of 16 tokens, tile by tile.  False: there are fewer.  Without a plan s_word has a word per adapter.
+template <bool SIXTEENS>
+__device__ __forceinline__ bool lora_tile(const LoraIo& io, int index, int* s_word, LoraTile& t) {
   const int lane = threadIdx.x & 63;
+  t.first = 0;
   if (io.order) {
-    if (index >= *io.n_tiles) return false;
-    const int4 e = io.tiles[index];
+    if (SIXTEENS) {
+      t.first = index & 3;
+      index >>= 2;
+      t.first *= 16;
+    }
+    const int n = *io.n_tiles;
+    const int4 e = io.tiles[index];   // one beyond the last: whatever is there
+    if (index >= n || t.first >= e.z) return false;
     t.adapter = e.x;
     t.count = e.z;
+    t.rank = e.w;
     t.token = io.order[e.y + min(lane, e.z - 1)];
-  } else {   // the tokens of token `index`'s adapter, if it is the first of them
-    int a = lane < io.t ? io.ids[lane] : -2;
-    if (lane < io.t && (a < 0 || a >= io.adapters)) a = -1;
-    t.adapter = __builtin_amdgcn_readlane(a, index);
+  } else {
+    // each adapter's word: its first token, and from bit 8 on its tokens
+    int a = lane < io.t ? io.ids[lane] : -2, rank = 0;
+    const bool here = lane < io.t;
+    if (here && (a < 0 || a >= io.adapters)) a = -1;
+    if (a >= 0) rank = io.ranks ? max(0, min(io.ranks[a], io.rank)) : io.rank;
+    int* word = s_word + (here ? a + 1 : 0);
+    const bool counts = threadIdx.x < 64 && here;
+    if (counts) *word = 64;
+    __syncthreads();
+    if (counts) atomicMin(word, lane);
+    __syncthreads();
+    if (counts) atomicAdd(word, 256);
+    __syncthreads();
+    const int w = here ? *word : 0;
+    const bool leads = here && (w & 255) == lane;
+    const int groups = SIXTEENS ? ((w >> 8) + 15) >> 4 : 1;
+    const uint64_t below = (1ull << lane) - 1;
+    int before = 0;
+#pragma unroll
+    for (int k = 1; k <= (SIXTEENS ? 4 : 1); ++k) before += __builtin_popcountll(__ballot(leads && groups >= k) & below);
+    const uint64_t mine = __ballot(leads && before <= index && index < before + groups);
+    if (!mine) return false;
+    const int leader = __builtin_ctzll(mine);
+    t.first = 16 * (index - __builtin_amdgcn_readlane(before, leader));
+    t.adapter = __builtin_amdgcn_readlane(a, leader);
+    t.rank = __builtin_amdgcn_readlane(rank, leader);
     const uint64_t m = __ballot(a == t.adapter);
-    if (__builtin_ctzll(m) != index) return false;
     t.count = __builtin_popcountll(m);
-    // lane l finds the l-th set bit: every lane tells its token to the lane of its rank
-    const int place = __builtin_popcountll(m & ((1ull << lane) - 1));
+    // every token of the tile goes to the lane of its rank among them; lanes behind the last take any
     const bool in = (m >> lane) & 1;
-    int src = 0;
-    src = __builtin_amdgcn_ds_permute(4 * (in ? place : 63), in ? lane : 0);
-    if (t.count < 64 && lane >= t.count) src = index;
-    t.token = src;
+    const int src = __builtin_amdgcn_ds_permute(4 * (in ? __builtin_popcountll(m & below) : 63), in ? lane : leader);
+    t.token = lane < t.count ? src : leader;
   }
   t.adapter = __builtin_amdgcn_readfirstlane(t.adapter);
   t.count = __builtin_amdgcn_readfirstlane(t.count);
-  t.rank = 0;
-  if (t.adapter >= 0) t.rank = io.ranks ? __builtin_amdgcn_readfirstlane(max(0, min(io.ranks[t.adapter], io.rank))) : io.rank;
-  t.groups = t.count <= 16 ? 1 : t.count <= 32 ? 2 : 4;
-  t.ways = 4 / t.groups;
+  t.rank = __builtin_amdgcn_readfirstlane(t.rank);
+  t.first = __builtin_amdgcn_readfirstlane(t.first);
   return true;
 }
 
-// h[part][token][rank] of a tile, for 64 ranks and one share of the long axis
-template <int TX, int TW>
+// h[part][token][rank] of 16 of a tile's tokens, for 16 * R ranks and one share of the long axis, which
+// the four waves take in turn, U steps of 32 elements at a time with all of their loads in flight.
+template <int TX, int TW, int R>
 __global__ void __launch_bounds__(256)
 lora_shrink_kernel(LoraIo io) {
   constexpr bool F16 = TX == FT_F16 && TW == FT_F16;
-  constexpr int PX = LORA_PIECES<TX, TW>, PW = LORA_PIECES<TW, TX>, RX = TX == FT_F32 ? 2 : 1, RW = TW == FT_F32 ? 2 : 1;
-  __shared__ __align__(16) float s_h[3][64][4][4];   // the other waves' sums
+  constexpr int PX = LORA_PIECES<TX, TW>, PW = LORA_PIECES<TW, TX>, RX = LORA_WORDS<TX>, RW = LORA_WORDS<TW>;
+  constexpr int U = RX + R * RW <= 3 ? 8 : RX + R * RW <= 6 ? 4 : 2;
+  __shared__ __align__(16) float s_h[3][R][64][4];   // the other waves' sums
+  extern __shared__ int s_word[];
   LoraTile tile;
-  if (!lora_tile(io, blockIdx.x, tile)) return;
-  const int r0 = blockIdx.z * LORA_RANKS;
+  if (!lora_tile<true>(io, blockIdx.x, s_word, tile)) return;
+  const int t0 = tile.first;
+  const int r0 = blockIdx.z * (16 * R);
   if (r0 >= tile.rank) return;
   const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, quad = lane >> 4;
-  const int group = wave & (tile.groups - 1), way = wave / tile.groups;
-  const int k = (int)io.k;
-  // the workgroup's share of the axis, in steps of 32, dealt to its ways
+  const int k = (int)io.k, n_rt = (tile.rank - r0 + 15) >> 4;   // tiles of 16 ranks
   const int first = blockIdx.y * io.part_k, last = min(k, first + io.part_k);
-  const int n_rt = min(4, (tile.rank - r0 + 15) >> 4);   // tiles of 16 ranks
-  const int tok = __shfl(tile.token, min(16 * group + l16, tile.count - 1), 64);
-  const int64_t xrow = (int64_t)tok * io.ldx;
-  int64_t arow[4];
-  bool there[4];
+  const int tok = __shfl(tile.token, min(t0 + l16, tile.count - 1), 64);
+  const int64_t xrow = (int64_t)tok * io.ldx + 8 * quad;
+  int64_t arow[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 16 * i + l16;
-    there[i] = r < tile.rank;
-    arow[i] = ((int64_t)tile.adapter * io.rank + (there[i] ? r : 0)) * k;
-  }
-  f32x4 acc[4];
+  for (int i = 0; i < R; ++i)   // rows past the adapter's rank: sums that nobody reads
+    arow[i] = ((int64_t)tile.adapter * io.rank + min(r0 + 16 * i + l16, tile.rank - 1)) * k + 8 * quad;
+  f32x4 acc[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = f32x4{0, 0, 0, 0};
-  const bool used = 16 * group < tile.count;   // three groups: the fourth wave has none
-  if (used) {
-    for (int k0 = first + 32 * way; k0 < last; k0 += 32 * tile.ways) {
-      const int e = k0 + 8 * quad;
-      u32x4 rx[RX], rw[4][RW];
-      lora_load<TX>(io.x, xrow + e, e, last, io.vec_x, rx);
+  for (int i = 0; i < R; ++i) acc[i] = f32x4{0, 0, 0, 0};
+  const auto sum = [&](const u32x4 (&rx)[RX], const u32x4 (&rw)[R][RW]) {
+    bf16x8 px[PX];
+    lora_operand<TX, PX>(rx, px);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n_rt) lora_load<TW>(io.a, arow[i] + e, e, there[i] ? last : 0, io.vec_a, rw[i]);
-      bf16x8 px[PX];
-      lora_operand<TX, PX>(rx, px);
+    for (int i = 0; i < R; ++i)
+      if (i < n_rt) {
+        bf16x8 pw[PW];
+        lora_operand<TW, PW>(rw[i], pw);
+        acc[i] = lora_mfma<F16>(pw, px, acc[i]);
+      }
+  };
+  for (int k0 = first + 32 * U * wave; k0 < last; k0 += 32 * U * 4) {
+    if (k0 + 32 * U <= last) {
+      u32x4 rx[U][RX], rw[U][R][RW];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n_rt) {
-          bf16x8 pw[PW];
-          lora_operand<TW, PW>(rw[i], pw);
-          acc[i] = lora_mfma<F16>(pw, px, acc[i]);
-        }
+      for (int u = 0; u < U; ++u) lora_load<TX>(io.x, xrow + k0 + 32 * u, rx[u]);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i < n_rt)
+#pragma unroll
+          for (int u = 0; u < U; ++u) lora_load<TW>(io.a, arow[i] + k0 + 32 * u, rw[u][i]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) sum(rx[u], rw[u]);
+    } else {
+      for (int e = k0; e < last; e += 32) {
+        u32x4 rx[RX], rw[R][RW];
+        lora_load_end<TX>(io.x, xrow + e, e + 8 * quad, last, rx);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (i < n_rt) lora_load_end<TW>(io.a, arow[i] + e, e + 8 * quad, last, rw[i]);
+        sum(rx, rw);
+      }
     }
   }
-  if (tile.ways > 1) {
-    if (way > 0)
+  // one wave for each tile of ranks adds the four up
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n_rt) *(f32x4*)s_h[wave - tile.groups][lane][i] = acc[i];
-    __syncthreads();
-    if (way > 0) return;
-    for (int j = 1; j < tile.ways; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n_rt) acc[i] += *(const f32x4*)s_h[(j - 1) * tile.groups + group][lane][i];
+  for (int i = 0; i < R; ++i) {
+    const int to = R == 1 ? 0 : i & 3;
+    if (wave != to) *(f32x4*)s_h[wave - (wave > to)][i][lane] = acc[i];
   }
-  if (!used || 16 * group + l16 >= tile.count) return;
-  float* o = io.h + ((int64_t)blockIdx.y * io.t + tok) * io.rank_pad + r0 + 4 * quad;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n_rt) *(f32x4*)(o + 16 * i) = acc[i];
+  for (int i = 0; i < R; ++i) {
+    if (wave != i || i >= n_rt || t0 + l16 >= tile.count) continue;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) acc[i] += *(const f32x4*)s_h[j][i][lane];
+    *(f32x4*)(io.h + ((int64_t)blockIdx.y * io.t + tok) * io.rank_pad + r0 + 16 * i + 4 * quad) = acc[i];
+  }
 }
 
-constexpr int LORA_COLS = 256;   // columns per workgroup of the second product
-
-// out = y + B h for a tile and 256 columns.  S: steps of 32 ranks
-template <int TW, int S>
+// out = y + B h for a tile and 64 * C columns, 16 * C a wave: the wave's rows of B stay in its registers while it
+// goes over the tile's tokens, 16 at a time, the next ones' y and h on their way.  With C = 4 the sums change
+// places over LDS, so that y and out are read and written 256 bytes of a row at a time.  S: steps of 32 ranks; ONE: most
+// tiles hold 16 tokens or fewer, nothing is kept ready for more
+template <int TW, int S, int C, bool ONE>
 __global__ void __launch_bounds__(256)
 lora_expand_kernel(LoraIo io) {
-  constexpr int PW = LORA_PIECES<TW, FT_F32>, RW = TW == FT_F32 ? 2 : 1;
+  constexpr int PW = LORA_PIECES<TW, FT_F32>, RW = LORA_WORDS<TW>, PITCH = 16 * C + 4;
+  constexpr int L = 4 * C, ROWS = 64 / L;   // lanes that share a row of y, rows they take at once
+  __shared__ __align__(16) float s_out[C == 1 ? 1 : 4][C == 1 ? 1 : 16 * PITCH];
+  extern __shared__ int s_word[];
   LoraTile tile;
-  if (!lora_tile(io, blockIdx.y, tile)) return;
+  if (!lora_tile<false>(io, blockIdx.y, s_word, tile)) return;
   if (tile.rank == 0 && !io.copies) return;
   const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, quad = lane >> 4;
-  const int group = wave & (tile.groups - 1), way = wave / tile.groups;
-  if (16 * group >= tile.count) return;
-  const bool live = 16 * group + l16 < tile.count;
-  const int tok = __shfl(tile.token, min(16 * group + l16, tile.count - 1), 64);
-  bf16x8 ph[S][3];
-  const float scale = tile.rank && io.scales ? io.scales[tile.adapter] : 1.0f;
+  const int n = (int)io.n, n0 = ((int)blockIdx.x * 4 + wave) * 16 * C;
+  if (n0 >= n) return;
+  // the lane's place in y: columns at .. at + 3 of row i * ROWS + line of 16
+  const int line = C == 1 ? l16 : lane / L, at = n0 + 4 * (C == 1 ? quad : lane % L);
+  constexpr int B = ONE ? 1 : 2;
+  f32x4 y[B][C];
+  f32x4 h[B][S][2];
+  int tok[B][C];
+  const auto load = [&](int t0, f32x4 (&y)[C], f32x4 (&h)[S][2], int (&tok)[C]) {
+    const float* p = io.h + (int64_t)__shfl(tile.token, min(t0 + l16, tile.count - 1), 64) * io.rank_pad + 8 * quad;
+    const int64_t step = (int64_t)io.t * io.rank_pad;
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const int r = 32 * s + 8 * quad;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (r < tile.rank) {
-      const float* p = io.h + (int64_t)tok * io.rank_pad + r;
-      const int64_t step = (int64_t)io.t * io.rank_pad;
-      f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-      for (int j = 0; j < io.parts; ++j, p += step) {
-        a += *(const f32x4*)p;
-        b += *(const f32x4*)(p + 4);
+    for (int i = 0; i < C; ++i) {
+      const int row = t0 + i * ROWS + line;
+      tok[i] = row < tile.count ? __shfl(tile.token, row, 64) : -1;
+      y[i] = f32x4{0, 0, 0, 0};
+      if (io.y && tok[i] >= 0) {
+        const float* q = io.y + tok[i] * io.ldy + at;
+        if (at + 4 <= n) y[i] = *(const f32x4_any*)q;
+        else
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (at + e < n) y[i][e] = q[e];
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = r + i < tile.rank ? (i < 4 ? a[i & 3] : b[i & 3]) * scale : 0.0f;
     }
-    lora_pieces<3>(v, ph[s]);
-  }
-  const int64_t yrow = (int64_t)tok * io.ldy, orow = (int64_t)tok * io.ldo;
-  const int64_t n1 = min(io.n, (int64_t)(blockIdx.x + 1) * LORA_COLS);
-  for (int64_t n0 = (int64_t)blockIdx.x * LORA_COLS + 16 * way; n0 < n1; n0 += 16 * tile.ways) {
-    const int64_t c = n0 + 4 * quad;   // the lane's columns of the result
-    f32x4 acc = {0, 0, 0, 0};
-    const int64_t bn = min(n0 + l16, io.n - 1);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      h[s][0] = h[s][1] = f32x4{0, 0, 0, 0};
+      if (32 * s + 8 * quad >= tile.rank) continue;
+#pragma unroll 4
+      for (int j = 0; j < io.parts; ++j) {
+        h[s][0] += *(const f32x4*)(p + j * step + 32 * s);
+        h[s][1] += *(const f32x4*)(p + j * step + 32 * s + 4);
+      }
+    }
+  };
+  u32x4 rw[S][C][RW];
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int r = 32 * s + 8 * quad, bn = min(n0 + 16 * c + l16, n - 1);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) rw[s][c][i] = u32x4{0, 0, 0, 0};
+      if (r < tile.rank) lora_load_end<TW>(io.b, ((int64_t)tile.adapter * io.n + bn) * io.rank + r, r, tile.rank, rw[s][c]);
+    }
+  load(0, y[0], h[0], tok[0]);
+  const float scale = tile.rank && io.scales ? io.scales[tile.adapter] : 1.0f;
+  bf16x8 pw[S][C][PW];
+  const auto operands = [&] {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int c = 0; c < C; ++c) lora_operand<TW, PW>(rw[s][c], pw[s][c]);
+  };
+  if (!ONE) operands();
+#pragma unroll(ONE ? 1 : 4)
+  for (int g = 0; g < 4; ++g) {
+    const int b = ONE ? 0 : g & 1;
+    if (16 * g >= tile.count) break;
+    if (ONE && g) load(16 * g, y[0], h[0], tok[0]);
+    if (ONE) operands();
+    if (!ONE && 16 * (g + 1) < tile.count) load(16 * (g + 1), y[B - 1 - b], h[B - 1 - b], tok[B - 1 - b]);
+    f32x4 acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       if (32 * s >= tile.rank) break;
-      const int r = 32 * s + 8 * quad;
-      u32x4 rw[RW];
-      lora_load<TW>(io.b, ((int64_t)tile.adapter * io.n + bn) * io.rank + r, r, tile.rank, io.vec_b, rw);
-      bf16x8 pw[PW];
-      lora_operand<TW, PW>(rw, pw);
-      acc = lora_mfma<false>(pw, ph[s], acc);
-    }
-    if (!live) continue;
-    if (io.vec_y && c + 4 <= io.n) {
-      if (io.y) acc += *(const f32x4*)(io.y + yrow + c);
-      *(f32x4*)(io.out + orow + c) = acc;
-    } else {
+      float v[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + i < io.n) io.out[orow + c + i] = acc[i] + (io.y ? io.y[yrow + c + i] : 0.0f);
+      for (int i = 0; i < 8; ++i) v[i] = 32 * s + 8 * quad + i < tile.rank ? h[b][s][i >> 2][i & 3] * scale : 0.0f;
+      bf16x8 ph[3];
+      lora_pieces<3>(v, ph);
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] = lora_mfma<false>(pw[s][c], ph, acc[c]);
+    }
+    if constexpr (C > 1) {
+      float* mine = s_out[wave];
+#pragma unroll
+      for (int c = 0; c < C; ++c) *(f32x4*)(mine + l16 * PITCH + 16 * c + 4 * quad) = acc[c];
+      wave_lds_sync();
+#pragma unroll
+      for (int i = 0; i < C; ++i) acc[i] = *(const f32x4*)(mine + (i * ROWS + line) * PITCH + 4 * (lane % L));
+      wave_lds_sync();
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if (tok[b][i] < 0) continue;
+      float* q = io.out + tok[b][i] * io.ldo + at;
+      const f32x4 o = y[b][i] + acc[i];
+      if (at + 4 <= n) *(f32x4_any*)q = o;
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (at + e < n) q[e] = o[e];
     }
   }
+}
+
+// the adapters of tokens i, i + 1024, .. (adapters: none; -2: no such token)
+__device__ __forceinline__ void lora_ids(const int32_t* ids, int t, int adapters, int i, int (&a)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a[j] = i + 1024 * j < t ? ids[i + 1024 * j] : -2;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (i + 1024 * j < t && (a[j] < 0 || a[j] >= adapters)) a[j] = adapters;
 }
 
 // The tokens sorted by adapter (those of none last) and cut into tiles, by one workgroup.
 // Within an adapter the order is free: a token's result does not depend on its place.
 __global__ void __launch_bounds__(1024)
-lora_plan_kernel(const int32_t* __restrict__ ids, int t, int adapters, int32_t* __restrict__ order, int4* __restrict__ tiles,
-                 int32_t* __restrict__ n_tiles) {
+lora_plan_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ ranks, int most, int t, int adapters, int32_t* __restrict__ order,
+                 int4* __restrict__ tiles, int32_t* __restrict__ n_tiles) {
   extern __shared__ int s_count[];   // [adapters + 1], then places
   __shared__ int s_wave[2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), many = adapters + 1;
   for (int a = tid; a < many; a += 1024) s_count[a] = 0;
   __syncthreads();
-  for (int i0 = 0; i0 < t; i0 += 1024) {
-    const int i = i0 + tid;
-    int a = i < t ? ids[i] : -2;
-    if (i < t && (a < 0 || a >= adapters)) a = adapters;
-    const int a0 = __builtin_amdgcn_readfirstlane(a);
-    if (a0 >= 0 && __ballot(a == a0) == ~0ull) {
-      if (lane == 0) atomicAdd(&s_count[a0], 64);
-    } else if (a >= 0) {
-      atomicAdd(&s_count[a], 1);
+  for (int i0 = 0; i0 < t; i0 += 4096) {
+    int a[4];
+    lora_ids(ids, t, adapters, i0 + tid, a);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int a0 = __builtin_amdgcn_readfirstlane(a[j]);
+      if (a0 >= 0 && __ballot(a[j] == a0) == ~0ull) {
+        if (lane == 0) atomicAdd(&s_count[a0], 64);
+      } else if (a[j] >= 0) {
+        atomicAdd(&s_count[a[j]], 1);
+      }
     }
   }
   __syncthreads();
@@ -333,44 +439,52 @@ lora_plan_kernel(const int32_t* __restrict__ ids, int t, int adapters, int32_t* 
   for (int a = b0; a < b1; ++a) {
     const int c = s_count[a];
     s_count[a] = before_n;
-    for (int j = 0; j < c; j += LORA_TILE) tiles[before_m++] = int4{a == adapters ? -1 : a, before_n + j, min(LORA_TILE, c - j), 0};
+    const int rank = a == adapters || c == 0 ? 0 : ranks ? max(0, min(ranks[a], most)) : most;
+    for (int j = 0; j < c; j += LORA_TILE) tiles[before_m++] = int4{a == adapters ? -1 : a, before_n + j, min(LORA_TILE, c - j), rank};
     before_n += c;
   }
   __syncthreads();
-  for (int i0 = 0; i0 < t; i0 += 1024) {
-    const int i = i0 + tid;
-    int a = i < t ? ids[i] : -2;
-    if (i < t && (a < 0 || a >= adapters)) a = adapters;
-    const int a0 = __builtin_amdgcn_readfirstlane(a);
-    int at = 0;
-    if (a0 >= 0 && __ballot(a == a0) == ~0ull) {
-      if (lane == 0) at = atomicAdd(&s_count[a0], 64);
-      at = __builtin_amdgcn_readfirstlane(at) + lane;
-    } else if (a >= 0) {
-      at = atomicAdd(&s_count[a], 1);
+  for (int i0 = 0; i0 < t; i0 += 4096) {
+    int a[4];
+    lora_ids(ids, t, adapters, i0 + tid, a);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 1024 * j + tid, a0 = __builtin_amdgcn_readfirstlane(a[j]);
+      int at = 0;
+      if (a0 >= 0 && __ballot(a[j] == a0) == ~0ull) {
+        if (lane == 0) at = atomicAdd(&s_count[a0], 64);
+        at = __builtin_amdgcn_readfirstlane(at) + lane;
+      } else if (a[j] >= 0) {
+        at = atomicAdd(&s_count[a[j]], 1);
+      }
+      if (i < t) order[at] = i;
     }
-    if (i < t) order[at] = i;
   }
 }
 
-// Partial sums: enough workgroups for two per CU, a share of at least 128 elements.  Adapters
-// that no token names cannot be told from here; each is counted as a tile.
+// Shares of the long axis: enough workgroups for two per CU, at least 128 elements each.  Adapters that no
+// token names cannot be told from here; each is counted as a tile.
 struct LoraPlan {
-  int parts, part_k, tiles;
+  int parts, part_k, tiles, sixteens;   // tiles, and groups of 16 tokens, that there can be
+  bool sorts;          // tiles from a plan, not from the ids
+  int64_t likely;      // tiles that probably hold tokens
   size_t h, order, list, total;
 };
 static LoraPlan lora_plan(int64_t t, int64_t k, int rank, int64_t adapters) {
   LoraPlan p;
-  const int64_t some = std::min<int64_t>(t, adapters + 1);
-  const int64_t likely = std::max<int64_t>((t + LORA_TILE - 1) / LORA_TILE, std::min<int64_t>(t, adapters));
-  int64_t parts = std::min<int64_t>(16, (2 * ftk_num_cus() + likely - 1) / likely);
+  const int64_t some = std::min<int64_t>(t, adapters + 1), cus = ftk_num_cus();
+  p.likely = std::max<int64_t>((t + LORA_TILE - 1) / LORA_TILE, std::min<int64_t>(t, adapters));
+  const int64_t sixteens = std::max<int64_t>((t + 15) / 16, std::min<int64_t>(t, adapters));
+  int64_t parts = std::min<int64_t>(16, (2 * cus + sixteens - 1) / sixteens);
   parts = std::max<int64_t>(1, std::min(parts, (k + 127) / 128));
   p.part_k = (int)(((k + parts - 1) / parts + 127) / 128 * 128);
   p.parts = (int)((k + p.part_k - 1) / p.part_k);
-  p.tiles = (int)(t <= 64 ? t : t / LORA_TILE + some);
+  p.sorts = t > 64 || adapters > LORA_FEW;
+  p.tiles = (int)(t <= 64 ? some : t / LORA_TILE + some);
+  p.sixteens = (int)(p.sorts ? 4 * p.tiles : some + (t - 1) / 16);
   const size_t rank_pad = (size_t)(rank + 15) / 16 * 16;
-  // parts * t grows with t up to here whatever the parts: a bound for every smaller t too
-  p.h = (size_t)std::min<int64_t>(16 * t, 128 * ftk_num_cus() + t) * rank_pad * 4;
+  // no fewer than parts * t, here and for every smaller t
+  p.h = (size_t)std::min<int64_t>(16 * t, 32 * cus + t) * rank_pad * 4;
   p.order = (p.h + 255) & ~(size_t)255;
   p.list = (p.order + (size_t)t * 4 + 255) & ~(size_t)255;
   p.total = p.list + 16 + (size_t)(t / LORA_TILE + some) * 16;
@@ -379,7 +493,9 @@ static LoraPlan lora_plan(int64_t t, int64_t k, int rank, int64_t adapters) {
 
 template <int TX, int TW>
 static hipError_t lora_shrink(const LoraIo& io, dim3 grid, hipStream_t st) {
-  lora_shrink_kernel<TX, TW><<<grid, 256, 0, st>>>(io);
+  if (io.rank <= 16) lora_shrink_kernel<TX, TW, 1><<<grid, 256, io.words, st>>>(io);
+  else if (io.rank <= 32) lora_shrink_kernel<TX, TW, 2><<<grid, 256, io.words, st>>>(io);
+  else lora_shrink_kernel<TX, TW, 4><<<grid, 256, io.words, st>>>(io);
   return hipGetLastError();
 }
 template <int TW>
@@ -387,13 +503,20 @@ static hipError_t lora_shrink_x(int tx, const LoraIo& io, dim3 grid, hipStream_t
   if (tx == FT_F32) return lora_shrink<FT_F32, TW>(io, grid, st);
   return tx == FT_F16 ? lora_shrink<FT_F16, TW>(io, grid, st) : lora_shrink<FT_BF16, TW>(io, grid, st);
 }
-template <int TW>
+// columns of a workgroup; ranks past 128 fill the registers with fewer
+static int lora_cols(bool wide, int rank) { return 64 * (!wide || rank > 128 ? 1 : rank > 64 ? 2 : 4); }
+template <int TW, int C, bool ONE>
 static hipError_t lora_expand(const LoraIo& io, dim3 grid, hipStream_t st) {
-  if (io.rank <= 32) lora_expand_kernel<TW, 1><<<grid, 256, 0, st>>>(io);
-  else if (io.rank <= 64) lora_expand_kernel<TW, 2><<<grid, 256, 0, st>>>(io);
-  else if (io.rank <= 128) lora_expand_kernel<TW, 4><<<grid, 256, 0, st>>>(io);
-  else lora_expand_kernel<TW, 8><<<grid, 256, 0, st>>>(io);
+  if (io.rank <= 32) lora_expand_kernel<TW, 1, C, ONE><<<grid, 256, io.words, st>>>(io);
+  else if (io.rank <= 64) lora_expand_kernel<TW, 2, C, ONE><<<grid, 256, io.words, st>>>(io);
+  else if (io.rank <= 128) lora_expand_kernel<TW, 4, C == 1 ? 1 : 2, ONE><<<grid, 256, io.words, st>>>(io);
+  else lora_expand_kernel<TW, 8, 1, true><<<grid, 256, io.words, st>>>(io);
   return hipGetLastError();
+}
+template <int TW>
+static hipError_t lora_expand_c(bool wide, bool one, const LoraIo& io, dim3 grid, hipStream_t st) {
+  if (one) return wide ? lora_expand<TW, 4, true>(io, grid, st) : lora_expand<TW, 1, true>(io, grid, st);
+  return wide ? lora_expand<TW, 4, false>(io, grid, st) : lora_expand<TW, 1, false>(io, grid, st);
 }
 
 }  // namespace ftk
@@ -422,11 +545,6 @@ hipError_t ftk_launch_lora(const LoraArgs& a, void* scratch, hipStream_t st) {
   io.rank = a.rank;
   io.adapters = (int)a.adapters;
   io.rank_pad = (a.rank + 15) / 16 * 16;
-  const int64_t wx = a.xtype == FT_F32 ? 4 : 8, ww = a.wtype == FT_F32 ? 4 : 8;
-  io.vec_x = ((uintptr_t)a.x & 15) == 0 && a.ldx % wx == 0;
-  io.vec_a = ((uintptr_t)a.a & 15) == 0 && a.k % ww == 0;
-  io.vec_b = ((uintptr_t)a.b & 15) == 0 && a.rank % ww == 0;
-  io.vec_y = (((uintptr_t)a.y | (uintptr_t)a.out) & 15) == 0 && (a.ldy % 4 == 0 || !a.y) && a.ldo % 4 == 0;
   io.copies = a.out != a.y;
   io.parts = p.parts;
   io.part_k = p.part_k;
@@ -434,24 +552,29 @@ hipError_t ftk_launch_lora(const LoraArgs& a, void* scratch, hipStream_t st) {
   io.order = nullptr;
   io.tiles = nullptr;
   io.n_tiles = nullptr;
+  io.words = p.sorts ? 0 : (int)(a.adapters + 1) * 4;
   hipError_t e = hipSuccess;
-  if (a.t > 64) {
+  if (p.sorts) {
     io.order = (int32_t*)(s + p.order);
     io.n_tiles = (int32_t*)(s + p.list);
     io.tiles = (int4*)(s + p.list + 16);
-    lora_plan_kernel<<<1, 1024, (size_t)(a.adapters + 1) * 4, st>>>(a.ids, io.t, io.adapters, (int32_t*)io.order, (int4*)io.tiles,
+    lora_plan_kernel<<<1, 1024, (size_t)(a.adapters + 1) * 4, st>>>(a.ids, a.ranks, a.rank, io.t, io.adapters, (int32_t*)io.order, (int4*)io.tiles,
                                                                      (int32_t*)io.n_tiles);
     e = hipGetLastError();
   }
-  const dim3 shrink((unsigned)p.tiles, (unsigned)p.parts, (unsigned)((a.rank + LORA_RANKS - 1) / LORA_RANKS));
-  const dim3 expand((unsigned)((a.n + LORA_COLS - 1) / LORA_COLS), (unsigned)p.tiles);   // tiles < 2^15: t is at most 2^20
+  const dim3 shrink((unsigned)p.sixteens, (unsigned)p.parts, (unsigned)((a.rank + LORA_RANKS - 1) / LORA_RANKS));
+  // 64 columns a wave where that still gives every CU a workgroup
+  const bool wide = p.likely * a.n >= 256 * (int64_t)ftk_num_cus();
+  const bool one = p.likely * 16 >= a.t;
+  const int cols = lora_cols(wide, a.rank);
+  const dim3 expand((unsigned)((a.n + cols - 1) / cols), (unsigned)p.tiles);   // tiles < 2^15: t is at most 2^20
   if (e == hipSuccess)
     e = a.wtype == FT_F32   ? lora_shrink_x<FT_F32>(a.xtype, io, shrink, st)
         : a.wtype == FT_F16 ? lora_shrink_x<FT_F16>(a.xtype, io, shrink, st)
                             : lora_shrink_x<FT_BF16>(a.xtype, io, shrink, st);
   if (e == hipSuccess)
-    e = a.wtype == FT_F32   ? lora_expand<FT_F32>(io, expand, st)
-        : a.wtype == FT_F16 ? lora_expand<FT_F16>(io, expand, st)
-                            : lora_expand<FT_BF16>(io, expand, st);
+    e = a.wtype == FT_F32   ? lora_expand_c<FT_F32>(wide, one, io, expand, st)
+        : a.wtype == FT_F16 ? lora_expand_c<FT_F16>(wide, one, io, expand, st)
+                            : lora_expand_c<FT_BF16>(wide, one, io, expand, st);
   return e;
 }

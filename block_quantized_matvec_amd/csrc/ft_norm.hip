@@ -22,12 +22,11 @@ namespace ftk {
 struct NormSide {
   const void* x;
   int64_t ld;
-  int vec;   // rows stay 16-byte aligned
 };
 struct NormIo {
   NormSide x, residual, gate, r, out;   // x.x null: not there
   const float *post_weight, *post_bias, *weight, *bias;
-  int vec_w, post, layer, ftype, act, scaled, width;
+  int post, layer, act, scaled, width;
   float scale;
   double eps, inv_width;
   uint8_t* xq;
@@ -35,41 +34,68 @@ struct NormIo {
   int64_t rows;
 };
 
-// eight elements of a row from e on (those past the width: 0), as 32-bit words
-__device__ __forceinline__ void norm_load(int type, const NormSide& s, int64_t row, int e, int width, u32x4 (&raw)[2]) {
-  const int64_t at[1] = {row * s.ld + e};
-  if (e + 8 <= width) {
-    u32x4 r[1][2];
-    kv_load_raw<1>(type, s.x, at, s.vec, r);
-    raw[0] = r[0][0];
-    if (type == FT_F32) raw[1] = r[0][1];
-    return;
-  }
-  raw[0] = raw[1] = u32x4{0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (e + i >= width) break;
-    if (type == FT_F32) raw[i >> 2][i & 3] = ((const uint32_t*)s.x)[at[0] + i];
-    else raw[0][i >> 1] |= (uint32_t)((const uint16_t*)s.x)[at[0] + i] << (16 * (i & 1));
-  }
-}
-__device__ __forceinline__ void norm_store(int type, const NormSide& s, int64_t row, int e, int width, const float (&v)[8]) {
+// Rows need no alignment past their elements': the vector loads and stores below are whole
+// whatever their address (a row of 5002 fp16 starts at any fourth byte).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+template <int TYPE> constexpr int NORM_WORDS = TYPE == FT_F32 ? 2 : 1;   // of 16 bytes for eight elements
+
+// eight elements of a row from e on; TAIL: those past the width are 0
+template <int TYPE, bool TAIL>
+__device__ __forceinline__ void norm_load(const NormSide& s, int64_t row, int e, int width, u32x4 (&raw)[NORM_WORDS<TYPE>]) {
   const int64_t at = row * s.ld + e;
-  void* base = const_cast<void*>(s.x);
-  if (e + 8 <= width) {
-    kv_store_n<8>(type, base, at, s.vec, v);
+  if (!TAIL || e + 8 <= width) {
+    const u32x4_any* p = (const u32x4_any*)((const uint8_t*)s.x + at * (TYPE == FT_F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < NORM_WORDS<TYPE>; ++i) raw[i] = p[i];
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (e + i >= width) break;
-    if (type == FT_F32) ((float*)base)[at + i] = v[i];
-    else ((uint16_t*)base)[at + i] = (uint16_t)float_bits16x2(type, v[i], v[i]);
+    uint32_t u = 0;
+    if (e + i < width) u = TYPE == FT_F32 ? ((const uint32_t*)s.x)[at + i] : ((const uint16_t*)s.x)[at + i];
+    if constexpr (TYPE == FT_F32) raw[i >> 2][i & 3] = u;
+    else raw[0][i >> 1] = i & 1 ? raw[0][i >> 1] | (u << 16) : u;
   }
 }
-__device__ __forceinline__ void norm_weights(const float* p, bool vec, int e, int width, float (&w)[8]) {
-  if (vec && e + 8 <= width) {
-    kv_load8(FT_F32, p, e, true, w);
+template <int TYPE>
+__device__ __forceinline__ void norm_values(const u32x4 (&raw)[NORM_WORDS<TYPE>], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (TYPE == FT_F32) v[i] = __uint_as_float(raw[i >> 2][i & 3]);
+    else if constexpr (TYPE == FT_BF16) v[i] = __uint_as_float(i & 1 ? raw[0][i >> 1] & 0xFFFF0000u : raw[0][i >> 1] << 16);
+    else v[i] = h2f((raw[0][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+  }
+}
+template <int TYPE, bool TAIL>
+__device__ __forceinline__ void norm_store(const NormSide& s, int64_t row, int e, int width, const float (&v)[8]) {
+  const int64_t at = row * s.ld + e;
+  uint8_t* base = (uint8_t*)const_cast<void*>(s.x) + at * (TYPE == FT_F32 ? 4 : 2);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (TYPE == FT_F32) w[i] = __float_as_uint(v[i]);
+    else if (!(i & 1)) w[i >> 1] = float_bits16x2(TYPE, v[i], v[i + 1]);
+  }
+  if (!TAIL || e + 8 <= width) {
+#pragma unroll
+    for (int i = 0; i < NORM_WORDS<TYPE>; ++i) ((u32x4_any*)base)[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (e + i < width) {
+      if constexpr (TYPE == FT_F32) ((uint32_t*)base)[i] = w[i];
+      else ((uint16_t*)base)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+template <bool TAIL>
+__device__ __forceinline__ void norm_weights(const float* p, int e, int width, float (&w)[8]) {
+  if (!TAIL || e + 8 <= width) {
+    const f32x4 a = ((const f32x4_any*)(p + e))[0], b = ((const f32x4_any*)(p + e))[1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = i < 4 ? a[i & 3] : b[i & 3];
     return;
   }
 #pragma unroll
@@ -119,93 +145,96 @@ __device__ __forceinline__ void norm_q8_k(const float (&v)[8], int l32, uint8_t*
   if (l32 == 0) *(float*)ob = d;
 }
 
-// sum over the lanes that share a row: a wave, or the workgroup (s_sum: a slot per wave and use)
-template <int THREADS>
+// sum over the lanes that share a row: a wave, or the workgroup (s_sum: a slot per wave, another array for
+// every use)
+template <bool WAVE>
 __device__ __forceinline__ double norm_sum(double s, double* s_sum) {
   s = lanes_sum(s, 6);
-  if constexpr (THREADS > 64) {
-    if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = s;
+  if constexpr (!WAVE) {
+    const int lane = threadIdx.x & 63;
+    if (lane == 0) s_sum[wave_id()] = s;
     __syncthreads();
-    s = 0.0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 64; ++i) s += s_sum[i];
+    s = lanes_sum((lane & 15) < (int)(blockDim.x >> 6) ? s_sum[lane & 15] : 0.0, 4);
   }
   return s;
 }
 
-// THREADS threads share a row, C chunks of eight elements each.  With 64 a workgroup holds four rows.
-template <int THREADS, int C>
-__global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS)
+// A workgroup of up to 1024 threads has a row, C chunks of eight elements per thread; with WAVE it
+// has four, one a wave.  TAIL: the width is no multiple of eight.
+template <int TYPE, int C, bool WAVE, bool TAIL>
+__global__ void __launch_bounds__(WAVE ? 256 : 1024, C == 1 ? 8 : 4)
 norm_kernel(NormIo io) {
-  constexpr int WAVES = THREADS / 64;
-  __shared__ double s_sum[4][WAVES];
-  const int tid = threadIdx.x & (THREADS - 1);
+  constexpr int W = NORM_WORDS<TYPE>;
+  __shared__ double s_sum[4][16];
+  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x, threads = C == 1 ? 0 : 1024;
   const int64_t wg = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-  const int64_t row = THREADS == 64 ? wg * 4 + wave_id() : wg;
+  const int64_t row = WAVE ? wg * 4 + wave_id() : wg;
   if (row >= io.rows) return;   // a whole workgroup, or waves that no barrier waits for
   const int width = io.width;
-  u32x4 rx[C][2], rr[C][2], rg[C][2];
+  const auto at = [&](int c) { return 8 * (tid + threads * c); };
+  u32x4 rx[C][W], rr[C][W], rg[C][W];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int e = 8 * (tid + THREADS * c);
-    if (e < width) norm_load(io.ftype, io.x, row, e, width, rx[c]);
-    else rx[c][0] = rx[c][1] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < W; ++i) rx[c][i] = rr[c][i] = rg[c][i] = u32x4{0, 0, 0, 0};
+    if (at(c) < width) norm_load<TYPE, TAIL>(io.x, row, at(c), width, rx[c]);
   }
-  if (io.residual.x)
+  constexpr bool AHEAD = C <= 2;   // room for every load that is still to come
+  if (AHEAD && io.residual.x)
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = 8 * (tid + THREADS * c);
-      if (e < width) norm_load(io.ftype, io.residual, row, e, width, rr[c]);
-    }
-  if (io.gate.x)
+    for (int c = 0; c < C; ++c)
+      if (at(c) < width) norm_load<TYPE, TAIL>(io.residual, row, at(c), width, rr[c]);
+  if (AHEAD && io.gate.x)
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = 8 * (tid + THREADS * c);
-      if (e < width) norm_load(io.ftype, io.gate, row, e, width, rg[c]);
-    }
+    for (int c = 0; c < C; ++c)
+      if (at(c) < width) norm_load<TYPE, TAIL>(io.gate, row, at(c), width, rg[c]);
   float v[C][8];
 #pragma unroll
-  for (int c = 0; c < C; ++c) kv_raw_values(io.ftype, rx[c], v[c]);
+  for (int c = 0; c < C; ++c) norm_values<TYPE>(rx[c], v[c]);
 
-  // v <- norm(v) w + b, elements past the width left at 0
+  // v <- norm(v) weight + bias; elements past the width are 0 before it, and anything after
   auto norm = [&](const float* weight, const float* bias, double* sums) {
-    double s = 0.0, mean = 0.0;
+    float w[C][8];
+    if (AHEAD && weight)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (at(c) < width) norm_weights<TAIL>(weight, at(c), width, w[c]);
+    double s = 0.0;
     if (io.layer) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) s += (double)v[c][i];
-      mean = norm_sum<THREADS>(s, sums) * io.inv_width;
+      const double mean = norm_sum<WAVE>(s, sums) * io.inv_width;
       s = 0.0;
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const double d = (double)v[c][i] - mean;
-          if (8 * (tid + THREADS * c) + i < width) s = fma(d, d, s);
+          if (at(c) + i < width) s = fma(d, d, s);
           v[c][i] = (float)d;
         }
     } else {
 #pragma unroll
       for (int c = 0; c < C; ++c) s += sum_squares(v[c]);
     }
-    const float r = rstd_of(fma(norm_sum<THREADS>(s, sums + WAVES), io.inv_width, io.eps));
+    const float r = rstd_of(fma(norm_sum<WAVE>(s, sums + 16), io.inv_width, io.eps));
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int e = 8 * (tid + THREADS * c);
-      if (e >= width) continue;
+      if (at(c) >= width) continue;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * r;
-      float w[8];
       if (weight) {
-        norm_weights(weight, io.vec_w, e, width, w);
+        if (!AHEAD) norm_weights<TAIL>(weight, at(c), width, w[c]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * w[i];
+        for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * w[c][i];
       }
       if (bias) {
-        norm_weights(bias, io.vec_w, e, width, w);
+        float b[8];
+        norm_weights<TAIL>(bias, at(c), width, b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] + w[i];
+        for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] + b[i];
       }
     }
   };
@@ -213,15 +242,11 @@ norm_kernel(NormIo io) {
   if (io.post) norm(io.post_weight, io.post_bias, s_sum[0]);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int e = 8 * (tid + THREADS * c);
-    if (e >= width) {   // a layer's norm leaves -mean there
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = 0.0f;
-      continue;
-    }
+    const int e = at(c);
     float o[8];
     if (io.gate.x) {
-      kv_raw_values(io.ftype, rg[c], o);
+      if (!AHEAD && e < width) norm_load<TYPE, TAIL>(io.gate, row, e, width, rg[c]);
+      norm_values<TYPE>(rg[c], o);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * o[i];
     }
@@ -229,25 +254,25 @@ norm_kernel(NormIo io) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * io.scale;
     if (io.residual.x) {
-      kv_raw_values(io.ftype, rr[c], o);
+      if (!AHEAD && e < width) norm_load<TYPE, TAIL>(io.residual, row, e, width, rr[c]);
+      norm_values<TYPE>(rr[c], o);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = o[i] + v[c][i];
     }
-    if (e + 8 > width)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e + i >= width) v[c][i] = 0.0f;
-    if (io.r.x) norm_store(io.ftype, io.r, row, e, width, v[c]);
+    for (int i = 0; i < 8; ++i)   // a norm leaves -mean or a bias past the width
+      if (TAIL ? e + i >= width : e >= width) v[c][i] = 0.0f;
+    if (io.r.x && e < width) norm_store<TYPE, TAIL>(io.r, row, e, width, v[c]);
   }
   if (!io.out.x && !io.xq) return;
   norm(io.weight, io.bias, s_sum[2]);
   uint8_t* xq = io.xq + row * io.xq_row;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int g = tid + THREADS * c, e = 8 * g;
-    if (e >= width) continue;
-    if (io.out.x) norm_store(io.ftype, io.out, row, e, width, v[c]);
-    if (io.xq) {   // whole blocks: a block's lanes are all here
+    const int g = tid + threads * c;
+    if (at(c) >= width) continue;
+    if (io.out.x) norm_store<TYPE, TAIL>(io.out, row, at(c), width, v[c]);
+    if (!TAIL && io.xq) {   // whole blocks: a block's lanes are all here
       if (io.act == FT_Q8_1) q8_1_part(v[c], g & 3, xq + (g >> 2) * 36);
       else if (io.act == FT_Q8_0) norm_q8_0(v[c], g & 3, xq + (g >> 2) * 34);
       else norm_q8_k(v[c], g & 31, xq + (g >> 5) * 292);
@@ -255,16 +280,24 @@ norm_kernel(NormIo io) {
   }
 }
 
-template <int THREADS, int C>
+template <int TYPE, int C, bool WAVE>
 static hipError_t norm_launch(const NormIo& io, hipStream_t st) {
-  const int64_t groups = THREADS == 64 ? (io.rows + 3) / 4 : io.rows;
+  const int64_t groups = WAVE ? (io.rows + 3) / 4 : io.rows;
   const int64_t x = groups < (1 << 20) ? groups : 1 << 20;   // fewer than 2^32 threads along a dimension
-  norm_kernel<THREADS, C><<<dim3((unsigned)x, (unsigned)((groups + x - 1) / x)), THREADS < 256 ? 256 : THREADS, 0, st>>>(io);
+  const dim3 grid((unsigned)x, (unsigned)((groups + x - 1) / x));
+  const int block = WAVE ? 256 : C > 1 ? 1024 : (io.width + 511) / 512 * 64;
+  if (io.width % 8) norm_kernel<TYPE, C, WAVE, true><<<grid, block, 0, st>>>(io);
+  else norm_kernel<TYPE, C, WAVE, false><<<grid, block, 0, st>>>(io);
   return hipGetLastError();
 }
 
-static NormSide norm_side(const void* x, int64_t ld, int ftype) {
-  return {x, ld, ((uintptr_t)x & 15) == 0 && ld % (ftype == FT_F32 ? 4 : 8) == 0};
+// a chunk per thread while a workgroup's threads last; rows of at most 512 go to single waves
+template <int TYPE>
+static hipError_t norm_pick(const NormIo& io, hipStream_t st) {
+  if (io.width <= 512) return norm_launch<TYPE, 1, true>(io, st);
+  if (io.width <= 8192) return norm_launch<TYPE, 1, false>(io, st);
+  if (io.width <= 16384) return norm_launch<TYPE, 2, false>(io, st);
+  return norm_launch<TYPE, 4, false>(io, st);
 }
 
 }  // namespace ftk
@@ -272,19 +305,17 @@ static NormSide norm_side(const void* x, int64_t ld, int ftype) {
 hipError_t ftk_launch_norm(const NormArgs& a, hipStream_t st) {
   using namespace ftk;
   NormIo io;
-  io.x = norm_side(a.x, a.ldx, a.ftype);
-  io.residual = norm_side(a.residual, a.ld_residual, a.ftype);
-  io.gate = norm_side(a.gate, a.ld_gate, a.ftype);
-  io.r = norm_side(a.r, a.ld_r, a.ftype);
-  io.out = norm_side(a.out, a.ld_out, a.ftype);
+  io.x = {a.x, a.ldx};
+  io.residual = {a.residual, a.ld_residual};
+  io.gate = {a.gate, a.ld_gate};
+  io.r = {a.r, a.ld_r};
+  io.out = {a.out, a.ld_out};
   io.post_weight = a.post_weight;
   io.post_bias = a.post_bias;
   io.weight = a.weight;
   io.bias = a.bias;
-  io.vec_w = (((uintptr_t)a.post_weight | (uintptr_t)a.post_bias | (uintptr_t)a.weight | (uintptr_t)a.bias) & 15) == 0;
   io.post = a.post;
   io.layer = a.layer;
-  io.ftype = a.ftype;
   io.act = a.act;
   io.scaled = a.scale != 1.0f;
   io.width = (int)a.width;
@@ -294,12 +325,6 @@ hipError_t ftk_launch_norm(const NormArgs& a, hipStream_t st) {
   io.xq = (uint8_t*)a.xq;
   io.xq_row = a.xq_row;
   io.rows = a.rows;
-  // the fewest threads whose lanes hold a row in four chunks, but a chunk each while rows are few
-  const int64_t w = a.width;
-  if (w <= 512) return norm_launch<64, 1>(io, st);
-  if (w <= 2048) return norm_launch<256, 1>(io, st);
-  if (w <= 4096) return norm_launch<256, 2>(io, st);
-  if (w <= 8192) return norm_launch<256, 4>(io, st);
-  if (w <= 16384) return norm_launch<512, 4>(io, st);
-  return norm_launch<1024, 4>(io, st);
+  if (a.ftype == FT_F32) return norm_pick<FT_F32>(io, st);
+  return a.ftype == FT_F16 ? norm_pick<FT_F16>(io, st) : norm_pick<FT_BF16>(io, st);
 }

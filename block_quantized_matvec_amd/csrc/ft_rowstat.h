@@ -18,14 +18,22 @@ __device__ __forceinline__ double xchg_d(double v) {
   const uint32_t hi = __float_as_uint(xchg<S>(__uint_as_float((uint32_t)(u >> 32))));
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
+// s plus the other half's (or the other 16 lanes' of a half): both registers of the exchange hold one side
+__device__ __forceinline__ double halves_sum(double v, bool wide) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+  const auto a = wide ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false) : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+  const auto b = wide ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false) : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+  return __builtin_bit_cast(double, ((uint64_t)b[0] << 32) | a[0]) + __builtin_bit_cast(double, ((uint64_t)b[1] << 32) | a[1]);
+}
 // sum over 1 << log_lanes aligned lanes (uniform over the wave), in all of them
 __device__ __forceinline__ double lanes_sum(double s, int log_lanes) {
   if (log_lanes > 0) s += xchg_d<1>(s);
   if (log_lanes > 1) s += xchg_d<2>(s);
   if (log_lanes > 2) s += xchg_d<4>(s);
   if (log_lanes > 3) s += xchg_d<8>(s);
-  if (log_lanes > 4) s += xchg_d<16>(s);
-  if (log_lanes > 5) s += xchg_d<32>(s);
+  if (log_lanes > 4) s = halves_sum(s, false);
+  if (log_lanes > 5) s = halves_sum(s, true);
   return s;
 }
 template <int N>

@@ -1,4 +1,6 @@
 """Helpers for the GPU parity tests (compare the HIP path with the oracle)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -33,6 +35,14 @@ def check_fp32(y, r, what="", rel=REL, nmse=NMSE):
     nm = np.sum((y - r) ** 2) / max(np.sum(r ** 2), 1e-300)
     assert err <= rel and nm <= nmse, f"{what}: normwise max rel {err:.3e}, NMSE {nm:.3e}"
     return err, nm
+
+
+def own_stream():
+    """A stream of its own, whose scratch pool is empty (torch hands the same few streams out in turn)."""
+    from block_quantized_matvec_amd import ft
+    handle = ctypes.c_void_p()
+    assert ft.lib().hipStreamCreate(ctypes.byref(handle)) == 0
+    return torch.cuda.ExternalStream(handle.value)
 
 
 def log(msg):

@@ -5,7 +5,7 @@ import torch
 
 from block_quantized_matvec_amd import ft
 from tests import layer_ref as ref
-from tests.gpu_util import dev, host, need_gpu
+from tests.gpu_util import dev, host, need_gpu, own_stream
 from tests.test_gpu_host_threads import together
 
 pytestmark = pytest.mark.gpu
@@ -139,7 +139,7 @@ def test_nothing_to_do():
 def test_two_graphs_with_workspaces(t):
     """Captured on one stream, each with its own workspace; replayed with other ids and rows."""
     need_gpu()
-    s, sets = torch.cuda.Stream(), []
+    s, sets = own_stream(), []
     need = ft.lora_scratch_bytes(t, 1024, 5, 16)
     for i in range(2):
         x, a, b, y, ids, sc = case(t, 1024, 300, 5, 16, seed=60 + i)
@@ -165,7 +165,7 @@ def test_two_graphs_with_workspaces(t):
 def test_capture_needs_scratch():
     need_gpu()
     x, a, b, y, ids, sc = case(9, 1024, 300, 5, 16)
-    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()   # a new stream: its pool is empty
+    s, graph = own_stream(), torch.cuda.CUDAGraph()
     out = torch.zeros(9, 300, device="cuda")
     torch.cuda.synchronize()
     with torch.cuda.graph(graph, stream=s):
@@ -193,7 +193,7 @@ def test_streams_and_threads():
         x, a, b, y, ids, sc = case(30 + 40 * seed, 512, 200, 4, 16, seed=seed)
         calls.append(lambda x=x, a=a, b=b, ids=ids, y=y: ft.lora(x, a, b, ids, y=y))
     together(calls)
-    streams = [torch.cuda.Stream() for _ in calls]
+    streams = [own_stream() for _ in calls]
     torch.cuda.synchronize()
     for _ in range(5):
         outs = []

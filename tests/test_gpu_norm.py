@@ -7,7 +7,7 @@ import torch
 import oracle
 from block_quantized_matvec_amd import ft
 from tests import layer_ref as ref
-from tests.gpu_util import dev, host, need_gpu
+from tests.gpu_util import dev, host, need_gpu, own_stream
 
 pytestmark = pytest.mark.gpu
 
@@ -191,7 +191,7 @@ def test_captured():
     need_gpu()
     x, res, w = lines(3, 4096, "f32", 26), lines(3, 4096, "f32", 27), dev(vector(4096, 28))
     r, xq = torch.empty_like(res), torch.empty(3, ft.row_bytes("Q8_1", 4096), dtype=torch.uint8, device="cuda")
-    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s, graph = own_stream(), torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph, stream=s):
         ft.norm(x, weight=w, residual=res, act="Q8_1", r=r, xq=xq, stream=s)

@@ -5,7 +5,7 @@ import torch
 
 from block_quantized_matvec_amd import ft
 from tests import layer_ref as ref
-from tests.gpu_util import dev, host, need_gpu
+from tests.gpu_util import dev, host, need_gpu, own_stream
 
 pytestmark = pytest.mark.gpu
 
@@ -201,7 +201,7 @@ def test_captured():
     fused, (pos, tab) = rows(t, heads + 2 * hk, dim, "f32"), setup(t, dim)
     pos, tab, slots = dev(pos), dev(tab), torch.tensor([3, 40, 17, -1], device="cuda")
     cache, out = cleared(4, page, hk, dim, "Q8_0", "Q8_0"), torch.empty(t, heads, dim, device="cuda")
-    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s, graph = own_stream(), torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph, stream=s):
         ft.kv_store_rope(cache, fused[:, :heads], fused[:, heads:heads + hk], fused[:, heads + hk:], slots, pos, tab, q_out=out, stream=s)
