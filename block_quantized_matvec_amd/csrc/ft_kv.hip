@@ -31,10 +31,11 @@ namespace ftk {
 // grid: (token tiles, heads, 2): z = 0 the keys, 1 the values
 template <int TK, int TV, int NB>
 __global__ void __launch_bounds__(256)
-kv_store_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int64_t t) {
+kv_store_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int64_t t, int span) {
   __shared__ KvTokens s_tok;
   __shared__ __align__(16) uint8_t s_tile[NB * 32 * KV_PITCH];
-  const int64_t t0 = (int64_t)blockIdx.x * KV_TILE;
+  const int64_t t0 = (int64_t)blockIdx.x * span;
+  t = min(t, t0 + span);
   if (blockIdx.z == 0) kv_store_side<TK, NB, false>(k, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
   else kv_store_side<TV, NB, true>(v, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
 }
@@ -125,10 +126,11 @@ __device__ __forceinline__ void kv_load_side(const KvIo& io, int ftype, const in
 
 template <int TK, int TV, int NB>
 __global__ void __launch_bounds__(256)
-kv_load_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int64_t t, int first) {
+kv_load_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int64_t t, int span, int first) {
   __shared__ KvTokens s_tok;
   __shared__ __align__(16) uint8_t s_tile[NB * 32 * KV_PITCH];
-  const int64_t t0 = (int64_t)blockIdx.x * KV_TILE;
+  const int64_t t0 = (int64_t)blockIdx.x * span;
+  t = min(t, t0 + span);
   if (blockIdx.z + first == 0) kv_load_side<TK, NB, false>(k, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
   else kv_load_side<TV, NB, true>(v, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
 }
@@ -136,13 +138,14 @@ kv_load_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int
 template <int TK, int TV, int NB>
 static hipError_t kv_launch(const KvArgs& a, bool load, hipStream_t st) {
   const KvIo k = kv_io(a, false), v = kv_io(a, true);
-  const unsigned tiles = (unsigned)((a.t + KV_TILE - 1) / KV_TILE);
+  const int span = kv_span(a.t);
+  const unsigned tiles = (unsigned)((a.t + span - 1) / span);
   if (!load) {
-    kv_store_kernel<TK, TV, NB><<<dim3(tiles, a.heads, 2), 256, 0, st>>>(k, v, a.ftype, a.slots, a.t);
+    kv_store_kernel<TK, TV, NB><<<dim3(tiles, a.heads, 2), 256, 0, st>>>(k, v, a.ftype, a.slots, a.t, span);
   } else {
     const int first = a.k ? 0 : 1;
-    kv_load_kernel<TK, TV, NB><<<dim3(tiles, a.heads, (a.k ? 1 : 0) + (a.v ? 1 : 0)), 256, 0, st>>>(k, v, a.ftype, a.slots,
-                                                                                                  a.t, first);
+    kv_load_kernel<TK, TV, NB><<<dim3(tiles, a.heads, (a.k ? 1 : 0) + (a.v ? 1 : 0)), 256, 0, st>>>(k, v, a.ftype, a.slots, a.t, span,
+                                                                                                  first);
   }
   return hipGetLastError();
 }

@@ -210,13 +210,14 @@ rope_kernel(RopeTurn c, RopeRows rows, RopeOut out, uint32_t tasks) {
 template <int TK, int TV, int NB, int HC>
 __global__ void __launch_bounds__(256)
 kv_store_rope_kernel(RopeTurn c, RopeRows k, RopeRows q, RopeOut out, KvIo kio, KvIo vio, const int64_t* __restrict__ slots,
-                     uint32_t v_groups, uint32_t k_tasks, uint32_t tasks) {
+                     int span, uint32_t v_groups, uint32_t k_tasks, uint32_t tasks) {
   __shared__ KvTokens s_tok;
   __shared__ __align__(16) uint8_t s_tile[NB * 32 * KV_PITCH > 8192 ? NB * 32 * KV_PITCH : 8192];
   const uint32_t wg = rope_group();
   if (wg < v_groups) {
     const uint32_t tile = wg / vio.heads;
-    kv_store_side<TV, NB, true>(vio, c.ftype, slots, c.t, (int64_t)tile * KV_TILE, (int)(wg - tile * vio.heads), s_tok, s_tile);
+    const int64_t t0 = (int64_t)tile * span;
+    kv_store_side<TV, NB, true>(vio, c.ftype, slots, min(c.t, t0 + span), t0, (int)(wg - tile * vio.heads), s_tok, s_tile);
     return;
   }
   uint32_t task = (wg - v_groups) * 4 + wave_id();
@@ -332,9 +333,10 @@ static hipError_t store_launch(const RopeArgs& a, hipStream_t st) {
   const RopeRows k = rope_rows_of(a.kv.k, a.kv.k_token, a.kv.k_head, a.kv.heads, a.k_weight, a, HC);
   const RopeOut out = {a.out, a.out_token, a.out_head, rope_vec(a.out, a.out_token, a.out_head, a.dim, a.ftype)};
   const int64_t per = 64 >> c.log_lanes, groups = (a.t + per - 1) / per;
-  const int64_t v_groups = (a.t + KV_TILE - 1) / KV_TILE * a.kv.heads, k_tasks = groups * k.chunks, tasks = k_tasks + groups * q.chunks;
+  const int span = kv_span(a.t);
+  const int64_t v_groups = (a.t + span - 1) / span * a.kv.heads, k_tasks = groups * k.chunks, tasks = k_tasks + groups * q.chunks;
   kv_store_rope_kernel<TK, TV, NB, HC><<<rope_grid(v_groups + (tasks + 3) / 4), 256, 0, st>>>(
-      c, k, q, out, kv_io(a.kv, false), kv_io(a.kv, true), a.kv.slots, (uint32_t)v_groups, (uint32_t)k_tasks, (uint32_t)tasks);
+      c, k, q, out, kv_io(a.kv, false), kv_io(a.kv, true), a.kv.slots, span, (uint32_t)v_groups, (uint32_t)k_tasks, (uint32_t)tasks);
   return hipGetLastError();
 }
 

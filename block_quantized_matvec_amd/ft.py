@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch  # loaded first so libft.so binds to the same HIP runtime as torch
 
@@ -20,6 +21,7 @@ TYPES = {"Q4_0": 0, "Q8_0": 1, "Q4_K": 2, "Q5_K": 3, "Q6_K": 4, "MXFP4": 5, "Q8_
          "Q2_K": 8, "Q3_K": 9, "Q4_1": 10, "Q5_0": 11, "Q5_1": 12}
 OPS = {"quantize": 0, "dequant": 1, "mmvq": 2, "moe_vec": 3, "grouped": 4, "block_dots": 5, "kv_cache": 6}
 FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ACT_BLOCKS = {"Q8_1": (32, 36), "Q8_0": (32, 34), "Q8_K": (256, 292)}  # activation formats: elements and bytes of a block
 STATUS = {0: "FT_OK", 1: "FT_ERR_INVALID_ARG", 2: "FT_ERR_UNSUPPORTED", 3: "FT_ERR_SHAPE",
           4: "FT_ERR_ALIGNMENT", 5: "FT_ERR_NO_SCRATCH", 6: "FT_ERR_HIP"}
 
@@ -81,6 +83,13 @@ class _LoraOpts(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+# the same structures packed (a fifth of the time that a Structure takes): ft_rotation, ft_qkv_rows, ft_norm_opts,
+# ft_lora_opts
+_pack_rotation = struct.Struct("@PPqqi0P").pack
+_pack_rows = struct.Struct("@PqqqPPqqPqqPPqqd").pack
+_pack_norm = struct.Struct("@PqPqiPPfidPPPqPqiP").pack
+_pack_lora = struct.Struct("@PPPN").pack
+
 _P, _I64 = ctypes.c_void_p, ctypes.c_int64
 
 EXPORTS = {
@@ -130,13 +139,12 @@ EXPORTS = {
     "ft_attn_kv_scratch_bytes": (ctypes.c_size_t, [ctypes.POINTER(_KvCache), _I64, _I64, _I64, _I64,
                                                    ctypes.POINTER(_AttnOpts)]),
     "ft_rope_table": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_double, _P, _P]),
-    "ft_rope": (ctypes.c_int, [ctypes.POINTER(_Rotation), ctypes.c_int, _P, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_double, _P,
+    "ft_rope": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_double, _P,
                                _I64, _I64, _P]),
-    "ft_kv_store_rope": (ctypes.c_int, [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rotation), ctypes.c_int,
-                                        ctypes.POINTER(_QkvRows), _P, _I64, _P]),
-    "ft_norm": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, ctypes.POINTER(_NormOpts), _P]),
+    "ft_kv_store_rope": (ctypes.c_int, [ctypes.POINTER(_KvCache), _P, ctypes.c_int, _P, _P, _I64, _P]),
+    "ft_norm": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, _P, _P]),
     "ft_lora": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, ctypes.c_int, _P, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64,
-                               ctypes.POINTER(_LoraOpts), _P]),
+                               _P, _P]),
     "ft_lora_scratch_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
     "ft_scratch_reserve": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t]),
     "ft_moe_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
@@ -605,12 +613,12 @@ def rope_table(n_pos: int, freqs, scale: float = 1.0, device="cuda", out: torch.
     return out
 
 
-def _rotation(table: torch.Tensor, positions: torch.Tensor, t: int, interleaved: bool, device) -> _Rotation:
+def _rotation(table: torch.Tensor, positions: torch.Tensor, t: int, interleaved: bool, device) -> bytes:
     if table.dim() != 2:
         raise ValueError("table must be (n_pos, rot_dim)")
     n_pos, rot = table.shape
-    return _Rotation(_plain(table, "table", torch.float32, (n_pos, rot), device),
-                     _plain(positions, "positions", torch.int32, (t,), device), n_pos, rot, interleaved)
+    return _pack_rotation(_plain(table, "table", torch.float32, (n_pos, rot), device),
+                          _plain(positions, "positions", torch.int32, (t,), device), n_pos, rot, interleaved)
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
@@ -622,11 +630,13 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interlea
         raise ValueError("x must be a device tensor (t, heads, dim)")
     ty, dev, shape = _float_type(x, "x"), x.device, x.shape
     t, heads, dim = shape
+    xs = _rows(x, "x", shape, x.dtype, dev)
     if out is None:
-        out = x.new_empty(shape)
-    xs, os_ = _rows(x, "x", shape, x.dtype, dev), _rows(out, "out", shape, x.dtype, dev)
-    r = _rotation(table, positions, t, interleaved, dev)
-    _call("ft_rope", dev, stream, ctypes.byref(r), ty, x.data_ptr(), xs[0], xs[1], t, heads, dim,
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        os_ = (heads * dim, dim)
+    else:
+        os_ = _rows(out, "out", shape, x.dtype, dev)
+    _call("ft_rope", dev, stream, _rotation(table, positions, t, interleaved, dev), ty, x.data_ptr(), xs[0], xs[1], t, heads, dim,
           None if weight is None else _plain(weight, "weight", torch.float32, (dim,), dev), eps, out.data_ptr(), os_[0], os_[1])
     return out
 
@@ -639,24 +649,25 @@ def kv_store_rope(cache: KvCache, q: torch.Tensor | None, k: torch.Tensor, v: to
     t, dev, dim = k.shape[0], cache.device, cache.head_dim
     ty, shape = _float_type(k, "k"), (t, cache.n_kv_head, dim)
     ks, vs = _rows(k, "k", shape, k.dtype, dev), _rows(v, "v", shape, k.dtype, dev)
-    r = _rotation(table, positions, t, interleaved, dev)
-    o = _QkvRows(None, 0, 0, 0, None, None, 0, 0, k.data_ptr(), ks[0], ks[1], None, v.data_ptr(), vs[0], vs[1], eps)
-    if k_weight is not None:
-        o.k_weight = _plain(k_weight, "k_weight", torch.float32, (dim,), dev)
+    kw = 0 if k_weight is None else _plain(k_weight, "k_weight", torch.float32, (dim,), dev)
+    qp = qw = op = heads = 0
+    qs = os_ = (0, 0)
     if q is not None:
         heads = q.shape[1]
         qshape = (t, heads, dim)
-        qs = _rows(q, "q", qshape, k.dtype, dev)
+        qs, qp = _rows(q, "q", qshape, k.dtype, dev), q.data_ptr()
         if q_out is None:
-            q_out = q.new_empty(qshape)
-        os_ = _rows(q_out, "q_out", qshape, k.dtype, dev)
-        o.q, o.q_token, o.q_head, o.n_head = q.data_ptr(), qs[0], qs[1], heads
-        o.q_out, o.out_token, o.out_head = q_out.data_ptr(), os_[0], os_[1]
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            os_ = (heads * dim, dim)
+        else:
+            os_ = _rows(q_out, "q_out", qshape, k.dtype, dev)
+        op = q_out.data_ptr()
         if q_weight is not None:
-            o.q_weight = _plain(q_weight, "q_weight", torch.float32, (dim,), dev)
+            qw = _plain(q_weight, "q_weight", torch.float32, (dim,), dev)
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight are q's")
-    _call("ft_kv_store_rope", dev, stream, cache._ref, ctypes.byref(r), ty, ctypes.byref(o),
+    o = _pack_rows(qp, qs[0], qs[1], heads, qw, op, os_[0], os_[1], k.data_ptr(), ks[0], ks[1], kw, v.data_ptr(), vs[0], vs[1], eps)
+    _call("ft_kv_store_rope", dev, stream, cache._ref, _rotation(table, positions, t, interleaved, dev), ty, o,
           _plain(slots, "slots", torch.int64, (t,), dev), t)
     return q_out
 
@@ -689,18 +700,17 @@ def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor
     t, width = shape
     if kind not in ("rms", "layer"):
         raise ValueError(f"kind must be rms or layer, not {kind}")
-    if act not in (None, "Q8_1", "Q8_0", "Q8_K"):
+    if act is not None and act not in ACT_BLOCKS:
         raise ValueError(f"act must be Q8_1, Q8_0 or Q8_K, not {act}")
     if not scale:
         raise ValueError("scale must not be 0")
     if post is None:
         post = post_weight is not None or post_bias is not None
-    o = _NormOpts(None, 0, None, 0, post, None, None, scale, kind == "layer", eps, None, None, None, 0, None, 0, 0, None)
-    for w, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias")):
-        if w is not None:
-            setattr(o, name, _plain(w, name, torch.float32, (width,), dev))
+    w = [0 if a is None else _plain(a, name, torch.float32, (width,), dev)
+         for a, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias"))]
+    rp = rl = gp = gl = sp = sl = np = nl = qp = 0
     if residual is not None:
-        o.residual, o.ld_residual = residual.data_ptr(), _line(residual, "residual", shape, dt, dev)
+        rp, rl = residual.data_ptr(), _line(residual, "residual", shape, dt, dev)
     if gate is not None:
         if gate.dim() == 1:
             gate = gate.unsqueeze(0)
@@ -709,30 +719,32 @@ def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor
             if gate.shape[0] not in (1, t):
                 raise ValueError(f"gate must be (1 or {t}, {width})")
         else:
-            o.ld_gate = _line(gate, "gate", shape, dt, dev)
-        o.gate = gate.data_ptr()
-    if r is None:
-        if post or residual is not None or gate is not None or scale != 1.0:
-            r = torch.empty(shape, dtype=dt, device=dev)
-            o.r, o.ld_r = r.data_ptr(), width
-        else:
-            r = x
+            gl = _line(gate, "gate", shape, dt, dev)
+        gp = gate.data_ptr()
+    if r is not None:
+        sp, sl = r.data_ptr(), _line(r, "r", shape, dt, dev)
+    elif post or rp or gp or scale != 1.0:
+        r = torch.empty_like(x, memory_format=torch.contiguous_format)
+        sp, sl = r.data_ptr(), width
     else:
-        o.r, o.ld_r = r.data_ptr(), _line(r, "r", shape, dt, dev)
-    if out is None:
-        if rows or act is None and rows is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
-            o.out, o.ld_out = out.data_ptr(), width
-    else:
-        o.out, o.ld_out = out.data_ptr(), _line(out, "out", shape, dt, dev)
+        r = x
+    if out is not None:
+        np, nl = out.data_ptr(), _line(out, "out", shape, dt, dev)
+    elif rows or act is None and rows is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        np, nl = out.data_ptr(), width
     if act is not None:
-        size = (t, row_bytes(act, width))
+        elems, size = ACT_BLOCKS[act]
+        size *= width // elems
         if xq is None:
-            xq = torch.empty(size, dtype=torch.uint8, device=dev)
-        o.act, o.xq = TYPES[act], _plain(xq, "xq", torch.uint8, size, dev)
+            xq = x.new_empty((t, size), dtype=torch.uint8)
+            qp = xq.data_ptr()
+        else:
+            qp = _plain(xq, "xq", torch.uint8, (t, size), dev)
     elif xq is not None:
         raise ValueError("xq needs an act")
-    _call("ft_norm", dev, stream, ty, x.data_ptr(), _line(x, "x", shape, dt, dev), t, width, ctypes.byref(o))
+    o = _pack_norm(rp, rl, gp, gl, post, w[2], w[3], scale, kind == "layer", eps, w[0], w[1], sp, sl, np, nl, TYPES[act] if act else 0, qp)
+    _call("ft_norm", dev, stream, ty, x.data_ptr(), _line(x, "x", shape, dt, dev), t, width, o)
     return r, out, xq
 
 
@@ -762,16 +774,19 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, y
     many, rank, _ = a.shape
     n = b.shape[1]
     if out is None:
-        out = torch.empty((t, n), dtype=torch.float32, device=dev)
-    o = _LoraOpts(None if ranks is None else _plain(ranks, "ranks", torch.int32, (many,), dev),
-                  None if scales is None else _plain(scales, "scales", torch.float32, (many,), dev), None, 0)
+        out = x.new_empty((t, n), dtype=torch.float32)
+        ldo = n
+    else:
+        ldo = _line(out, "out", (t, n), torch.float32, dev)
+    wp = wb = 0
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous on {dev}")
-        o.workspace, o.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    o = _pack_lora(0 if ranks is None else _plain(ranks, "ranks", torch.int32, (many,), dev),
+                   0 if scales is None else _plain(scales, "scales", torch.float32, (many,), dev), wp, wb)
     yp, ldy = (None, 0) if y is None else (y.data_ptr(), _line(y, "y", (t, n), torch.float32, dev))
     _call("ft_lora", dev, stream, tx, x.data_ptr(), _line(x, "x", shape, x.dtype, dev), t, k, tw,
           _plain(a, "a", a.dtype, (many, rank, k), dev), _plain(b, "b", a.dtype, (many, n, rank), dev), many, rank, n,
-          _plain(ids, "ids", torch.int32, (t,), dev), yp, ldy, out.data_ptr(), _line(out, "out", (t, n), torch.float32, dev),
-          ctypes.byref(o))
+          _plain(ids, "ids", torch.int32, (t,), dev), yp, ldy, out.data_ptr(), ldo, o)
     return out
