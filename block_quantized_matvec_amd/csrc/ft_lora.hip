@@ -504,10 +504,15 @@ lora_plan_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ ra
   __shared__ int s_wave[2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), many = adapters + 1;
   for (int a = tid; a < many; a += 1024) s_count[a] = 0;
+  int kept[4];   // the first tokens' adapters, for both passes; the rank of this thread's first adapter, for the list
+  lora_ids(ids, t, adapters, tid, kept);
+  const int per = (many + 1023) / 1024, b0 = min(many, tid * per), b1 = min(many, b0 + per);
+  int rank0 = most;
+  if (ranks && b0 < adapters) rank0 = max(0, min(ranks[b0], most));
   __syncthreads();
   for (int i0 = 0; i0 < t; i0 += 4096) {
-    int a[4];
-    lora_ids(ids, t, adapters, i0 + tid, a);
+    int a[4] = {kept[0], kept[1], kept[2], kept[3]};
+    if (i0) lora_ids(ids, t, adapters, i0 + tid, a);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int a0 = __builtin_amdgcn_readfirstlane(a[j]);
@@ -520,7 +525,6 @@ lora_plan_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ ra
   }
   __syncthreads();
   // places and tiles before each adapter's: a run of adapters per thread, then over the threads
-  const int per = (many + 1023) / 1024, b0 = min(many, tid * per), b1 = min(many, b0 + per);
   int n = 0, m = 0;
   for (int a = b0; a < b1; ++a) {
     n += s_count[a];
@@ -541,14 +545,14 @@ lora_plan_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ ra
   for (int a = b0; a < b1; ++a) {
     const int c = s_count[a];
     s_count[a] = before_n;
-    const int rank = a == adapters || c == 0 ? 0 : ranks ? max(0, min(ranks[a], most)) : most;
+    const int rank = a == adapters || c == 0 ? 0 : a == b0 || !ranks ? rank0 : max(0, min(ranks[a], most));
     for (int j = 0; j < c; j += LORA_TILE) tiles[before_m++] = int4{a == adapters ? -1 : a, before_n + j, min(LORA_TILE, c - j), rank};
     before_n += c;
   }
   __syncthreads();
   for (int i0 = 0; i0 < t; i0 += 4096) {
-    int a[4];
-    lora_ids(ids, t, adapters, i0 + tid, a);
+    int a[4] = {kept[0], kept[1], kept[2], kept[3]};
+    if (i0) lora_ids(ids, t, adapters, i0 + tid, a);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int i = i0 + 1024 * j + tid, a0 = __builtin_amdgcn_readfirstlane(a[j]);

@@ -10,9 +10,16 @@
 // a half-integer does not hang on the order of the sum.
 //
 // A row is read once: it stays in the registers of one workgroup, eight consecutive
-// elements a chunk, between its two norms, and every load of a row (x, residual, gate) is
-// issued before the first is used.  The quantizers' blocks lie in neighbouring lanes (four
-// for 32 elements, 32 for 256), so their maxima meet in lane exchanges.
+// elements a thread, between its two norms, and every load of a row (x, residual, gate, the
+// coming norm's weights) is issued before the first is used.  The quantizers' blocks lie in
+// neighbouring lanes (four for 32 elements, 32 for 256), so their maxima meet in lane
+// exchanges.
+//
+// Bound by memory once there are rows for the chip (a 2 GiB copy moves 5.0 TB/s here): 8192 rows of 4096,
+// bf16, both norms and the residual 46-52 us (5.2-5.8 TB/s; 91 with two chunks per thread and loads that
+// waited for each other); fp32 to Q8_K blocks 82 us (5.4); 8192 rows of 2048 fp32 41 us (64 with the registers
+// held to eight waves per SIMD, which spilled); 1500 layer-normed rows of 5002 fp16 with a gate 21 us (two
+// rounds of workgroups, the second half full).  One row of 4096: 3.3 us, the launch and two memory latencies.
 #include "ft_kv.h"
 #include "ft_rowstat.h"
 #include "ft_internal.h"
@@ -162,7 +169,7 @@ __device__ __forceinline__ double norm_sum(double s, double* s_sum) {
 // A workgroup of up to 1024 threads has a row, C chunks of eight elements per thread; with WAVE it
 // has four, one a wave.  TAIL: the width is no multiple of eight.
 template <int TYPE, int C, bool WAVE, bool TAIL>
-__global__ void __launch_bounds__(WAVE ? 256 : 1024, C == 1 ? 8 : 4)
+__global__ void __launch_bounds__(WAVE ? 256 : 1024)
 norm_kernel(NormIo io) {
   constexpr int W = NORM_WORDS<TYPE>;
   __shared__ double s_sum[4][16];

@@ -57,34 +57,8 @@ class _AttnOpts(ctypes.Structure):
                 ("n_shared", ctypes.c_int64), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
-class _Rotation(ctypes.Structure):
-    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int64),
-                ("interleaved", ctypes.c_int)]
-
-
-class _QkvRows(ctypes.Structure):
-    _fields_ = [("q", ctypes.c_void_p), ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64), ("n_head", ctypes.c_int64),
-                ("q_weight", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("out_token", ctypes.c_int64),
-                ("out_head", ctypes.c_int64), ("k", ctypes.c_void_p), ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
-                ("k_weight", ctypes.c_void_p), ("v", ctypes.c_void_p), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
-                ("eps", ctypes.c_double)]
-
-
-class _NormOpts(ctypes.Structure):
-    _fields_ = [("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("gate", ctypes.c_void_p),
-                ("ld_gate", ctypes.c_int64), ("post", ctypes.c_int), ("post_weight", ctypes.c_void_p),
-                ("post_bias", ctypes.c_void_p), ("scale", ctypes.c_float), ("layer", ctypes.c_int), ("eps", ctypes.c_double),
-                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("r", ctypes.c_void_p), ("ld_r", ctypes.c_int64),
-                ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("act", ctypes.c_int), ("xq", ctypes.c_void_p)]
-
-
-class _LoraOpts(ctypes.Structure):
-    _fields_ = [("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
-                ("workspace_bytes", ctypes.c_size_t)]
-
-
-# the same structures packed (a fifth of the time that a Structure takes): ft_rotation, ft_qkv_rows, ft_norm_opts,
-# ft_lora_opts
+# ft_rotation, ft_qkv_rows, ft_norm_opts and ft_lora_opts, packed (a fifth of the time that a ctypes Structure takes);
+# 0 is a NULL pointer
 _pack_rotation = struct.Struct("@PPqqi0P").pack
 _pack_rows = struct.Struct("@PqqqPPqqPqqPPqqd").pack
 _pack_norm = struct.Struct("@PqPqiPPfidPPPqPqiP").pack

@@ -47,7 +47,7 @@ def test_types_and_sizes(k, n, rank, tx, tw):
 
 
 @pytest.mark.parametrize("t,many", [(1, 1), (2, 2), (16, 1), (17, 1), (31, 2), (33, 1), (48, 1), (49, 1), (63, 1), (64, 1), (64, 64), (65, 1), (65, 64), (127, 1),
-                                    (128, 3), (129, 1), (300, 40), (1000, 7), (1100, 1), (2500, 300), (130, 8192)])
+                                    (128, 3), (129, 1), (300, 40), (1000, 7), (1100, 1), (2500, 300), (130, 8192), (40, 2000), (64, 1023), (64, 1024), (64, 1025), (200, 200)])
 def test_tiles(t, many):
     """Every number of groups of tokens, and of adapters beside them."""
     need_gpu()
@@ -126,6 +126,17 @@ def test_rows_keep_to_themselves(t):
     assert torch.isnan(out[2:4]).all()
     x[2:4] = 1e38   # large, and finite in pieces
     check(ft.lora(x, a * 1e-3, b * 1e-3, ids, y=y), x, a * 1e-3, b * 1e-3, ids, y, rows=keep.cpu().numpy())
+
+
+@pytest.mark.parametrize("tx,tw", [("f16", "f16"), ("f16", "bf16"), ("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")])
+def test_small_and_large_values(tx, tw):
+    """Values down to a type's least, and up to where only the product is finite."""
+    need_gpu()
+    for t in (3, 70):
+        for sx, sw in ((2.0 ** -24, 1.0), (2.0 ** -20, 2.0 ** -20), (2.0 ** 14, 2.0 ** -14), (2.0 ** -14, 2.0 ** 10)):
+            x, a, b, y, ids, sc = case(t, 48, 50, 2, 8)
+            x, a, b = ((v * s).to(ref.DT[d]) for v, s, d in ((x, sx, tx), (a, sw, tw), (b, 1.0, tw)))
+            check(ft.lora(x, a, b, ids), x, a, b, ids)
 
 
 def test_nothing_to_do():

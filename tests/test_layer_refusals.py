@@ -12,21 +12,25 @@ from tests.test_kv_refusals import FAKE, ODD, cache, status
 BIG = 1 << 41
 
 
+def packed(pack, fields):
+    return pack(*(0 if v is None else v for v in fields.values()))
+
+
 def rotation(**kw):
     f = dict(table=FAKE, positions=FAKE, n_pos=100, rot_dim=64, interleaved=0)
     f.update(kw)
-    return ft._Rotation(*f.values())
+    return packed(ft._pack_rotation, f)
 
 
 def rope(rot=None, ty=0, x=FAKE, xt=256, xh=64, t=2, heads=4, dim=64, weight=None, eps=0.0, out=FAKE + 4096, ot=256, oh=64):
-    return status("ft_rope", ctypes.byref(rot or rotation()), ty, x, xt, xh, t, heads, dim, weight, eps, out, ot, oh, None)
+    return status("ft_rope", rot or rotation(), ty, x, xt, xh, t, heads, dim, weight, eps, out, ot, oh, None)
 
 
 def store(c=None, rot=None, ty=0, slots=FAKE, t=2, **o):
     f = dict(q=FAKE, q_token=256, q_head=64, n_head=4, q_weight=None, q_out=FAKE + 4096, out_token=256, out_head=64, k=FAKE, k_token=128,
              k_head=64, k_weight=None, v=FAKE, v_token=128, v_head=64, eps=0.0)
     f.update(o)
-    return status("ft_kv_store_rope", ctypes.byref(c or cache()), ctypes.byref(rot or rotation()), ty, ctypes.byref(ft._QkvRows(*f.values())), slots, t,
+    return status("ft_kv_store_rope", ctypes.byref(c or cache()), rot or rotation(), ty, packed(ft._pack_rows, f), slots, t,
                   None)
 
 
@@ -34,13 +38,13 @@ def norm(ty=0, x=FAKE, ldx=64, rows=2, width=64, **o):
     f = dict(residual=None, ld_residual=0, gate=None, ld_gate=0, post=0, post_weight=None, post_bias=None, scale=0.0, layer=0, eps=0.0,
              weight=None, bias=None, r=None, ld_r=0, out=FAKE, ld_out=64, act=0, xq=None)
     f.update(o)
-    return status("ft_norm", ty, x, ldx, rows, width, ctypes.byref(ft._NormOpts(*f.values())), None)
+    return status("ft_norm", ty, x, ldx, rows, width, packed(ft._pack_norm, f), None)
 
 
 def lora(tx=0, x=FAKE, ldx=64, t=2, k=64, tw=2, a=FAKE, b=FAKE, many=3, rank=16, n=32, ids=FAKE, y=FAKE, ldy=32, out=FAKE, ldo=32, **o):
     f = dict(ranks=None, scales=None, workspace=None, workspace_bytes=0)
     f.update(o)
-    return status("ft_lora", tx, x, ldx, t, k, tw, a, b, many, rank, n, ids, y, ldy, out, ldo, ctypes.byref(ft._LoraOpts(*f.values())), None)
+    return status("ft_lora", tx, x, ldx, t, k, tw, a, b, many, rank, n, ids, y, ldy, out, ldo, packed(ft._pack_lora, f), None)
 
 
 def test_rope_refused():
@@ -74,7 +78,7 @@ def test_store_refused():
                      (dict(v_head=BIG), "FT_ERR_INVALID_ARG"), (dict(q_head=1), "FT_ERR_INVALID_ARG"), (dict(out_token=63), "FT_ERR_INVALID_ARG"),
                      (dict(q_out=FAKE, out_token=512), "FT_ERR_INVALID_ARG"), (dict(t=(1 << 24) + 1), "FT_ERR_SHAPE")):
         assert store(**kw) == want, kw
-    assert status("ft_kv_store_rope", ctypes.byref(cache()), ctypes.byref(rotation()), 0, None, FAKE, 2, None) == "FT_ERR_INVALID_ARG"
+    assert status("ft_kv_store_rope", ctypes.byref(cache()), rotation(), 0, None, FAKE, 2, None) == "FT_ERR_INVALID_ARG"
 
 
 def test_table_refused():
