@@ -53,28 +53,46 @@ __device__ __forceinline__ void kv_load_side(const KvIo& io, int ftype, const in
   __syncthreads();
   const int nt = (int)min((int64_t)KV_TILE, t - t0);
   if constexpr (V) {   // the codes into the transposed tile first
-    const int n_run = __popcll(runs);
-    for (int i = tid; i < n_run * ROWS; i += 256) {   // a row's runs side by side: often one piece of a page
-      const int r = i / n_run, c = i - r * n_run;
-      const int tok = nth_bit(runs, c);
-      const uint8_t* ph = io.pages + tk.at[tok];
-      const u32x4 w = *(const u32x4*)(ph + r * io.page + tk.key[tok]);
-      uint8_t* dst = s_tile + r * KV_PITCH + tok;
-      if ((tok & 3) == 0) {
+    // (both loops: four loads per thread in flight before the first is put down)
+    const int n_run = __popcll(runs), n_rest = __popcll(valid & ~cover16(runs));
+    for (int i0 = tid; i0 < n_run * ROWS; i0 += 1024) {   // a row's runs side by side: often one piece of a page
+      u32x4 w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ((uint32_t*)dst)[k] = w[k];
-      } else {
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + 256 * q, r = i / n_run;
+        if (i >= n_run * ROWS) continue;
+        const int tok = nth_bit(runs, i - r * n_run);
+        w[q] = *(const u32x4*)(io.pages + tk.at[tok] + r * io.page + tk.key[tok]);
+      }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) dst[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + 256 * q, r = i / n_run;
+        if (i >= n_run * ROWS) continue;
+        const int tok = nth_bit(runs, i - r * n_run);
+        uint8_t* dst = s_tile + r * KV_PITCH + tok;
+        if ((tok & 3) == 0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ((uint32_t*)dst)[k] = w[q][k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) dst[k] = (uint8_t)(w[q][k >> 2] >> (8 * (k & 3)));
+        }
       }
     }
-    const uint64_t rest = valid & ~cover16(runs);
-    const int n_rest = __popcll(rest);
-    for (int i = tid; i < n_rest * ROWS; i += 256) {
-      const int c = i / ROWS, r = i - c * ROWS;
-      const int tok = nth_bit(rest, c);
-      const uint8_t* ph = io.pages + tk.at[tok];
-      s_tile[r * KV_PITCH + tok] = ph[r * io.page + tk.key[tok]];
+    for (int i0 = tid; i0 < n_rest * ROWS; i0 += 1024) {
+      uint8_t b[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + 256 * q, c = i / ROWS;
+        if (i >= n_rest * ROWS) continue;
+        const int tok = tk.rest[c];
+        b[q] = (io.pages + tk.at[tok])[(i - c * ROWS) * io.page + tk.key[tok]];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + 256 * q, c = i / ROWS;
+        if (i < n_rest * ROWS) s_tile[(i - c * ROWS) * KV_PITCH + tk.rest[c]] = b[q];
+      }
     }
     __syncthreads();
   }
@@ -138,7 +156,7 @@ kv_load_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int
 template <int TK, int TV, int NB>
 static hipError_t kv_launch(const KvArgs& a, bool load, hipStream_t st) {
   const KvIo k = kv_io(a, false), v = kv_io(a, true);
-  const int span = kv_span(a.t);
+  const int span = kv_span(a.t, a.heads);
   const unsigned tiles = (unsigned)((a.t + span - 1) / span);
   if (!load) {
     kv_store_kernel<TK, TV, NB><<<dim3(tiles, a.heads, 2), 256, 0, st>>>(k, v, a.ftype, a.slots, a.t, span);

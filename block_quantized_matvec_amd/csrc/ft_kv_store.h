@@ -92,7 +92,14 @@ __device__ __forceinline__ int64_t kv_slot(const int64_t* slots, int64_t t0, int
 struct KvTokens {
   int64_t at[KV_TILE];   // byte of the page head in the pool
   int key[KV_TILE];      // the key in its page; -1: not in the cache (padding, or out of range)
+  uint8_t rest[KV_TILE]; // the tokens of the cache that no run covers, in order
 };
+__device__ __forceinline__ uint64_t cover16(uint64_t m) {   // bits j .. j+15 of every bit j
+  m |= m << 1;
+  m |= m << 2;
+  m |= m << 4;
+  return m | (m << 8);
+}
 // The tile's slots, and which of its tokens start a run that fills 16 slots from a
 // multiple of 16 on.  Every wave computes the same masks.
 template <class IO>
@@ -112,7 +119,10 @@ __device__ __forceinline__ uint64_t kv_runs(const IO& io, int64_t s, int head_by
   run &= run >> 4;            // eight
   run &= (next >> 9) & (next >> 10) & (next >> 11) & (next >> 12);   // ... fifteen
   run &= (next >> 13) & (next >> 14) & (next >> 15);
-  return run & __ballot(s >= 0 && (s & 15) == 0 && lane <= 48);
+  run &= __ballot(s >= 0 && (s & 15) == 0 && lane <= 48);
+  const uint64_t rest = valid & ~cover16(run);
+  if (threadIdx.x < 64 && ((rest >> lane) & 1)) tk.rest[__popcll(rest & ((1ull << lane) - 1))] = (uint8_t)lane;
+  return run;
 }
 
 // n-th set bit of m (m has more than n)
@@ -120,13 +130,6 @@ __device__ __forceinline__ int nth_bit(uint64_t m, int n) {
   for (int i = 0; i < n; ++i) m &= m - 1;
   return __builtin_ctzll(m);
 }
-__device__ __forceinline__ uint64_t cover16(uint64_t m) {   // bits j .. j+15 of every bit j
-  m |= m << 1;
-  m |= m << 2;
-  m |= m << 4;
-  return m | (m << 8);
-}
-
 // A unit is one block of four tokens, in 16 lanes: lane 16r + 4u + l4 of a wave holds
 // elements 8 l4 .. 8 l4 + 7 of its token r, u one of the wave's four units.  A workgroup
 // takes 16 units at a time, NB times; unit n is block n % NB of tokens 4 (n / NB) ..
@@ -251,20 +254,23 @@ __device__ __forceinline__ void kv_store_side(const KvIo& io, int ftype, const i
       }
       *(u32x4*)(ph + r * io.page + tk.key[tok]) = w;
     }
-    const uint64_t rest = valid & ~cover16(runs);
-    const int n_rest = __popcll(rest);
+    const int n_rest = __popcll(valid & ~cover16(runs));
     for (int i = tid; i < n_rest * ROWS; i += 256) {
       const int c = i / ROWS, r = i - c * ROWS;
-      const int tok = nth_bit(rest, c);
+      const int tok = tk.rest[c];
       uint8_t* ph = io.pages + tk.at[tok];
       ph[r * io.page + tk.key[tok]] = s_tile[r * KV_PITCH + tok];
     }
   }
 }
 
-// Tokens that a workgroup takes: a step's few tokens, whose values are single bytes far apart, spread over more
-// workgroups (24 tokens of 4 heads of 128, queries and keys turned beside them: 8.8 -> 3.8 us, reading back 11.1 -> 3.6)
-inline int kv_span(int64_t t) { return t <= 32 ? 4 : KV_TILE; }
+// Tokens that a workgroup takes.  Values of tokens that lie far apart are single bytes, and what a workgroup of 64 does
+// with them one after the other takes longer than all else: while there are CUs to spare it takes 16 or 4, at the
+// price of runs of 16 that two workgroups share (SPANFIG)
+inline int kv_span(int64_t t, int heads) {
+  if ((t + 3) / 4 * heads <= ftk_num_cus()) return 4;
+  return (t + 15) / 16 * heads <= 2 * ftk_num_cus() ? 16 : KV_TILE;
+}
 
 inline KvIo kv_io(const KvArgs& a, bool v) {
   KvIo io;

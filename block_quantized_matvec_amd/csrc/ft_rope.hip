@@ -333,7 +333,7 @@ static hipError_t store_launch(const RopeArgs& a, hipStream_t st) {
   const RopeRows k = rope_rows_of(a.kv.k, a.kv.k_token, a.kv.k_head, a.kv.heads, a.k_weight, a, HC);
   const RopeOut out = {a.out, a.out_token, a.out_head, rope_vec(a.out, a.out_token, a.out_head, a.dim, a.ftype)};
   const int64_t per = 64 >> c.log_lanes, groups = (a.t + per - 1) / per;
-  const int span = kv_span(a.t);
+  const int span = kv_span(a.t, a.kv.heads);
   const int64_t v_groups = (a.t + span - 1) / span * a.kv.heads, k_tasks = groups * k.chunks, tasks = k_tasks + groups * q.chunks;
   kv_store_rope_kernel<TK, TV, NB, HC><<<rope_grid(v_groups + (tasks + 3) / 4), 256, 0, st>>>(
       c, k, q, out, kv_io(a.kv, false), kv_io(a.kv, true), a.kv.slots, span, (uint32_t)v_groups, (uint32_t)k_tasks, (uint32_t)tasks);
