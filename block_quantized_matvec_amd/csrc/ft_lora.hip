@@ -2,17 +2,25 @@
 //   out_i = y_i + s_a B_a (A_a x_i),  a the adapter of token i.
 //
 // Tokens of one adapter are taken together, up to 64 a tile: up to 64 tokens in all, every
-// workgroup of the first product finds its tile from the ids by itself and leaves it for the second;
-// beyond, one workgroup sorts the tokens first (lora_plan_kernel).  Two launches: h = A x (lora_shrink_kernel), the long axis split
-// over waves and over workgroups whose partial sums the second adds up, and out = y + B h
-// (lora_expand_kernel).  A tile of 16 or fewer tokens gives its workgroup's four waves four
-// shares of the axis (or of the columns), one of 64 gives each 16 tokens.
+// workgroup of the first product finds its tile from the ids by itself and leaves it for the
+// second; beyond, one workgroup sorts the tokens first (lora_plan_kernel, 5 us).  Two launches:
+// h = A x (lora_shrink_kernel), the long axis split over a workgroup's waves and over workgroups,
+// and out = y + B h (lora_expand_kernel), whose workgroups first add up the shares of h.
 //
 // Both products run on v_mfma_f32_16x16x32 with the weights' rows as rows of the result and
-// the tokens as columns.  Accuracy is fp32's: an fp32 operand is taken as three bf16 pieces
-// (8 bits each, cut off, so their sum is exact), an fp16 one as two, and the products of pieces
-// down to 2^-16 of the first are summed (those left out are below 2^-24 of it).  fp16 rows with
-// fp16 weights, and bf16 with bf16, are one product.  h stays in fp32 between the launches.
+// the tokens as columns, so that a token's values come from its own row alone.  Accuracy is fp32's:
+// an fp32 operand is taken as three bf16 pieces (8 bits each, cut off, so their sum is exact), an
+// fp16 one as two, and the products of pieces down to 2^-16 of the first are summed (those left out
+// are below 2^-24 of it).  fp16 rows with fp16 weights, and bf16 with bf16, are one product.  h
+// stays in fp32 between the launches.
+//
+// Bound by memory: x, y, out and the rows of A and B that the tokens name.  4096 fp32 tokens,
+// 4096 -> 14336, rank 64, bf16 weights (540 MB): 120 us (4.5 TB/s; a 2 GiB copy 5.0), of which 100 the
+// second product, 21 the first.  1500 bf16 tokens of 16 adapters in any order, 14336 -> 4096, ranks
+// 8 to 64 (110 MB): 42 us, a third of it two chains of dependent loads (tile, tokens, rows) and the sort.
+// 48 tokens of 32 adapters, ranks 8 to 64, fp16 weights, 4096 -> 14336: 25 us; B's rows of 8 to 32 ranks lie
+// 128 bytes apart, and whole lines come (59 MB for 27).  One token, 4096 -> 6144, rank 16: 7.2 us, two launches; in
+// one launch, every workgroup reading all of A again, 9.5 to 11.
 #include <algorithm>
 
 #include "ft_internal.h"

@@ -472,12 +472,14 @@ def kv_load(cache: KvCache, slots: torch.Tensor, dtype=torch.float32, k: torch.T
     if dtype not in FLOATS:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
     if k is None and v is None:
-        k, v = torch.empty((2, *shape), dtype=dtype, device=dev)
-    elif k is None:
-        k = torch.empty(shape, dtype=dtype, device=dev)
-    elif v is None:
-        v = torch.empty(shape, dtype=dtype, device=dev)
-    ks, vs = _rows(k, "k", shape, dtype, dev), _rows(v, "v", shape, dtype, dev)
+        k, v = torch.empty((2, *shape), dtype=dtype, device=dev).unbind()
+        ks = vs = (cache.n_kv_head * cache.head_dim, cache.head_dim)
+    else:
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=dev)
+        elif v is None:
+            v = torch.empty(shape, dtype=dtype, device=dev)
+        ks, vs = _rows(k, "k", shape, dtype, dev), _rows(v, "v", shape, dtype, dev)
     _call("ft_kv_load", dev, stream, cache._ref, _plain(slots, "slots", torch.int64, (t,), dev), t, FLOATS[dtype],
           k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
     return k, v
@@ -680,8 +682,11 @@ def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor
         raise ValueError("scale must not be 0")
     if post is None:
         post = post_weight is not None or post_bias is not None
-    w = [0 if a is None else _plain(a, name, torch.float32, (width,), dev)
-         for a, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias"))]
+    one = (width,)
+    wp = 0 if weight is None else _plain(weight, "weight", torch.float32, one, dev)
+    bp = 0 if bias is None else _plain(bias, "bias", torch.float32, one, dev)
+    pwp = 0 if post_weight is None else _plain(post_weight, "post_weight", torch.float32, one, dev)
+    pbp = 0 if post_bias is None else _plain(post_bias, "post_bias", torch.float32, one, dev)
     rp = rl = gp = gl = sp = sl = np = nl = qp = 0
     if residual is not None:
         rp, rl = residual.data_ptr(), _line(residual, "residual", shape, dt, dev)
@@ -717,7 +722,7 @@ def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor
             qp = _plain(xq, "xq", torch.uint8, (t, size), dev)
     elif xq is not None:
         raise ValueError("xq needs an act")
-    o = _pack_norm(rp, rl, gp, gl, post, w[2], w[3], scale, kind == "layer", eps, w[0], w[1], sp, sl, np, nl, TYPES[act] if act else 0, qp)
+    o = _pack_norm(rp, rl, gp, gl, post, pwp, pbp, scale, kind == "layer", eps, wp, bp, sp, sl, np, nl, TYPES[act] if act else 0, qp)
     _call("ft_norm", dev, stream, ty, x.data_ptr(), _line(x, "x", shape, dt, dev), t, width, o)
     return r, out, xq
 

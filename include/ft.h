@@ -39,7 +39,7 @@
  *  - Calls on different streams may run concurrently; calls that share a
  *    stream's scratch pool are ordered by that stream, from however many host
  *    threads they come (a call holds the pool until it has enqueued its work).
- *    Scratch that a caller gives (ft_attn_opts.workspace) is the caller's to order.
+ *    Scratch that a caller gives (ft_attn_opts, ft_lora_opts) is the caller's to order.
  */
 #ifndef FT_H
 #define FT_H
@@ -92,8 +92,8 @@ typedef enum {
   FT_OP_KV_CACHE = 6 /* w: the keys' block type, act: the values' */
 } ft_op;
 
-/* element types of the plain tensors around the key/value cache and the scored
-   router (every other call's plain tensors are fp32) */
+/* element types of the plain tensors around the key/value cache, the scored router, the
+   rotation, the norm and the adapters (every other call's plain tensors are fp32) */
 typedef enum { FT_F32 = 0, FT_F16 = 1, FT_BF16 = 2 } ft_float;
 
 /* Elements per block (32 or 256) and bytes per block; 0 for an unknown type. */
@@ -412,7 +412,7 @@ typedef struct {
 ft_status ft_rope_table(const double* freqs, int64_t half, int64_t n_pos, double scale, float* table, ft_stream_t stream);
 /* Turn the rows of x, [t][n_head][dim] of `type`, into out (which may be x itself, with its
    strides; otherwise they must not overlap).  Element stride 1, token and head strides in
-   elements.  With weight ([dim] fp32) each row is first x * rstd * weight, rstd = 1 / sqrt(mean x^2 + eps)
+   elements; no two rows of out overlap.  With weight ([dim] fp32) each row is first x * rstd * weight, rstd = 1 / sqrt(mean x^2 + eps)
    (mean in 64 bits, rstd rounded to fp32).  dim 2 .. 512, t <= 2^24, n_head <= 1024, t * n_head <= 2^30. */
 ft_status ft_rope(const ft_rotation* rot, ft_float type, const void* x, int64_t x_token, int64_t x_head, int64_t t,
                   int64_t n_head, int64_t dim, const float* weight, double eps, void* out, int64_t out_token,
