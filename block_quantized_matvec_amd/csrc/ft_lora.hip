@@ -52,8 +52,8 @@ struct LoraIo {
   int parts, part_k;                 // shares of the long axis
   int blocks;                        // blocks of columns per workgroup of the second product
   float* h;            // [parts][t][rank_pad]
-  int32_t* order;      // tokens by tile
-  int4* tiles;         // adapter, first place in order, tokens, rank
+  int32_t* order;      // [tiles][64] tokens
+  int4* tiles;         // adapter, rank, tokens
   int32_t* n_tiles;
   int sorted;          // the plan has run: they are there for the first product too
 };
@@ -151,12 +151,13 @@ struct LoraTile {
 __device__ __forceinline__ bool lora_tile(const LoraIo& io, int index, LoraTile& t) {
   const int lane = threadIdx.x & 63;
   const int n = *io.n_tiles;
-  const int4 e = io.tiles[index];   // one beyond the last: whatever is there
+  const int4 e = io.tiles[index];   // one beyond the last: whatever is there, as behind a tile's last token
+  const int token = io.order[64 * index + lane];
   if (index >= n || t.first >= e.z) return false;
   t.adapter = __builtin_amdgcn_readfirstlane(e.x);
+  t.rank = __builtin_amdgcn_readfirstlane(e.y);
   t.count = __builtin_amdgcn_readfirstlane(e.z);
-  t.rank = __builtin_amdgcn_readfirstlane(e.w);
-  t.token = io.order[e.y + min(lane, e.z - 1)];
+  t.token = lane < t.count ? token : __builtin_amdgcn_readfirstlane(token);
   return true;
 }
 // The same from up to 64 ids, the index counting groups of 16 tokens, tile by tile; `leave`: the workgroup
@@ -199,7 +200,7 @@ __device__ __forceinline__ bool lora_find(const LoraIo& io, int index, int* s_wo
     const int tile = __builtin_popcountll(leaders & ((1ull << leader) - 1));
     io.order[64 * tile + lane] = t.token;
     if (lane == 0) {
-      io.tiles[tile] = int4{t.adapter, 64 * tile, t.count, t.rank};
+      io.tiles[tile] = int4{t.adapter, t.rank, t.count, 0};
       if (tile == 0) *io.n_tiles = __builtin_popcountll(leaders);
     }
   }
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(1024)
 lora_plan_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ ranks, int most, int t, int adapters, int32_t* __restrict__ order,
                  int4* __restrict__ tiles, int32_t* __restrict__ n_tiles) {
   extern __shared__ int s_count[];   // [adapters + 1], then places
-  __shared__ int s_wave[2][16];
+  __shared__ int s_wave[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), many = adapters + 1;
   for (int a = tid; a < many; a += 1024) s_count[a] = 0;
   int kept[4];   // the first tokens' adapters, for both passes; the rank of this thread's first adapter, for the list
@@ -532,30 +533,25 @@ lora_plan_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ ra
     }
   }
   __syncthreads();
-  // places and tiles before each adapter's: a run of adapters per thread, then over the threads
-  int n = 0, m = 0;
-  for (int a = b0; a < b1; ++a) {
-    n += s_count[a];
-    m += (s_count[a] + LORA_TILE - 1) / LORA_TILE;
-  }
-  int before_n = n, before_m = m;
+  // the tiles before each adapter's: a run of adapters per thread, then over the threads
+  int m = 0;
+  for (int a = b0; a < b1; ++a) m += (s_count[a] + LORA_TILE - 1) / LORA_TILE;
+  int before_m = m;
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) {
-    const int un = __shfl_up(before_n, s, 64), um = __shfl_up(before_m, s, 64);
-    if (lane >= s) before_n += un, before_m += um;
+    const int um = __shfl_up(before_m, s, 64);
+    if (lane >= s) before_m += um;
   }
-  if (lane == 63) s_wave[0][wave] = before_n, s_wave[1][wave] = before_m;
+  if (lane == 63) s_wave[wave] = before_m;
   __syncthreads();
-  before_n -= n;
   before_m -= m;
-  for (int w = 0; w < wave; ++w) before_n += s_wave[0][w], before_m += s_wave[1][w];
+  for (int w = 0; w < wave; ++w) before_m += s_wave[w];
   if (tid == 1023) *n_tiles = before_m + m;
   for (int a = b0; a < b1; ++a) {
     const int c = s_count[a];
-    s_count[a] = before_n;
+    s_count[a] = LORA_TILE * before_m;
     const int rank = a == adapters || c == 0 ? 0 : a == b0 || !ranks ? rank0 : max(0, min(ranks[a], most));
-    for (int j = 0; j < c; j += LORA_TILE) tiles[before_m++] = int4{a == adapters ? -1 : a, before_n + j, min(LORA_TILE, c - j), rank};
-    before_n += c;
+    for (int j = 0; j < c; j += LORA_TILE) tiles[before_m++] = int4{a == adapters ? -1 : a, rank, min(LORA_TILE, c - j), 0};
   }
   __syncthreads();
   for (int i0 = 0; i0 < t; i0 += 4096) {
@@ -605,8 +601,9 @@ static LoraPlan lora_plan(int64_t t, int64_t k, int rank, int64_t adapters) {
   const int64_t most = std::max(16 * LORA_WGS, 64);
   p.h = (size_t)std::min<int64_t>(16 * t, most * cus + t) * rank_pad * 4;
   p.order = (p.h + 255) & ~(size_t)255;
-  p.list = (p.order + (size_t)std::max<int64_t>(t, 64 * std::min<int64_t>(t, 64)) * 4 + 255) & ~(size_t)255;
-  p.total = p.list + 16 + (size_t)(t / LORA_TILE + some) * 16;
+  const size_t most_tiles = (size_t)(t / LORA_TILE + some);
+  p.list = p.order + most_tiles * LORA_TILE * 4;
+  p.total = p.list + 16 + most_tiles * 16;
   return p;
 }
 

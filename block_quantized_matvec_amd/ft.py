@@ -753,7 +753,7 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, y
     many, rank, _ = a.shape
     n = b.shape[1]
     if out is None:
-        out = x.new_empty((t, n), dtype=torch.float32)
+        out = x.new_empty((t, n), dtype=torch.float32) if y is None else torch.empty_like(y, memory_format=torch.contiguous_format)
         ldo = n
     else:
         ldo = _line(out, "out", (t, n), torch.float32, dev)
