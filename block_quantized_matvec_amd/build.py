@@ -1,22 +1,26 @@
-"""Build libft.so (the gfx950 HIP kernels + C ABI) in-tree with hipcc.
+"""Build libft.so (the gfx950 HIP kernels + C ABI) in-tree with hipcc, and _ft_bind.so (marshalling of the smallest
+calls, against torch's headers) with g++.
 
     python -m block_quantized_matvec_amd.build
 
-Always recompiles.  Translation units compile in parallel; the shared object is
-written next to this file so that it travels with the source tree.
+Always recompiles.  Translation units compile in parallel; the shared objects are
+written next to this file so that they travel with the source tree.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libft.so")
+BIND = os.path.join(PKG, "_ft_bind.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -54,6 +58,22 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _bind() -> None:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-I" + os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", "/opt/rocm/include",
+           os.path.join(CSRC, "ft_bind.cpp"), "-o", tmp, "-L" + PKG, "-l:libft.so", "-L" + os.path.join(torch, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for ft_bind.cpp:\n{r.stdout}\n{r.stderr}")
+    if "warning" in r.stderr:
+        sys.stderr.write(r.stderr + "\n")
+    os.replace(tmp, BIND)
+
+
 def build(jobs: int | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(len(SOURCES), max(1, min(os.cpu_count() or 2, 16)))
@@ -65,6 +85,7 @@ def build(jobs: int | None = None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _bind()
     return LIB
 
 

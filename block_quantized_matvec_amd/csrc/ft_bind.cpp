@@ -1,0 +1,337 @@
+// ft_bind.cpp -- argument marshalling of the operators of a decoder layer's step (ft.rope, ft.kv_store_rope, ft.norm,
+// ft.lora): torch tensors into pointers, sizes and strides, outputs allocated, a status raised.  Checks and calls
+// only, no arithmetic.  In Python the same took 4 to 6 us a call, longer than most of these kernels run at a
+// decode step; here it takes about one.
+#include <torch/csrc/python_headers.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "ft.h"
+
+namespace {
+
+using at::Tensor;
+PyObject* g_error = nullptr;   // ft.FtError
+
+const Tensor& tensor(PyObject* o, const char* name) {
+  TORCH_CHECK_TYPE(THPVariable_Check(o), name, " must be a tensor, not ", Py_TYPE(o)->tp_name);
+  return THPVariable_Unpack(o);
+}
+const Tensor* maybe(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
+bool truth(PyObject* o) {
+  const int r = PyObject_IsTrue(o);
+  if (r < 0) throw python_error();
+  return r != 0;
+}
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+int64_t whole(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+ft_float float_type(const Tensor& t, const char* name) {
+  switch (t.scalar_type()) {
+    case at::kFloat: return FT_F32;
+    case at::kHalf: return FT_F16;
+    case at::kBFloat16: return FT_BF16;
+    default: TORCH_CHECK_VALUE(false, name, " must be float32, float16 or bfloat16, not ", t.dtype());
+  }
+}
+// pointer of a contiguous tensor of this type, shape and device (null: not given)
+void* plain(const Tensor* t, const char* name, at::ScalarType type, at::IntArrayRef shape, at::Device dev) {
+  if (!t) return nullptr;
+  TORCH_CHECK_VALUE(t->scalar_type() == type && t->sizes() == shape && t->device() == dev && t->is_contiguous(), name,
+                    " must be a contiguous ", type, " tensor of shape ", shape, " on ", dev, ", not ", t->dtype(), " ", t->sizes(), " on ",
+                    t->device());
+  return t->data_ptr();
+}
+// strides of a (tokens, heads, dim) tensor, and of a (rows, width) one
+struct Rows {
+  int64_t token, head;
+};
+Rows rows(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
+  TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == type && t.device() == dev && t.stride(2) == 1, name, " must be ", shape, " ", type,
+                    " on ", dev, " with unit element stride, not ", t.sizes(), " ", t.dtype(), " on ", t.device());
+  return {t.stride(0), t.stride(1)};
+}
+int64_t line(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
+  TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == type && t.device() == dev && (t.stride(1) == 1 || shape[1] <= 1), name, " must be ",
+                    shape, " ", type, " on ", dev, " with unit element stride, not ", t.sizes(), " ", t.dtype(), " on ", t.device());
+  return shape[0] > 1 ? t.stride(0) : shape[1];
+}
+Tensor empty(at::IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options().requires_grad(false)); }
+
+// The caller's stream (None: the current one of the device), with the device as the library's current one.
+struct On {
+  c10::OptionalDeviceGuard guard;
+  ft_stream_t stream;
+  On(at::Device dev, PyObject* o) : guard(dev) {
+    if (o == Py_None) {
+      stream = c10::hip::getCurrentHIPStream(dev.index()).stream();
+      return;
+    }
+    const auto get = [&](const char* name) {
+      PyObject* a = PyObject_GetAttrString(o, name);
+      if (!a) throw python_error();
+      const unsigned long long v = PyLong_AsUnsignedLongLongMask(a);
+      Py_DECREF(a);
+      if (PyErr_Occurred()) throw python_error();
+      return v;
+    };
+    TORCH_CHECK_VALUE((int64_t)get("device_index") == dev.index(), "the stream is on another device than the tensors, which are on ", dev);
+    stream = (ft_stream_t)(uintptr_t)get("cuda_stream");
+  }
+};
+template <class Call>
+void run(const char* name, Call&& call) {
+  ft_status s;
+  Py_BEGIN_ALLOW_THREADS
+  s = call();
+  Py_END_ALLOW_THREADS
+  if (s == FT_OK) return;
+  PyObject* e = PyObject_CallFunction(g_error, "is", (int)s, name);
+  if (e) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  throw python_error();
+}
+PyObject* given(PyObject* o, const Tensor& t) {   // the caller's object, or the new tensor
+  if (o == Py_None) return THPVariable_Wrap(t);
+  Py_INCREF(o);
+  return o;
+}
+
+ft_rotation rotation(PyObject* table, PyObject* positions, PyObject* interleaved, int64_t t, at::Device dev) {
+  const Tensor& tab = tensor(table, "table");
+  const Tensor& pos = tensor(positions, "positions");
+  TORCH_CHECK_VALUE(tab.dim() == 2, "table must be (n_pos, rot_dim)");
+  ft_rotation r = {};
+  r.table = (const float*)plain(&tab, "table", at::kFloat, tab.sizes(), dev);
+  r.positions = (const int32_t*)plain(&pos, "positions", at::kInt, {t}, dev);
+  r.n_pos = tab.size(0);
+  r.rot_dim = tab.size(1);
+  r.interleaved = truth(interleaved);
+  return r;
+}
+
+// x, positions, table, interleaved, weight, eps, out, stream
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const Tensor& x = tensor(a[0], "x");
+  TORCH_CHECK_VALUE(x.is_cuda() && x.dim() == 3, "x must be a device tensor (t, heads, dim)");
+  const ft_float ty = float_type(x, "x");
+  const at::Device dev = x.device();
+  const auto type = x.scalar_type();
+  const int64_t t = x.size(0), heads = x.size(1), dim = x.size(2);
+  const Rows xs = rows(x, "x", x.sizes(), type, dev);
+  const ft_rotation r = rotation(a[2], a[1], a[3], t, dev);
+  const float* w = (const float*)plain(maybe(a[4], "weight"), "weight", at::kFloat, {dim}, dev);
+  const double eps = number(a[5]);
+  const Tensor out = a[6] == Py_None ? empty(x.sizes(), x) : tensor(a[6], "out");
+  const Rows os = rows(out, "out", x.sizes(), type, dev);
+  const On on(dev, a[7]);
+  run("ft_rope", [&] {
+    return ft_rope(&r, ty, x.data_ptr(), xs.token, xs.head, t, heads, dim, w, eps, out.data_ptr(), os.token, os.head, on.stream);
+  });
+  return given(a[6], out);
+  END_HANDLE_TH_ERRORS
+}
+
+// address of the cache's structure, its k_pages, q, k, v, slots, positions, table, interleaved, q_weight, k_weight, eps, q_out, stream
+PyObject* kv_store_rope(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const auto* cache = (const ft_kv_cache*)(uintptr_t)whole(a[0]);
+  const at::Device dev = tensor(a[1], "k_pages").device();
+  const Tensor& k = tensor(a[3], "k");
+  const Tensor& v = tensor(a[4], "v");
+  const Tensor& slots = tensor(a[5], "slots");
+  const ft_float ty = float_type(k, "k");
+  const auto type = k.scalar_type();
+  TORCH_CHECK_VALUE(k.dim() == 3, "k must be (t, n_kv_head, head_dim)");
+  const int64_t t = k.size(0), dim = cache->head_dim;
+  const int64_t shape[3] = {t, cache->n_kv_head, dim};
+  const Rows ks = rows(k, "k", shape, type, dev), vs = rows(v, "v", shape, type, dev);
+  const ft_rotation r = rotation(a[7], a[6], a[8], t, dev);
+  ft_qkv_rows o = {};
+  o.k = k.data_ptr();
+  o.k_token = ks.token;
+  o.k_head = ks.head;
+  o.v = v.data_ptr();
+  o.v_token = vs.token;
+  o.v_head = vs.head;
+  o.k_weight = (const float*)plain(maybe(a[10], "k_weight"), "k_weight", at::kFloat, {dim}, dev);
+  o.eps = number(a[11]);
+  const void* at_slots = plain(&slots, "slots", at::kLong, {t}, dev);
+  Tensor out;
+  if (a[2] != Py_None) {
+    const Tensor& q = tensor(a[2], "q");
+    TORCH_CHECK_VALUE(q.dim() == 3, "q must be (t, heads, head_dim)");
+    const int64_t qshape[3] = {t, q.size(1), dim};
+    const Rows qs = rows(q, "q", qshape, type, dev);
+    out = a[12] == Py_None ? empty(qshape, q) : tensor(a[12], "q_out");
+    const Rows os = rows(out, "q_out", qshape, type, dev);
+    o.q = q.data_ptr();
+    o.q_token = qs.token;
+    o.q_head = qs.head;
+    o.n_head = q.size(1);
+    o.q_weight = (const float*)plain(maybe(a[9], "q_weight"), "q_weight", at::kFloat, {dim}, dev);
+    o.q_out = out.data_ptr();
+    o.out_token = os.token;
+    o.out_head = os.head;
+  } else {
+    TORCH_CHECK_VALUE(a[9] == Py_None && a[12] == Py_None, "q_out and q_weight are q's");
+  }
+  const On on(dev, a[13]);
+  run("ft_kv_store_rope", [&] { return ft_kv_store_rope(cache, &r, ty, &o, (const int64_t*)at_slots, t, on.stream); });
+  if (a[2] == Py_None) Py_RETURN_NONE;
+  return given(a[12], out);
+  END_HANDLE_TH_ERRORS
+}
+
+// x, weight, bias, residual, post_weight, post_bias, post (None: by the weights), gate, scale, layer, eps, act (-1: none), rows (None:
+// without an act), r, out, xq, stream
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const Tensor& x = tensor(a[0], "x");
+  TORCH_CHECK_VALUE(x.is_cuda() && x.dim() == 2, "x must be a device tensor (t, width)");
+  const ft_float ty = float_type(x, "x");
+  const at::Device dev = x.device();
+  const auto type = x.scalar_type();
+  const int64_t t = x.size(0), width = x.size(1);
+  const at::IntArrayRef shape = x.sizes();
+  ft_norm_opts o = {};
+  const auto vec = [&](int i, const char* name) { return (const float*)plain(maybe(a[i], name), name, at::kFloat, {width}, dev); };
+  o.weight = vec(1, "weight");
+  o.bias = vec(2, "bias");
+  o.post_weight = vec(4, "post_weight");
+  o.post_bias = vec(5, "post_bias");
+  o.post = a[6] == Py_None ? o.post_weight || o.post_bias : truth(a[6]);
+  o.scale = (float)number(a[8]);
+  TORCH_CHECK_VALUE(o.scale != 0.0f, "scale must not be 0");
+  o.layer = truth(a[9]);
+  o.eps = number(a[10]);
+  const int64_t ldx = line(x, "x", shape, type, dev);
+  if (const Tensor* p = maybe(a[3], "residual")) {
+    o.ld_residual = line(*p, "residual", shape, type, dev);
+    o.residual = p->data_ptr();
+  }
+  if (const Tensor* p = maybe(a[7], "gate")) {
+    const bool flat = p->dim() == 1;
+    TORCH_CHECK_VALUE((flat || p->dim() == 2) && p->scalar_type() == type && p->device() == dev && p->size(-1) == width &&
+                          (flat || p->size(0) == 1 || p->size(0) == t) && (width <= 1 || p->stride(-1) == 1),
+                      "gate must be (1 or ", t, ", ", width, ") ", type, " on ", dev, " with unit element stride, not ", p->sizes(), " ",
+                      p->dtype(), " on ", p->device());
+    if (!flat && p->size(0) > 1) o.ld_gate = p->stride(0);   // 0: one row for all
+    o.gate = p->data_ptr();
+  }
+  Tensor r, out, xq;
+  bool made_r = false;
+  if (a[13] != Py_None) {
+    r = tensor(a[13], "r");
+    o.ld_r = line(r, "r", shape, type, dev);
+  } else if (o.post || o.residual || o.gate || o.scale != 1.0f) {
+    r = empty(shape, x);
+    o.ld_r = width;
+    made_r = true;
+  }
+  if (r.defined()) o.r = r.data_ptr();
+  const int64_t act = whole(a[11]);
+  if (a[14] != Py_None) {
+    out = tensor(a[14], "out");
+    o.ld_out = line(out, "out", shape, type, dev);
+  } else if (a[12] == Py_None ? act < 0 : truth(a[12])) {
+    out = empty(shape, x);
+    o.ld_out = width;
+  }
+  if (out.defined()) o.out = out.data_ptr();
+  if (act >= 0) {
+    o.act = (ft_type)act;
+    const int64_t size[2] = {t, width / ft_block_elems(o.act) * (int64_t)ft_block_bytes(o.act)};
+    xq = a[15] == Py_None ? at::empty(size, x.options().dtype(at::kByte).requires_grad(false)) : tensor(a[15], "xq");
+    o.xq = plain(&xq, "xq", at::kByte, size, dev);
+  } else {
+    TORCH_CHECK_VALUE(a[15] == Py_None, "xq needs an act");
+  }
+  const On on(dev, a[16]);
+  run("ft_norm", [&] { return ft_norm(ty, x.data_ptr(), ldx, t, width, &o, on.stream); });
+  PyObject* pr = made_r ? THPVariable_Wrap(r) : a[13] == Py_None ? a[0] : a[13];
+  if (!made_r) Py_INCREF(pr);
+  PyObject* po = out.defined() ? given(a[14], out) : Py_NewRef(Py_None);
+  PyObject* pq = xq.defined() ? given(a[15], xq) : Py_NewRef(Py_None);
+  return Py_BuildValue("(NNN)", pr, po, pq);
+  END_HANDLE_TH_ERRORS
+}
+
+// x, a, b, ids, y, scales, ranks, out, workspace, stream
+PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const Tensor& x = tensor(a[0], "x");
+  const Tensor& wa = tensor(a[1], "a");
+  const Tensor& wb = tensor(a[2], "b");
+  const Tensor& ids = tensor(a[3], "ids");
+  TORCH_CHECK_VALUE(x.is_cuda() && x.dim() == 2 && wa.dim() == 3 && wb.dim() == 3,
+                    "x must be a device tensor (t, k), a (n_adapter, rank, k), b (n_adapter, n, rank)");
+  const ft_float tx = float_type(x, "x"), tw = float_type(wa, "a");
+  const at::Device dev = x.device();
+  const int64_t t = x.size(0), k = x.size(1), many = wa.size(0), rank = wa.size(1), n = wb.size(1);
+  const int64_t oshape[2] = {t, n};
+  const int64_t ldx = line(x, "x", x.sizes(), x.scalar_type(), dev);
+  const void* pa = plain(&wa, "a", wa.scalar_type(), {many, rank, k}, dev);
+  const void* pb = plain(&wb, "b", wa.scalar_type(), {many, n, rank}, dev);
+  const void* pi = plain(&ids, "ids", at::kInt, {t}, dev);
+  const Tensor* y = maybe(a[4], "y");
+  const int64_t ldy = y ? line(*y, "y", oshape, at::kFloat, dev) : 0;
+  ft_lora_opts o = {};
+  o.scales = (const float*)plain(maybe(a[5], "scales"), "scales", at::kFloat, {many}, dev);
+  o.ranks = (const int32_t*)plain(maybe(a[6], "ranks"), "ranks", at::kInt, {many}, dev);
+  const Tensor out = a[7] == Py_None ? at::empty(oshape, x.options().dtype(at::kFloat).requires_grad(false)) : tensor(a[7], "out");
+  const int64_t ldo = line(out, "out", oshape, at::kFloat, dev);
+  if (const Tensor* w = maybe(a[8], "workspace")) {
+    TORCH_CHECK_VALUE(w->device() == dev && w->is_contiguous(), "workspace must be contiguous on ", dev);
+    o.workspace = w->data_ptr();
+    o.workspace_bytes = w->nbytes();
+  }
+  const On on(dev, a[9]);
+  run("ft_lora", [&] {
+    return ft_lora(tx, x.data_ptr(), ldx, t, k, tw, pa, pb, many, rank, n, (const int32_t*)pi, y ? (const float*)y->data_ptr() : nullptr, ldy,
+                   (float*)out.data_ptr(), ldo, &o, on.stream);
+  });
+  return given(a[7], out);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* setup(PyObject*, PyObject* error) {
+  Py_INCREF(error);
+  Py_XDECREF(g_error);
+  g_error = error;
+  Py_RETURN_NONE;
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t), int N>
+PyObject* counted(PyObject* m, PyObject* const* a, Py_ssize_t n) {
+  if (n != N) return PyErr_Format(PyExc_TypeError, "takes %d arguments, not %zd", N, n);
+  return F(m, a, n);
+}
+PyMethodDef methods[] = {
+    {"setup", setup, METH_O, "FtError"},
+    {"rope", (PyCFunction)(void*)counted<rope, 8>, METH_FASTCALL, nullptr},
+    {"kv_store_rope", (PyCFunction)(void*)counted<kv_store_rope, 14>, METH_FASTCALL, nullptr},
+    {"norm", (PyCFunction)(void*)counted<norm, 17>, METH_FASTCALL, nullptr},
+    {"lora", (PyCFunction)(void*)counted<lora, 10>, METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ft_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__ft_bind(void) { return PyModule_Create(&module); }

@@ -10,7 +10,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 
 import torch  # loaded first so libft.so binds to the same HIP runtime as torch
 
@@ -21,7 +20,7 @@ TYPES = {"Q4_0": 0, "Q8_0": 1, "Q4_K": 2, "Q5_K": 3, "Q6_K": 4, "MXFP4": 5, "Q8_
          "Q2_K": 8, "Q3_K": 9, "Q4_1": 10, "Q5_0": 11, "Q5_1": 12}
 OPS = {"quantize": 0, "dequant": 1, "mmvq": 2, "moe_vec": 3, "grouped": 4, "block_dots": 5, "kv_cache": 6}
 FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-ACT_BLOCKS = {"Q8_1": (32, 36), "Q8_0": (32, 34), "Q8_K": (256, 292)}  # activation formats: elements and bytes of a block
+ACTS = ("Q8_1", "Q8_0", "Q8_K")  # the formats of activations
 STATUS = {0: "FT_OK", 1: "FT_ERR_INVALID_ARG", 2: "FT_ERR_UNSUPPORTED", 3: "FT_ERR_SHAPE",
           4: "FT_ERR_ALIGNMENT", 5: "FT_ERR_NO_SCRATCH", 6: "FT_ERR_HIP"}
 
@@ -56,13 +55,6 @@ class _AttnOpts(ctypes.Structure):
                 ("window", ctypes.c_int64), ("slopes", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
                 ("n_shared", ctypes.c_int64), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
-
-# ft_rotation, ft_qkv_rows, ft_norm_opts and ft_lora_opts, packed (a fifth of the time that a ctypes Structure takes);
-# 0 is a NULL pointer
-_pack_rotation = struct.Struct("@PPqqi0P").pack
-_pack_rows = struct.Struct("@PqqqPPqqPqqPPqqd").pack
-_pack_norm = struct.Struct("@PqPqiPPfidPPPqPqiP").pack
-_pack_lora = struct.Struct("@PPPN").pack
 
 _P, _I64 = ctypes.c_void_p, ctypes.c_int64
 
@@ -144,6 +136,23 @@ def lib() -> ctypes.CDLL:
             f.argtypes = args
         _lib = L
     return _lib
+
+
+_ext = None
+
+
+def _bind():
+    """The marshalling of the calls of a decoder layer's step, compiled against torch (raises if it was not built)."""
+    global _ext
+    if _ext is None:
+        lib()
+        try:
+            from . import _ft_bind
+        except ImportError as e:
+            raise RuntimeError(f"{_PKG}/_ft_bind.so does not load: run `python -m block_quantized_matvec_amd.build`") from e
+        _ft_bind.setup(FtError)
+        _ext = _ft_bind
+    return _ext
 
 
 def _check(status: int, what: str) -> None:
@@ -431,7 +440,7 @@ class KvCache:
         self.k, self.v = k, v
         self.n_pages, self.page_size, self.n_kv_head, self.head_dim = n, page_size, n_kv_head, head_dim
         self._c = _KvCache(TYPES[k], TYPES[v], k_pages.data_ptr(), v_pages.data_ptr(), n, page_size, n_kv_head, head_dim)
-        self._ref = ctypes.byref(self._c)
+        self._ref, self._at = ctypes.byref(self._c), ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_kv_head: int, head_dim: int, k: str = "Q8_0", v: str = "Q8_0",
@@ -589,32 +598,12 @@ def rope_table(n_pos: int, freqs, scale: float = 1.0, device="cuda", out: torch.
     return out
 
 
-def _rotation(table: torch.Tensor, positions: torch.Tensor, t: int, interleaved: bool, device) -> bytes:
-    if table.dim() != 2:
-        raise ValueError("table must be (n_pos, rot_dim)")
-    n_pos, rot = table.shape
-    return _pack_rotation(_plain(table, "table", torch.float32, (n_pos, rot), device),
-                          _plain(positions, "positions", torch.int32, (t,), device), n_pos, rot, interleaved)
-
-
 def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
          weight: torch.Tensor | None = None, eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The rows of x ((t, heads, dim), strided tokens and heads) turned by their token's position (int32 (t,)): pairs
     (j, j + rot_dim / 2), or neighbours with interleaved; elements from the table's width on stay.  weight (float32
     (dim,)): each row is first divided by its root mean square (with eps) and multiplied by weight.  out may be x."""
-    if not x.is_cuda or x.dim() != 3:
-        raise ValueError("x must be a device tensor (t, heads, dim)")
-    ty, dev, shape = _float_type(x, "x"), x.device, x.shape
-    t, heads, dim = shape
-    xs = _rows(x, "x", shape, x.dtype, dev)
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        os_ = (heads * dim, dim)
-    else:
-        os_ = _rows(out, "out", shape, x.dtype, dev)
-    _call("ft_rope", dev, stream, _rotation(table, positions, t, interleaved, dev), ty, x.data_ptr(), xs[0], xs[1], t, heads, dim,
-          None if weight is None else _plain(weight, "weight", torch.float32, (dim,), dev), eps, out.data_ptr(), os_[0], os_[1])
-    return out
+    return _bind().rope(x, positions, table, interleaved, weight, eps, out, stream)
 
 
 def kv_store_rope(cache: KvCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -622,44 +611,13 @@ def kv_store_rope(cache: KvCache, q: torch.Tensor | None, k: torch.Tensor, v: to
                   k_weight: torch.Tensor | None = None, eps: float = 1e-6, q_out: torch.Tensor | None = None, stream=None):
     """kv_store with the keys turned (and normed, with k_weight) on the way, and the queries q ((t, heads, head_dim),
     any number of heads, or None) turned in the same launch, as rope does: returns them (in q_out, which may be q)."""
-    t, dev, dim = k.shape[0], cache.device, cache.head_dim
-    ty, shape = _float_type(k, "k"), (t, cache.n_kv_head, dim)
-    ks, vs = _rows(k, "k", shape, k.dtype, dev), _rows(v, "v", shape, k.dtype, dev)
-    kw = 0 if k_weight is None else _plain(k_weight, "k_weight", torch.float32, (dim,), dev)
-    qp = qw = op = heads = 0
-    qs = os_ = (0, 0)
-    if q is not None:
-        heads = q.shape[1]
-        qshape = (t, heads, dim)
-        qs, qp = _rows(q, "q", qshape, k.dtype, dev), q.data_ptr()
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            os_ = (heads * dim, dim)
-        else:
-            os_ = _rows(q_out, "q_out", qshape, k.dtype, dev)
-        op = q_out.data_ptr()
-        if q_weight is not None:
-            qw = _plain(q_weight, "q_weight", torch.float32, (dim,), dev)
-    elif q_out is not None or q_weight is not None:
-        raise ValueError("q_out and q_weight are q's")
-    o = _pack_rows(qp, qs[0], qs[1], heads, qw, op, os_[0], os_[1], k.data_ptr(), ks[0], ks[1], kw, v.data_ptr(), vs[0], vs[1], eps)
-    _call("ft_kv_store_rope", dev, stream, cache._ref, _rotation(table, positions, t, interleaved, dev), ty, o,
-          _plain(slots, "slots", torch.int64, (t,), dev), t)
-    return q_out
+    return _bind().kv_store_rope(cache._at, cache.k_pages, q, k, v, slots, positions, table, interleaved, q_weight, k_weight, eps,
+                                 q_out, stream)
 
 
 # ---------------------------------------------------------------------------
 # the norm around a block
 # ---------------------------------------------------------------------------
-def _line(t: torch.Tensor, name: str, shape: tuple, dtype, device) -> int:
-    """Row stride of a (rows, width) tensor."""
-    ld, step = t.stride() if t.dim() == 2 else (0, 0)
-    if t.shape != shape or t.dtype is not dtype or t.device != device or (step != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be {shape} {dtype} on {device} with unit element stride, "
-                         f"not {tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
-    return ld if shape[0] > 1 else shape[1]
-
-
 def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
          residual: torch.Tensor | None = None, post_weight: torch.Tensor | None = None, post_bias: torch.Tensor | None = None,
          post: bool | None = None, gate: torch.Tensor | None = None, scale: float = 1.0, kind: str = "rms", eps: float = 1e-6,
@@ -670,61 +628,12 @@ def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor
     (1, width) or (width,) for all rows.  kind: "rms" or "layer".  act ("Q8_1", "Q8_0", "Q8_K"): n as quantized blocks,
     xq, and as rows only with rows=True; without act n is rows.  r is x where nothing is done to it.  What is not
     computed is None.  r and out may be x or residual."""
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError("x must be a device tensor (t, width)")
-    ty, dev, dt, shape = _float_type(x, "x"), x.device, x.dtype, x.shape
-    t, width = shape
     if kind not in ("rms", "layer"):
         raise ValueError(f"kind must be rms or layer, not {kind}")
-    if act is not None and act not in ACT_BLOCKS:
+    if act is not None and act not in ACTS:
         raise ValueError(f"act must be Q8_1, Q8_0 or Q8_K, not {act}")
-    if not scale:
-        raise ValueError("scale must not be 0")
-    if post is None:
-        post = post_weight is not None or post_bias is not None
-    one = (width,)
-    wp = 0 if weight is None else _plain(weight, "weight", torch.float32, one, dev)
-    bp = 0 if bias is None else _plain(bias, "bias", torch.float32, one, dev)
-    pwp = 0 if post_weight is None else _plain(post_weight, "post_weight", torch.float32, one, dev)
-    pbp = 0 if post_bias is None else _plain(post_bias, "post_bias", torch.float32, one, dev)
-    rp = rl = gp = gl = sp = sl = np = nl = qp = 0
-    if residual is not None:
-        rp, rl = residual.data_ptr(), _line(residual, "residual", shape, dt, dev)
-    if gate is not None:
-        if gate.dim() == 1:
-            gate = gate.unsqueeze(0)
-        if gate.shape[0] == 1 or gate.stride(0) == 0:
-            _line(gate[:1], "gate", (1, width), dt, dev)
-            if gate.shape[0] not in (1, t):
-                raise ValueError(f"gate must be (1 or {t}, {width})")
-        else:
-            gl = _line(gate, "gate", shape, dt, dev)
-        gp = gate.data_ptr()
-    if r is not None:
-        sp, sl = r.data_ptr(), _line(r, "r", shape, dt, dev)
-    elif post or rp or gp or scale != 1.0:
-        r = torch.empty_like(x, memory_format=torch.contiguous_format)
-        sp, sl = r.data_ptr(), width
-    else:
-        r = x
-    if out is not None:
-        np, nl = out.data_ptr(), _line(out, "out", shape, dt, dev)
-    elif rows or act is None and rows is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        np, nl = out.data_ptr(), width
-    if act is not None:
-        elems, size = ACT_BLOCKS[act]
-        size *= width // elems
-        if xq is None:
-            xq = x.new_empty((t, size), dtype=torch.uint8)
-            qp = xq.data_ptr()
-        else:
-            qp = _plain(xq, "xq", torch.uint8, (t, size), dev)
-    elif xq is not None:
-        raise ValueError("xq needs an act")
-    o = _pack_norm(rp, rl, gp, gl, post, pwp, pbp, scale, kind == "layer", eps, wp, bp, sp, sl, np, nl, TYPES[act] if act else 0, qp)
-    _call("ft_norm", dev, stream, ty, x.data_ptr(), _line(x, "x", shape, dt, dev), t, width, o)
-    return r, out, xq
+    return _bind().norm(x, weight, bias, residual, post_weight, post_bias, post, gate, scale, kind == "layer", eps,
+                        -1 if act is None else TYPES[act], rows, r, out, xq, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -746,26 +655,4 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, y
     (default: zeros) and out are float32 (t, n); out may be y.  scales float32, ranks int32 (n_adapter,): an
     adapter's own rank, what a and b hold beyond is not used.  workspace: uint8, lora_scratch_bytes (default: the
     stream's pool)."""
-    if not x.is_cuda or x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
-        raise ValueError("x must be a device tensor (t, k), a (n_adapter, rank, k), b (n_adapter, n, rank)")
-    tx, tw, dev = _float_type(x, "x"), _float_type(a, "a"), x.device
-    t, k = shape = x.shape
-    many, rank, _ = a.shape
-    n = b.shape[1]
-    if out is None:
-        out = x.new_empty((t, n), dtype=torch.float32) if y is None else torch.empty_like(y, memory_format=torch.contiguous_format)
-        ldo = n
-    else:
-        ldo = _line(out, "out", (t, n), torch.float32, dev)
-    wp = wb = 0
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    o = _pack_lora(0 if ranks is None else _plain(ranks, "ranks", torch.int32, (many,), dev),
-                   0 if scales is None else _plain(scales, "scales", torch.float32, (many,), dev), wp, wb)
-    yp, ldy = (None, 0) if y is None else (y.data_ptr(), _line(y, "y", (t, n), torch.float32, dev))
-    _call("ft_lora", dev, stream, tx, x.data_ptr(), _line(x, "x", shape, x.dtype, dev), t, k, tw,
-          _plain(a, "a", a.dtype, (many, rank, k), dev), _plain(b, "b", a.dtype, (many, n, rank), dev), many, rank, n,
-          _plain(ids, "ids", torch.int32, (t,), dev), yp, ldy, out.data_ptr(), ldo, o)
-    return out
+    return _bind().lora(x, a, b, ids, y, scales, ranks, out, workspace, stream)

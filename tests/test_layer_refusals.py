@@ -2,6 +2,7 @@
 before anything is enqueued), their sizes, and the angles of long contexts."""
 import ctypes
 import math
+import struct
 
 import pytest
 import torch
@@ -10,16 +11,18 @@ from block_quantized_matvec_amd import ft
 from tests.test_kv_refusals import FAKE, ODD, cache, status
 
 BIG = 1 << 41
+# ft_rotation, ft_qkv_rows, ft_norm_opts and ft_lora_opts; 0 is a NULL pointer
+ROTATION, ROWS, NORM, LORA = (struct.Struct(f) for f in ("@PPqqi0P", "@PqqqPPqqPqqPPqqd", "@PqPqiPPfidPPPqPqiP", "@PPPN"))
 
 
-def packed(pack, fields):
-    return pack(*(0 if v is None else v for v in fields.values()))
+def packed(struct, fields):
+    return struct.pack(*(0 if v is None else v for v in fields.values()))
 
 
 def rotation(**kw):
     f = dict(table=FAKE, positions=FAKE, n_pos=100, rot_dim=64, interleaved=0)
     f.update(kw)
-    return packed(ft._pack_rotation, f)
+    return packed(ROTATION, f)
 
 
 def rope(rot=None, ty=0, x=FAKE, xt=256, xh=64, t=2, heads=4, dim=64, weight=None, eps=0.0, out=FAKE + 4096, ot=256, oh=64):
@@ -30,7 +33,7 @@ def store(c=None, rot=None, ty=0, slots=FAKE, t=2, **o):
     f = dict(q=FAKE, q_token=256, q_head=64, n_head=4, q_weight=None, q_out=FAKE + 4096, out_token=256, out_head=64, k=FAKE, k_token=128,
              k_head=64, k_weight=None, v=FAKE, v_token=128, v_head=64, eps=0.0)
     f.update(o)
-    return status("ft_kv_store_rope", ctypes.byref(c or cache()), rot or rotation(), ty, packed(ft._pack_rows, f), slots, t,
+    return status("ft_kv_store_rope", ctypes.byref(c or cache()), rot or rotation(), ty, packed(ROWS, f), slots, t,
                   None)
 
 
@@ -38,13 +41,13 @@ def norm(ty=0, x=FAKE, ldx=64, rows=2, width=64, **o):
     f = dict(residual=None, ld_residual=0, gate=None, ld_gate=0, post=0, post_weight=None, post_bias=None, scale=0.0, layer=0, eps=0.0,
              weight=None, bias=None, r=None, ld_r=0, out=FAKE, ld_out=64, act=0, xq=None)
     f.update(o)
-    return status("ft_norm", ty, x, ldx, rows, width, packed(ft._pack_norm, f), None)
+    return status("ft_norm", ty, x, ldx, rows, width, packed(NORM, f), None)
 
 
 def lora(tx=0, x=FAKE, ldx=64, t=2, k=64, tw=2, a=FAKE, b=FAKE, many=3, rank=16, n=32, ids=FAKE, y=FAKE, ldy=32, out=FAKE, ldo=32, **o):
     f = dict(ranks=None, scales=None, workspace=None, workspace_bytes=0)
     f.update(o)
-    return status("ft_lora", tx, x, ldx, t, k, tw, a, b, many, rank, n, ids, y, ldy, out, ldo, packed(ft._pack_lora, f), None)
+    return status("ft_lora", tx, x, ldx, t, k, tw, a, b, many, rank, n, ids, y, ldy, out, ldo, packed(LORA, f), None)
 
 
 def test_rope_refused():
@@ -143,6 +146,13 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         ft.norm(x[0])
     with pytest.raises(ValueError):
         ft.lora(x[0], torch.zeros(1, 4, 64), torch.zeros(1, 8, 4), torch.zeros(4, dtype=torch.int32))
+    for call in (lambda: ft.rope([1.0], None, None), lambda: ft.norm(None), lambda: ft.lora(x[0], None, None, None),
+                 lambda: ft.norm(x[0], eps="1")):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    for kw in (dict(kind="mean"), dict(act="Q4_0")):
+        with pytest.raises(ValueError):
+            ft.norm(x[0], **kw)
 
 
 def test_angles():
