@@ -1,13 +1,14 @@
-// ft_bind.cpp -- argument marshalling of the operators of a decoder layer's step (ft.rope, ft.kv_store_rope, ft.norm,
-// ft.lora): torch tensors into pointers, sizes and strides, outputs allocated, a status raised.  Checks and calls
+// ft_bind.cpp -- argument marshalling of the operators of a decoder layer's step (ft.rope, ft.kv_store_rope, ft.kv_load,
+// ft.norm, ft.lora): torch tensors into pointers, sizes and strides, outputs allocated, a status raised.  Checks and calls
 // only, no arithmetic.  In Python the same took 4 to 6 us a call, longer than most of these kernels run at a
-// decode step; here it takes about one.
+// decode step; here it takes 0.4 to 0.6.
 #include <torch/csrc/python_headers.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -39,12 +40,12 @@ int64_t whole(PyObject* o) {
   return v;
 }
 
-ft_float float_type(const Tensor& t, const char* name) {
-  switch (t.scalar_type()) {
+ft_float float_type(at::ScalarType type, const char* name) {
+  switch (type) {
     case at::kFloat: return FT_F32;
     case at::kHalf: return FT_F16;
     case at::kBFloat16: return FT_BF16;
-    default: TORCH_CHECK_VALUE(false, name, " must be float32, float16 or bfloat16, not ", t.dtype());
+    default: TORCH_CHECK_VALUE(false, name, " must be float32, float16 or bfloat16, not ", type);
   }
 }
 // pointer of a contiguous tensor of this type, shape and device (null: not given)
@@ -130,7 +131,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Tensor& x = tensor(a[0], "x");
   TORCH_CHECK_VALUE(x.is_cuda() && x.dim() == 3, "x must be a device tensor (t, heads, dim)");
-  const ft_float ty = float_type(x, "x");
+  const ft_float ty = float_type(x.scalar_type(), "x");
   const at::Device dev = x.device();
   const auto type = x.scalar_type();
   const int64_t t = x.size(0), heads = x.size(1), dim = x.size(2);
@@ -156,7 +157,7 @@ PyObject* kv_store_rope(PyObject*, PyObject* const* a, Py_ssize_t) {
   const Tensor& k = tensor(a[3], "k");
   const Tensor& v = tensor(a[4], "v");
   const Tensor& slots = tensor(a[5], "slots");
-  const ft_float ty = float_type(k, "k");
+  const ft_float ty = float_type(k.scalar_type(), "k");
   const auto type = k.scalar_type();
   TORCH_CHECK_VALUE(k.dim() == 3, "k must be (t, n_kv_head, head_dim)");
   const int64_t t = k.size(0), dim = cache->head_dim;
@@ -199,13 +200,40 @@ PyObject* kv_store_rope(PyObject*, PyObject* const* a, Py_ssize_t) {
   END_HANDLE_TH_ERRORS
 }
 
+// address of the cache's structure, its k_pages, slots, dtype of new tensors, k, v, stream
+PyObject* kv_load(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const auto* cache = (const ft_kv_cache*)(uintptr_t)whole(a[0]);
+  const Tensor& pages = tensor(a[1], "k_pages");
+  const at::Device dev = pages.device();
+  const Tensor& slots = tensor(a[2], "slots");
+  TORCH_CHECK_VALUE(slots.dim() == 1, "slots must be (t,)");
+  TORCH_CHECK_TYPE(THPDtype_Check(a[3]), "dtype must be a torch.dtype");
+  const Tensor *ko = maybe(a[4], "k"), *vo = maybe(a[5], "v");
+  const auto type = ko ? ko->scalar_type() : vo ? vo->scalar_type() : reinterpret_cast<THPDtype*>(a[3])->scalar_type;
+  const int64_t t = slots.size(0);
+  const int64_t shape[3] = {t, cache->n_kv_head, cache->head_dim};
+  const ft_float ty = float_type(type, "dtype");
+  const auto fresh = pages.options().dtype(type).requires_grad(false);
+  const Tensor k = ko ? *ko : at::empty(shape, fresh), v = vo ? *vo : at::empty(shape, fresh);
+  const Rows ks = rows(k, "k", shape, type, dev), vs = rows(v, "v", shape, type, dev);
+  const void* at_slots = plain(&slots, "slots", at::kLong, {t}, dev);
+  const On on(dev, a[6]);
+  run("ft_kv_load", [&] {
+    return ft_kv_load(cache, (const int64_t*)at_slots, t, ty, k.data_ptr(), ks.token, ks.head, v.data_ptr(), vs.token, vs.head, on.stream);
+  });
+  PyObject* pk = given(a[4], k);
+  return Py_BuildValue("(NN)", pk, given(a[5], v));
+  END_HANDLE_TH_ERRORS
+}
+
 // x, weight, bias, residual, post_weight, post_bias, post (None: by the weights), gate, scale, layer, eps, act (-1: none), rows (None:
 // without an act), r, out, xq, stream
 PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Tensor& x = tensor(a[0], "x");
   TORCH_CHECK_VALUE(x.is_cuda() && x.dim() == 2, "x must be a device tensor (t, width)");
-  const ft_float ty = float_type(x, "x");
+  const ft_float ty = float_type(x.scalar_type(), "x");
   const at::Device dev = x.device();
   const auto type = x.scalar_type();
   const int64_t t = x.size(0), width = x.size(1);
@@ -282,7 +310,7 @@ PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t) {
   const Tensor& ids = tensor(a[3], "ids");
   TORCH_CHECK_VALUE(x.is_cuda() && x.dim() == 2 && wa.dim() == 3 && wb.dim() == 3,
                     "x must be a device tensor (t, k), a (n_adapter, rank, k), b (n_adapter, n, rank)");
-  const ft_float tx = float_type(x, "x"), tw = float_type(wa, "a");
+  const ft_float tx = float_type(x.scalar_type(), "x"), tw = float_type(wa.scalar_type(), "a");
   const at::Device dev = x.device();
   const int64_t t = x.size(0), k = x.size(1), many = wa.size(0), rank = wa.size(1), n = wb.size(1);
   const int64_t oshape[2] = {t, n};
@@ -327,6 +355,7 @@ PyMethodDef methods[] = {
     {"setup", setup, METH_O, "FtError"},
     {"rope", (PyCFunction)(void*)counted<rope, 8>, METH_FASTCALL, nullptr},
     {"kv_store_rope", (PyCFunction)(void*)counted<kv_store_rope, 14>, METH_FASTCALL, nullptr},
+    {"kv_load", (PyCFunction)(void*)counted<kv_load, 7>, METH_FASTCALL, nullptr},
     {"norm", (PyCFunction)(void*)counted<norm, 17>, METH_FASTCALL, nullptr},
     {"lora", (PyCFunction)(void*)counted<lora, 10>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -474,24 +474,7 @@ def kv_load(cache: KvCache, slots: torch.Tensor, dtype=torch.float32, k: torch.T
             v: torch.Tensor | None = None, stream=None):
     """The slots' rows as plain numbers: (k, v), each (t, n_kv_head, head_dim) of dtype, into the given tensors where
     there are any (whose type then counts).  A negative slot gives zeros."""
-    t, dev = slots.shape[0], cache.device
-    shape = (t, cache.n_kv_head, cache.head_dim)
-    if k is not None or v is not None:
-        dtype = (k if k is not None else v).dtype
-    if dtype not in FLOATS:
-        raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
-    if k is None and v is None:
-        k, v = torch.empty((2, *shape), dtype=dtype, device=dev).unbind()
-        ks = vs = (cache.n_kv_head * cache.head_dim, cache.head_dim)
-    else:
-        if k is None:
-            k = torch.empty(shape, dtype=dtype, device=dev)
-        elif v is None:
-            v = torch.empty(shape, dtype=dtype, device=dev)
-        ks, vs = _rows(k, "k", shape, dtype, dev), _rows(v, "v", shape, dtype, dev)
-    _call("ft_kv_load", dev, stream, cache._ref, _plain(slots, "slots", torch.int64, (t,), dev), t, FLOATS[dtype],
-          k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
-    return k, v
+    return _bind().kv_load(cache._at, cache.k_pages, slots, dtype, k, v, stream)
 
 
 def attn_kv_scratch_bytes(cache: KvCache, n_tok: int, n_head: int, n_seq: int, max_kv: int, causal: bool = True,

@@ -1,5 +1,5 @@
-"""GPU: what ft.rope, ft.kv_store_rope, ft.norm and ft.lora refuse of their tensors before the library is called, and the
-objects that they return."""
+"""GPU: what ft.rope, ft.kv_store_rope, ft.kv_load, ft.norm and ft.lora refuse of their tensors before the library is
+called, and the objects that they return."""
 import gc
 import weakref
 
@@ -29,6 +29,12 @@ def store():
         table=some(10, 32), q_weight=some(D), k_weight=some(D), q_out=some(T, H, D))
 
 
+def load():
+    cache = ft.KvCache.empty(2, 16, 2, D)
+    ft.kv_store(cache, 127 * some(T, 2, D), 127 * some(T, 2, D), torch.arange(T, device="cuda"))
+    return lambda **kw: ft.kv_load(cache, **kw), dict(slots=torch.arange(T, device="cuda"), k=some(T, 2, D), v=some(T, 2, D))
+
+
 def norm():
     return ft.norm, dict(x=some(T, W), weight=some(W), bias=some(W), residual=some(T, W), post_weight=some(W), post_bias=some(W), gate=some(T, W),
                          act="Q8_1", r=some(T, W), out=some(T, W), xq=some(T, W // 32 * 36, dtype=torch.uint8))
@@ -40,7 +46,7 @@ def lora():
                          workspace=some(ft.lora_scratch_bytes(T, W, 5, 8), dtype=torch.uint8))
 
 
-@pytest.mark.parametrize("make", (rope, store, norm, lora))
+@pytest.mark.parametrize("make", (rope, store, load, norm, lora))
 def test_wrong_tensors_refused(make):
     need_gpu()
     f, good = make()
@@ -87,12 +93,12 @@ def test_refusals_name_their_cause():
         ft.rope(x, at, table, stream=3)
 
 
-@pytest.mark.parametrize("make", (rope, store, norm, lora))
+@pytest.mark.parametrize("make", (rope, store, load, norm, lora))
 def test_given_tensors_come_back(make):
     """What was given is returned itself and kept by nobody; what was not is new, of its own, and needs no gradient."""
     need_gpu()
     f, good = make()
-    outs = [n for n in ("r", "q_out", "out", "xq") if n in good]
+    outs = [n for n in (("k", "v") if make is load else ("r", "q_out", "out", "xq")) if n in good]
     got = f(**good)
     got = got if isinstance(got, tuple) else (got,)
     assert all(a is good[n] for a, n in zip(got, outs)) and len(got) == len(outs)
@@ -134,6 +140,17 @@ def test_without_queries():
     x = some(T, 2, D)
     cache = ft.KvCache.empty(2, 16, 2, D)
     assert ft.kv_store_rope(cache, None, x, x, torch.arange(T, device="cuda"), some(T, dtype=torch.int32), some(10, 32)) is None
+
+
+def test_what_a_load_returns():
+    need_gpu()
+    f, good = load()
+    for kw, dtype in ((dict(), torch.float32), (dict(dtype=torch.float16), torch.float16), (dict(v=some(T, 2, D, dtype=torch.bfloat16)), torch.bfloat16)):
+        k, v = f(slots=good["slots"], **kw)
+        assert k.dtype is v.dtype is dtype and k.shape == v.shape == (T, 2, D) and torch.equal(k, torch.full_like(k, 127)) and torch.equal(v, k)
+    for kw in (dict(dtype=torch.float64), dict(k=good["k"], v=some(T, 2, D, dtype=torch.float16)), dict(dtype="float32")):
+        with pytest.raises((ValueError, TypeError)):
+            f(slots=good["slots"], **kw)
 
 
 def test_no_tokens():
