@@ -15,9 +15,9 @@
 // stays in fp32 between the launches.
 //
 // Bound by memory: x, y, out and the rows of A and B that the tokens name.  4096 fp32 tokens,
-// 4096 -> 14336, rank 64, bf16 weights (540 MB): 120 us (4.5 TB/s; a 2 GiB copy 5.0), of which 100 the
-// second product, 21 the first.  1500 bf16 tokens of 16 adapters in any order, 14336 -> 4096, ranks
-// 8 to 64 (110 MB): 42 us, a third of it two chains of dependent loads (tile, tokens, rows) and the sort.
+// 4096 -> 14336, rank 64, bf16 weights (540 MB): 118 us (4.6 TB/s; a 2 GiB copy 5.0), of which 99 the
+// second product, 19 the first.  1500 bf16 tokens of 16 adapters in any order, 14336 -> 4096, ranks
+// 8 to 64 (110 MB): 41 us, a third of it two chains of dependent loads (tile, tokens, rows) and the sort.
 // 48 tokens of 32 adapters, ranks 8 to 64, fp16 weights, 4096 -> 14336: 25 us; B's rows of 8 to 32 ranks lie
 // 128 bytes apart, and whole lines come (59 MB for 27).  One token, 4096 -> 6144, rank 16: 7.2 us, two launches; in
 // one launch, every workgroup reading all of A again, 9.5 to 11.
@@ -208,17 +208,17 @@ __device__ __forceinline__ bool lora_find(const LoraIo& io, int index, int* s_wo
 }
 
 // h[part][token][rank] of 16 * G of a tile's tokens, for 16 * R ranks and one share of the long axis, which
-// the four waves take in turn, U steps of 32 elements at a time, a run's loads ahead of the one before.  G is 4
+// the W waves take in turn, U steps of 32 elements at a time, a run's loads ahead of the one before.  G is 4
 // where tiles are likely to be full: a row of A is then read once for 64 tokens (it comes from an L2 that all
 // of them share, at half of the time of the whole kernel with G = 1).  The share is the fastest of
 // the grid's indices: with eight of them, or four, each of the chip's eight L2s holds its own part of A.
-template <int TX, int TW, int R, int G>
-__global__ void __launch_bounds__(256)
+template <int TX, int TW, int R, int G, int W>
+__global__ void __launch_bounds__(64 * W)
 lora_shrink_kernel(LoraIo io) {
   constexpr bool F16 = TX == FT_F16 && TW == FT_F16;
   constexpr int PX = LORA_PIECES<TX, TW>, PW = LORA_PIECES<TW, TX>, RX = LORA_WORDS<TX>, RW = LORA_WORDS<TW>;
-  constexpr int U = G * RX + R * RW <= 8 ? 2 : 1;
-  __shared__ __align__(16) float s_h[3][G * R][64][4];   // the other waves' sums
+  constexpr int U = G * RX + R * RW <= 8 && (G * R < 16 || PW == 1) ? 2 : 1;   // the last: for the registers
+  __shared__ __align__(16) float s_h[W - 1][G * R][64][4];   // the other waves' sums
   extern __shared__ int s_word[];
   LoraTile tile;
   if (io.sorted) {
@@ -283,18 +283,18 @@ lora_shrink_kernel(LoraIo io) {
       }
   };
   // whole runs of U steps, the next one's loads ahead of each; then what is left of the share, by the last wave
-  const int run = 32 * U, runs = (last - first) / run, mine = runs > wave ? (runs - wave + 3) / 4 : 0, k0 = first + run * wave;
+  const int run = 32 * U, runs = (last - first) / run, mine = runs > wave ? (runs - wave + W - 1) / W : 0, k0 = first + run * wave;
   if (mine > 0) load(k0, rx[0], rw[0]);
   for (int j = 0; j < mine; j += 2) {
-    if (j + 1 < mine) load(k0 + (j + 1) * 4 * run, rx[1], rw[1]);
+    if (j + 1 < mine) load(k0 + (j + 1) * W * run, rx[1], rw[1]);
 #pragma unroll
     for (int u = 0; u < U; ++u) sum(rx[0][u], rw[0][u]);
     if (j + 1 >= mine) break;
-    if (j + 2 < mine) load(k0 + (j + 2) * 4 * run, rx[0], rw[0]);
+    if (j + 2 < mine) load(k0 + (j + 2) * W * run, rx[0], rw[0]);
 #pragma unroll
     for (int u = 0; u < U; ++u) sum(rx[1][u], rw[1][u]);
   }
-  if (wave == 3)
+  if (wave == W - 1)
     for (int e = first + runs * run; e < last; e += 32) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
@@ -304,12 +304,12 @@ lora_shrink_kernel(LoraIo io) {
         if (i < n_rt) lora_load_end<TW>(a, arow[i] + e, e + 8 * quad, last, rw[0][0][i]);
       sum(rx[0][0], rw[0][0]);
     }
-  // the four waves' sums meet: wave (g R + i) % 4 adds up group g's ranks 16 i ..
+  // the waves' sums meet: wave (g R + i) % W adds up group g's ranks 16 i ..
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int to = (g * R + i) & 3;
+      const int to = (g * R + i) & (W - 1);
       if (wave != to && g < n_g && i < n_rt) *(f32x4*)s_h[wave - (wave > to)][g * R + i][lane] = acc[g][i];
     }
   __syncthreads();
@@ -317,11 +317,11 @@ lora_shrink_kernel(LoraIo io) {
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int to = (g * R + i) & 3;
+      const int to = (g * R + i) & (W - 1);
       if (wave != to || i >= n_rt || tile.first + 16 * g + l16 >= tile.count) continue;
       f32x4 s = {0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)   // in the waves' order, whichever group the token is in
+      for (int j = 0; j < W; ++j)   // in the waves' order, whichever group the token is in
         s += j == to ? acc[g][i] : *(const f32x4*)s_h[j - (j > to)][g * R + i][lane];
       *(f32x4*)(io.h + ((int64_t)blockIdx.x * io.t + tok[g]) * io.rank_pad + r0 + 16 * i + 4 * quad) = s;
     }
@@ -607,22 +607,32 @@ static LoraPlan lora_plan(int64_t t, int64_t k, int rank, int64_t adapters) {
   return p;
 }
 
-template <int TX, int TW, int G>
-static hipError_t lora_shrink(const LoraIo& io, dim3 grid, hipStream_t st) {
+template <int TX, int TW, int R, int G>
+static hipError_t lora_shrink_r(const LoraIo& io, bool eight, dim3 grid, hipStream_t st) {
   const int words = io.sorted ? 0 : (io.adapters + 1) * 4;   // for finding tiles
-  if (io.rank <= 16) lora_shrink_kernel<TX, TW, 1, G><<<grid, 256, words, st>>>(io);
-  else if (io.rank <= 32) lora_shrink_kernel<TX, TW, 2, G><<<grid, 256, words, st>>>(io);
-  else lora_shrink_kernel<TX, TW, 4, G><<<grid, 256, words, st>>>(io);
+  // 64 ranks with many pieces: no registers for eight waves
+  if constexpr (G == 4 && (R < 4 || LORA_PIECES<TX, TW> + LORA_PIECES<TW, TX> <= 4))
+    if (eight) {
+      lora_shrink_kernel<TX, TW, R, G, 8><<<grid, 512, words, st>>>(io);
+      return hipGetLastError();
+    }
+  lora_shrink_kernel<TX, TW, R, G, 4><<<grid, 256, words, st>>>(io);
   return hipGetLastError();
 }
+template <int TX, int TW, int G>
+static hipError_t lora_shrink(const LoraIo& io, bool eight, dim3 grid, hipStream_t st) {
+  if (io.rank <= 16) return lora_shrink_r<TX, TW, 1, G>(io, eight, grid, st);
+  if (io.rank <= 32) return lora_shrink_r<TX, TW, 2, G>(io, eight, grid, st);
+  return lora_shrink_r<TX, TW, 4, G>(io, eight, grid, st);
+}
 template <int TW>
-static hipError_t lora_shrink_x(int tx, bool full, const LoraIo& io, dim3 grid, hipStream_t st) {
+static hipError_t lora_shrink_x(int tx, bool full, bool eight, const LoraIo& io, dim3 grid, hipStream_t st) {
   if (full) {
-    if (tx == FT_F32) return lora_shrink<FT_F32, TW, 4>(io, grid, st);
-    return tx == FT_F16 ? lora_shrink<FT_F16, TW, 4>(io, grid, st) : lora_shrink<FT_BF16, TW, 4>(io, grid, st);
+    if (tx == FT_F32) return lora_shrink<FT_F32, TW, 4>(io, eight, grid, st);
+    return tx == FT_F16 ? lora_shrink<FT_F16, TW, 4>(io, eight, grid, st) : lora_shrink<FT_BF16, TW, 4>(io, eight, grid, st);
   }
-  if (tx == FT_F32) return lora_shrink<FT_F32, TW, 1>(io, grid, st);
-  return tx == FT_F16 ? lora_shrink<FT_F16, TW, 1>(io, grid, st) : lora_shrink<FT_BF16, TW, 1>(io, grid, st);
+  if (tx == FT_F32) return lora_shrink<FT_F32, TW, 1>(io, eight, grid, st);
+  return tx == FT_F16 ? lora_shrink<FT_F16, TW, 1>(io, eight, grid, st) : lora_shrink<FT_BF16, TW, 1>(io, eight, grid, st);
 }
 // tiles of 16 columns that a wave takes at a time; ranks past 64 fill the registers with fewer
 static int lora_wide(bool wide, bool one, int rank) { return !wide || rank > 128 ? 1 : one || rank > 64 ? 2 : 4; }
@@ -684,18 +694,21 @@ hipError_t ftk_launch_lora(const LoraArgs& a, void* scratch, hipStream_t st) {
     lora_plan_kernel<<<1, 1024, (size_t)(a.adapters + 1) * 4, st>>>(a.ids, a.ranks, a.rank, io.t, io.adapters, io.order, io.tiles, io.n_tiles);
     e = hipGetLastError();
   }
+  const int64_t cus = ftk_num_cus();
   const dim3 shrink((unsigned)p.parts, (unsigned)(p.full ? p.tiles : p.sixteens), (unsigned)((a.rank + LORA_RANKS - 1) / LORA_RANKS));
   // many columns a wave where that still gives every CU a workgroup; full tiles take a block of them, others so
   // many that three workgroups come to a CU
-  const int64_t cus = ftk_num_cus();
   const bool wide = p.likely * a.n >= 256 * cus, one = !p.full;
   const int64_t cols = 64 * lora_wide(wide, one, a.rank), across = (a.n + cols - 1) / cols;
   io.blocks = one || a.rank > 128 ? (int)std::max<int64_t>(1, std::min(across, p.likely * across / (3 * cus))) : 1;
   const dim3 expand((unsigned)((across + io.blocks - 1) / io.blocks), (unsigned)p.tiles);   // tiles < 2^15: t is at most 2^20
+  // A workgroup that has a CU to itself keeps more loads on their way with eight waves (4096 fp32 tokens of one
+  // adapter: first product 21.3 -> 19.0 us); where several share a CU four are faster (20000 bf16 tokens of 40, rank 64: 74 -> 69)
+  const bool eight = p.likely * shrink.x * shrink.z <= cus;
   if (e == hipSuccess)
-    e = a.wtype == FT_F32   ? lora_shrink_x<FT_F32>(a.xtype, p.full, io, shrink, st)
-        : a.wtype == FT_F16 ? lora_shrink_x<FT_F16>(a.xtype, p.full, io, shrink, st)
-                            : lora_shrink_x<FT_BF16>(a.xtype, p.full, io, shrink, st);
+    e = a.wtype == FT_F32   ? lora_shrink_x<FT_F32>(a.xtype, p.full, eight, io, shrink, st)
+        : a.wtype == FT_F16 ? lora_shrink_x<FT_F16>(a.xtype, p.full, eight, io, shrink, st)
+                            : lora_shrink_x<FT_BF16>(a.xtype, p.full, eight, io, shrink, st);
   if (e == hipSuccess)
     e = a.wtype == FT_F32   ? lora_expand_c<FT_F32>(wide, one, io, expand, st)
         : a.wtype == FT_F16 ? lora_expand_c<FT_F16>(wide, one, io, expand, st)
