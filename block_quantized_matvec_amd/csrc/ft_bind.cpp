@@ -208,8 +208,8 @@ PyObject* kv_load(PyObject*, PyObject* const* a, Py_ssize_t) {
   const at::Device dev = pages.device();
   const Tensor& slots = tensor(a[2], "slots");
   TORCH_CHECK_VALUE(slots.dim() == 1, "slots must be (t,)");
-  TORCH_CHECK_TYPE(THPDtype_Check(a[3]), "dtype must be a torch.dtype");
   const Tensor *ko = maybe(a[4], "k"), *vo = maybe(a[5], "v");
+  TORCH_CHECK_VALUE(ko || vo || THPDtype_Check(a[3]), "dtype must be float32, float16 or bfloat16");
   const auto type = ko ? ko->scalar_type() : vo ? vo->scalar_type() : reinterpret_cast<THPDtype*>(a[3])->scalar_type;
   const int64_t t = slots.size(0);
   const int64_t shape[3] = {t, cache->n_kv_head, cache->head_dim};
