@@ -8,9 +8,11 @@
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Device.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include "ft.h"
 
@@ -81,16 +83,18 @@ struct On {
       stream = c10::hip::getCurrentHIPStream(dev.index()).stream();
       return;
     }
-    const auto get = [&](const char* name) {
-      PyObject* a = PyObject_GetAttrString(o, name);
-      if (!a) throw python_error();
-      const unsigned long long v = PyLong_AsUnsignedLongLongMask(a);
-      Py_DECREF(a);
-      if (PyErr_Occurred()) throw python_error();
-      return v;
+    // any object with the two attributes of a torch stream that name it: its device and its handle
+    const auto held = [](PyObject* p) {
+      if (!p) throw python_error();
+      return THPObjectPtr(p);
     };
-    TORCH_CHECK_VALUE((int64_t)get("device_index") == dev.index(), "the stream is on another device than the tensors, which are on ", dev);
-    stream = (ft_stream_t)(uintptr_t)get("cuda_stream");
+    THPObjectPtr at = held(PyObject_GetAttrString(o, "device")), want = held(THPDevice_New(dev));
+    const int same = PyObject_RichCompareBool(at.get(), want.get(), Py_EQ);
+    if (same < 0) throw python_error();
+    TORCH_CHECK_VALUE(same, "the stream is on another device than the tensors, which are on ", dev);
+    THPObjectPtr handle = held(PyObject_GetAttrString(o, "cuda_stream"));
+    stream = (ft_stream_t)(uintptr_t)PyLong_AsUnsignedLongLongMask(handle.get());
+    if (PyErr_Occurred()) throw python_error();
   }
 };
 template <class Call>

@@ -30,3 +30,23 @@ def test_a_given_side_decides_the_type(stored, side):
         assert torch.equal(k, torch.full_like(k, 127.0)) and torch.equal(v, k)
     with pytest.raises(ValueError, match="dtype must be"):
         ft.kv_load(*stored, dtype=None)
+
+
+class Handle:
+    """A stream as its device and handle, and nothing else."""
+
+    def __init__(self, stream):
+        self.device, self.cuda_stream = stream.device, stream.cuda_stream
+
+
+def test_a_stream_is_its_device_and_handle(stored):
+    cache, slots = stored
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    k, v = ft.kv_load(cache, slots, stream=Handle(stream))
+    stream.synchronize()
+    assert torch.equal(k, torch.full_like(k, 127.0)) and torch.equal(v, k)
+    elsewhere = Handle(stream)
+    elsewhere.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="the stream is on"):
+        ft.kv_load(cache, slots, stream=elsewhere)
