@@ -64,8 +64,8 @@ def _bind() -> None:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            "-I" + os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", "/opt/rocm/include",
-           os.path.join(CSRC, "ft_bind.cpp"), "-o", tmp, "-L" + PKG, "-l:libft.so", "-L" + os.path.join(torch, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+           os.path.join(CSRC, "ft_bind.cpp"), "-o", tmp, "-L" + os.path.join(torch, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for ft_bind.cpp:\n{r.stdout}\n{r.stderr}")

@@ -21,6 +21,17 @@ namespace {
 using at::Tensor;
 PyObject* g_error = nullptr;   // ft.FtError
 
+// The library's entry points, as ft.py loaded them (from wherever: this extension does not link to a copy of its own)
+struct Library {
+  decltype(&ft_rope) rope;
+  decltype(&ft_kv_store_rope) kv_store_rope;
+  decltype(&ft_kv_load) kv_load;
+  decltype(&ft_norm) norm;
+  decltype(&ft_lora) lora;
+  decltype(&ft_block_elems) block_elems;
+  decltype(&ft_block_bytes) block_bytes;
+} g_lib = {};
+
 const Tensor& tensor(PyObject* o, const char* name) {
   TORCH_CHECK_TYPE(THPVariable_Check(o), name, " must be a tensor, not ", Py_TYPE(o)->tp_name);
   return THPVariable_Unpack(o);
@@ -147,7 +158,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t) {
   const Rows os = rows(out, "out", x.sizes(), type, dev);
   const On on(dev, a[7]);
   run("ft_rope", [&] {
-    return ft_rope(&r, ty, x.data_ptr(), xs.token, xs.head, t, heads, dim, w, eps, out.data_ptr(), os.token, os.head, on.stream);
+    return g_lib.rope(&r, ty, x.data_ptr(), xs.token, xs.head, t, heads, dim, w, eps, out.data_ptr(), os.token, os.head, on.stream);
   });
   return given(a[6], out);
   END_HANDLE_TH_ERRORS
@@ -198,7 +209,7 @@ PyObject* kv_store_rope(PyObject*, PyObject* const* a, Py_ssize_t) {
     TORCH_CHECK_VALUE(a[9] == Py_None && a[12] == Py_None, "q_out and q_weight are q's");
   }
   const On on(dev, a[13]);
-  run("ft_kv_store_rope", [&] { return ft_kv_store_rope(cache, &r, ty, &o, (const int64_t*)at_slots, t, on.stream); });
+  run("ft_kv_store_rope", [&] { return g_lib.kv_store_rope(cache, &r, ty, &o, (const int64_t*)at_slots, t, on.stream); });
   if (a[2] == Py_None) Py_RETURN_NONE;
   return given(a[12], out);
   END_HANDLE_TH_ERRORS
@@ -224,7 +235,7 @@ PyObject* kv_load(PyObject*, PyObject* const* a, Py_ssize_t) {
   const void* at_slots = plain(&slots, "slots", at::kLong, {t}, dev);
   const On on(dev, a[6]);
   run("ft_kv_load", [&] {
-    return ft_kv_load(cache, (const int64_t*)at_slots, t, ty, k.data_ptr(), ks.token, ks.head, v.data_ptr(), vs.token, vs.head, on.stream);
+    return g_lib.kv_load(cache, (const int64_t*)at_slots, t, ty, k.data_ptr(), ks.token, ks.head, v.data_ptr(), vs.token, vs.head, on.stream);
   });
   PyObject* pk = given(a[4], k);
   return Py_BuildValue("(NN)", pk, given(a[5], v));
@@ -289,14 +300,14 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
   if (out.defined()) o.out = out.data_ptr();
   if (act >= 0) {
     o.act = (ft_type)act;
-    const int64_t size[2] = {t, width / ft_block_elems(o.act) * (int64_t)ft_block_bytes(o.act)};
+    const int64_t size[2] = {t, width / g_lib.block_elems(o.act) * (int64_t)g_lib.block_bytes(o.act)};
     xq = a[15] == Py_None ? at::empty(size, x.options().dtype(at::kByte).requires_grad(false)) : tensor(a[15], "xq");
     o.xq = plain(&xq, "xq", at::kByte, size, dev);
   } else {
     TORCH_CHECK_VALUE(a[15] == Py_None, "xq needs an act");
   }
   const On on(dev, a[16]);
-  run("ft_norm", [&] { return ft_norm(ty, x.data_ptr(), ldx, t, width, &o, on.stream); });
+  run("ft_norm", [&] { return g_lib.norm(ty, x.data_ptr(), ldx, t, width, &o, on.stream); });
   PyObject* pr = made_r ? THPVariable_Wrap(r) : a[13] == Py_None ? a[0] : a[13];
   if (!made_r) Py_INCREF(pr);
   PyObject* po = out.defined() ? given(a[14], out) : Py_NewRef(Py_None);
@@ -336,18 +347,30 @@ PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t) {
   }
   const On on(dev, a[9]);
   run("ft_lora", [&] {
-    return ft_lora(tx, x.data_ptr(), ldx, t, k, tw, pa, pb, many, rank, n, (const int32_t*)pi, y ? (const float*)y->data_ptr() : nullptr, ldy,
+    return g_lib.lora(tx, x.data_ptr(), ldx, t, k, tw, pa, pb, many, rank, n, (const int32_t*)pi, y ? (const float*)y->data_ptr() : nullptr, ldy,
                    (float*)out.data_ptr(), ldo, &o, on.stream);
   });
   return given(a[7], out);
   END_HANDLE_TH_ERRORS
 }
 
-PyObject* setup(PyObject*, PyObject* error) {
-  Py_INCREF(error);
+// FtError, the addresses of Library's entry points in their order
+PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  Library l;
+  l.rope = (decltype(l.rope))whole(a[1]);
+  l.kv_store_rope = (decltype(l.kv_store_rope))whole(a[2]);
+  l.kv_load = (decltype(l.kv_load))whole(a[3]);
+  l.norm = (decltype(l.norm))whole(a[4]);
+  l.lora = (decltype(l.lora))whole(a[5]);
+  l.block_elems = (decltype(l.block_elems))whole(a[6]);
+  l.block_bytes = (decltype(l.block_bytes))whole(a[7]);
+  g_lib = l;
+  Py_INCREF(a[0]);
   Py_XDECREF(g_error);
-  g_error = error;
+  g_error = a[0];
   Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
 }
 
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t), int N>
@@ -356,7 +379,7 @@ PyObject* counted(PyObject* m, PyObject* const* a, Py_ssize_t n) {
   return F(m, a, n);
 }
 PyMethodDef methods[] = {
-    {"setup", setup, METH_O, "FtError"},
+    {"setup", (PyCFunction)(void*)counted<setup, 8>, METH_FASTCALL, nullptr},
     {"rope", (PyCFunction)(void*)counted<rope, 8>, METH_FASTCALL, nullptr},
     {"kv_store_rope", (PyCFunction)(void*)counted<kv_store_rope, 14>, METH_FASTCALL, nullptr},
     {"kv_load", (PyCFunction)(void*)counted<kv_load, 7>, METH_FASTCALL, nullptr},

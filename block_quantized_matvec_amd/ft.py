@@ -139,18 +139,20 @@ def lib() -> ctypes.CDLL:
 
 
 _ext = None
+# the entry points that the compiled marshalling calls, in its order
+_MARSHALLED = ("ft_rope", "ft_kv_store_rope", "ft_kv_load", "ft_norm", "ft_lora", "ft_block_elems", "ft_block_bytes")
 
 
 def _bind():
     """The marshalling of the calls of a decoder layer's step, compiled against torch (raises if it was not built)."""
     global _ext
     if _ext is None:
-        lib()
+        L = lib()
         try:
             from . import _ft_bind
         except ImportError as e:
             raise RuntimeError(f"{_PKG}/_ft_bind.so does not load: run `python -m block_quantized_matvec_amd.build`") from e
-        _ft_bind.setup(FtError)
+        _ft_bind.setup(FtError, *(ctypes.cast(getattr(L, f), _P).value for f in _MARSHALLED))
         _ext = _ft_bind
     return _ext
 
