@@ -143,18 +143,28 @@ _ext = None
 _MARSHALLED = ("ft_rope", "ft_kv_store_rope", "ft_kv_load", "ft_norm", "ft_lora", "ft_block_elems", "ft_block_bytes")
 
 
-def _bind():
-    """The marshalling of the calls of a decoder layer's step, compiled against torch (raises if it was not built)."""
+def _marshalling():
+    """The marshalling of the calls of a decoder layer's step, compiled against torch, or the ImportError where it does
+    not load."""
     global _ext
     if _ext is None:
         L = lib()
         try:
             from . import _ft_bind
         except ImportError as e:
-            raise RuntimeError(f"{_PKG}/_ft_bind.so does not load: run `python -m block_quantized_matvec_amd.build`") from e
-        _ft_bind.setup(FtError, *(ctypes.cast(getattr(L, f), _P).value for f in _MARSHALLED))
-        _ext = _ft_bind
+            _ext = e
+        else:
+            _ft_bind.setup(FtError, *(ctypes.cast(getattr(L, f), _P).value for f in _MARSHALLED))
+            _ext = _ft_bind
     return _ext
+
+
+def _bind():
+    """The compiled marshalling (raises if it was not built)."""
+    ext = _ext or _marshalling()
+    if isinstance(ext, ImportError):
+        raise RuntimeError(f"{_PKG}/_ft_bind.so does not load: run `python -m block_quantized_matvec_amd.build`") from ext
+    return ext
 
 
 def _check(status: int, what: str) -> None:
@@ -476,7 +486,21 @@ def kv_load(cache: KvCache, slots: torch.Tensor, dtype=torch.float32, k: torch.T
             v: torch.Tensor | None = None, stream=None):
     """The slots' rows as plain numbers: (k, v), each (t, n_kv_head, head_dim) of dtype, into the given tensors where
     there are any (whose type then counts).  A negative slot gives zeros."""
-    return _bind().kv_load(cache._at, cache.k_pages, slots, dtype, k, v, stream)
+    ext = _ext or _marshalling()
+    if not isinstance(ext, ImportError):
+        return ext.kv_load(cache._at, cache.k_pages, slots, dtype, k, v, stream)
+    # with the library alone: the same from here, 2 us a call longer
+    t, dev = slots.shape[0], cache.device
+    shape = (t, cache.n_kv_head, cache.head_dim)
+    if k is not None or v is not None:
+        dtype = (k if k is not None else v).dtype
+    if dtype not in FLOATS:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
+    k, v = (torch.empty(shape, dtype=dtype, device=dev) if x is None else x for x in (k, v))
+    ks, vs = _rows(k, "k", shape, dtype, dev), _rows(v, "v", shape, dtype, dev)
+    _call("ft_kv_load", dev, stream, cache._ref, _plain(slots, "slots", torch.int64, (t,), dev), t, FLOATS[dtype],
+          k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
+    return k, v
 
 
 def attn_kv_scratch_bytes(cache: KvCache, n_tok: int, n_head: int, n_seq: int, max_kv: int, causal: bool = True,

@@ -1,4 +1,6 @@
 """GPU: forms of ft.kv_load's arguments that its callers use."""
+import sys
+
 import pytest
 import torch
 
@@ -50,3 +52,23 @@ def test_a_stream_is_its_device_and_handle(stored):
     elsewhere.device = torch.device("cuda", 1)
     with pytest.raises(ValueError, match="the stream is on"):
         ft.kv_load(cache, slots, stream=elsewhere)
+
+
+def test_the_library_alone_is_enough(stored, monkeypatch):
+    """Without the compiled marshalling (a package with libft.so only) rows are read back all the same, and refused the same way."""
+    want = ft.kv_load(*stored, dtype=torch.bfloat16)
+    monkeypatch.setattr(ft, "_ext", None)
+    monkeypatch.setitem(sys.modules, "block_quantized_matvec_amd._ft_bind", None)
+    monkeypatch.delattr("block_quantized_matvec_amd._ft_bind", raising=False)
+    with pytest.raises(RuntimeError, match="does not load"):
+        ft.norm(torch.ones(2, 32, device="cuda"))
+    cache, slots = stored
+    for kw in (dict(dtype=torch.bfloat16), dict(k=want[0].clone()), dict(dtype=None, v=want[1].clone()), dict(dtype=torch.bfloat16, stream=torch.cuda.current_stream())):
+        got = ft.kv_load(cache, slots, **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert all(g is kw[n] for n, g in zip("kv", got) if n in kw)
+    for bad in (dict(dtype=torch.float64), dict(dtype=None), dict(k=want[0][:2]), dict(v=want[1].cpu())):
+        with pytest.raises(ValueError):
+            ft.kv_load(cache, slots, **bad)
+    with pytest.raises((ValueError, ft.FtError)):
+        ft.kv_load(cache, slots.int())
