@@ -181,6 +181,13 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream):
+    """torch.cuda.stream of a call's stream (nothing for None)."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):  # its handle is enough
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=getattr(stream, "device", None))
+    return torch.cuda.stream(stream)
+
+
 def _dev(t: torch.Tensor, name: str) -> torch.Tensor:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -596,7 +603,8 @@ def rope_table(n_pos: int, freqs, scale: float = 1.0, device="cuda", out: torch.
     """The table of rope and kv_store_rope, float32 (n_pos, 2 * len(freqs)): row p the cosines, then the sines of
     p * freqs, times scale, computed in 64 bits.  freqs: a list, or a float64 tensor on the device."""
     if not isinstance(freqs, torch.Tensor):
-        freqs = torch.tensor(freqs, dtype=torch.float64, device=device)
+        with _on(stream):  # this call's own: nobody else can keep it until the stream has read it
+            freqs = torch.tensor(freqs, dtype=torch.float64, device=device)
     dev, half = freqs.device, freqs.numel()
     if not freqs.is_cuda:
         raise ValueError("freqs must be a list or a device tensor")
