@@ -14,6 +14,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
+#include <optional>
+
 #include "ft.h"
 
 namespace {
@@ -85,10 +87,17 @@ int64_t line(const Tensor& t, const char* name, at::IntArrayRef shape, at::Scala
 }
 Tensor empty(at::IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options().requires_grad(false)); }
 
-// The caller's stream (None: the current one of the device), with the device as the library's current one.
+// The caller's stream (None: the current one of the device), with the device as the library's current one, and the
+// stream as torch's current one: tensors made meanwhile are that stream's, as under torch.cuda.stream.  (Memory that the
+// current stream gave back may still be in use there; the allocator hands it out to tensors of that stream only.)
 struct On {
   c10::OptionalDeviceGuard guard;
   ft_stream_t stream;
+  std::optional<c10::hip::HIPStream> before;
+  On(const On&) = delete;
+  ~On() {
+    if (before) c10::hip::setCurrentHIPStream(*before);
+  }
   On(at::Device dev, PyObject* o) : guard(dev) {
     if (o == Py_None) {
       stream = c10::hip::getCurrentHIPStream(dev.index()).stream();
@@ -106,6 +115,8 @@ struct On {
     THPObjectPtr handle = held(PyObject_GetAttrString(o, "cuda_stream"));
     stream = (ft_stream_t)(uintptr_t)PyLong_AsUnsignedLongLongMask(handle.get());
     if (PyErr_Occurred()) throw python_error();
+    before = c10::hip::getCurrentHIPStream(dev.index());
+    c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal((hipStream_t)stream, dev.index()));
   }
 };
 template <class Call>
@@ -154,9 +165,9 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t) {
   const ft_rotation r = rotation(a[2], a[1], a[3], t, dev);
   const float* w = (const float*)plain(maybe(a[4], "weight"), "weight", at::kFloat, {dim}, dev);
   const double eps = number(a[5]);
+  const On on(dev, a[7]);
   const Tensor out = a[6] == Py_None ? empty(x.sizes(), x) : tensor(a[6], "out");
   const Rows os = rows(out, "out", x.sizes(), type, dev);
-  const On on(dev, a[7]);
   run("ft_rope", [&] {
     return g_lib.rope(&r, ty, x.data_ptr(), xs.token, xs.head, t, heads, dim, w, eps, out.data_ptr(), os.token, os.head, on.stream);
   });
@@ -189,6 +200,7 @@ PyObject* kv_store_rope(PyObject*, PyObject* const* a, Py_ssize_t) {
   o.k_weight = (const float*)plain(maybe(a[10], "k_weight"), "k_weight", at::kFloat, {dim}, dev);
   o.eps = number(a[11]);
   const void* at_slots = plain(&slots, "slots", at::kLong, {t}, dev);
+  const On on(dev, a[13]);
   Tensor out;
   if (a[2] != Py_None) {
     const Tensor& q = tensor(a[2], "q");
@@ -208,7 +220,6 @@ PyObject* kv_store_rope(PyObject*, PyObject* const* a, Py_ssize_t) {
   } else {
     TORCH_CHECK_VALUE(a[9] == Py_None && a[12] == Py_None, "q_out and q_weight are q's");
   }
-  const On on(dev, a[13]);
   run("ft_kv_store_rope", [&] { return g_lib.kv_store_rope(cache, &r, ty, &o, (const int64_t*)at_slots, t, on.stream); });
   if (a[2] == Py_None) Py_RETURN_NONE;
   return given(a[12], out);
@@ -230,10 +241,10 @@ PyObject* kv_load(PyObject*, PyObject* const* a, Py_ssize_t) {
   const int64_t shape[3] = {t, cache->n_kv_head, cache->head_dim};
   const ft_float ty = float_type(type, "dtype");
   const auto fresh = pages.options().dtype(type).requires_grad(false);
+  const On on(dev, a[6]);
   const Tensor k = ko ? *ko : at::empty(shape, fresh), v = vo ? *vo : at::empty(shape, fresh);
   const Rows ks = rows(k, "k", shape, type, dev), vs = rows(v, "v", shape, type, dev);
   const void* at_slots = plain(&slots, "slots", at::kLong, {t}, dev);
-  const On on(dev, a[6]);
   run("ft_kv_load", [&] {
     return g_lib.kv_load(cache, (const int64_t*)at_slots, t, ty, k.data_ptr(), ks.token, ks.head, v.data_ptr(), vs.token, vs.head, on.stream);
   });
@@ -278,6 +289,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
     if (!flat && p->size(0) > 1) o.ld_gate = p->stride(0);   // 0: one row for all
     o.gate = p->data_ptr();
   }
+  const On on(dev, a[16]);
   Tensor r, out, xq;
   bool made_r = false;
   if (a[13] != Py_None) {
@@ -306,7 +318,6 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
   } else {
     TORCH_CHECK_VALUE(a[15] == Py_None, "xq needs an act");
   }
-  const On on(dev, a[16]);
   run("ft_norm", [&] { return g_lib.norm(ty, x.data_ptr(), ldx, t, width, &o, on.stream); });
   PyObject* pr = made_r ? THPVariable_Wrap(r) : a[13] == Py_None ? a[0] : a[13];
   if (!made_r) Py_INCREF(pr);
@@ -338,6 +349,7 @@ PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t) {
   ft_lora_opts o = {};
   o.scales = (const float*)plain(maybe(a[5], "scales"), "scales", at::kFloat, {many}, dev);
   o.ranks = (const int32_t*)plain(maybe(a[6], "ranks"), "ranks", at::kInt, {many}, dev);
+  const On on(dev, a[9]);
   const Tensor out = a[7] == Py_None ? at::empty(oshape, x.options().dtype(at::kFloat).requires_grad(false)) : tensor(a[7], "out");
   const int64_t ldo = line(out, "out", oshape, at::kFloat, dev);
   if (const Tensor* w = maybe(a[8], "workspace")) {
@@ -345,7 +357,6 @@ PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t) {
     o.workspace = w->data_ptr();
     o.workspace_bytes = w->nbytes();
   }
-  const On on(dev, a[9]);
   run("ft_lora", [&] {
     return g_lib.lora(tx, x.data_ptr(), ldx, t, k, tw, pa, pb, many, rank, n, (const int32_t*)pi, y ? (const float*)y->data_ptr() : nullptr, ldy,
                    (float*)out.data_ptr(), ldo, &o, on.stream);

@@ -4,6 +4,9 @@ Every step of the path runs in the gfx950 kernels behind the C ABI declared in
 include/ft.h; this module turns torch tensors (device memory, current stream)
 into pointers and sizes and raises on a non-OK status.  There is no CPU
 fallback: if libft.so is missing or cannot load, every call raises.
+
+A call with `stream` does all of its work on that stream, as under torch.cuda.stream(stream): the tensors that
+it makes are the stream's, and the caller orders the stream after the work that its inputs come from.
 """
 from __future__ import annotations
 
@@ -188,6 +191,15 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor of the call's stream.  (Memory that the current stream gave back may still be in use there; the
+    allocator hands it out to tensors of that stream only.)"""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t: torch.Tensor, name: str) -> torch.Tensor:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -225,7 +237,7 @@ def quantize_act(act: str, x: torch.Tensor, out: torch.Tensor | None = None, str
         raise ValueError("x must have unit element stride and rows at least k apart")
     ldx = x.stride(0) if rows > 1 else k
     if out is None:
-        out = torch.empty((rows, row_bytes(act, k)), dtype=torch.uint8, device=x.device)
+        out = _new((rows, row_bytes(act, k)), torch.uint8, x.device, stream)
     _check(lib().ft_quantize_act(TYPES[act], _ptr(x), rows, k, ldx, _ptr(out), _stream(stream)), "ft_quantize_act")
     return out
 
@@ -234,7 +246,7 @@ def dequant(w: str, blocks: torch.Tensor, rows: int, k: int, out: torch.Tensor |
             stream=None) -> torch.Tensor:
     _dev(blocks, "blocks")
     if out is None:
-        out = torch.empty((rows, k), dtype=torch.float32, device=blocks.device)
+        out = _new((rows, k), torch.float32, blocks.device, stream)
     _check(lib().ft_dequant(TYPES[w], _ptr(blocks), rows, k, _ptr(out), _stream(stream)), "ft_dequant")
     return out
 
@@ -244,7 +256,7 @@ def mul_mat_vec_q(w: str, W: torch.Tensor, n: int, k: int, act: str, xq: torch.T
     _dev(W, "W")
     _dev(xq, "xq")
     if out is None:
-        out = torch.empty((t, n), dtype=torch.float32, device=W.device)
+        out = _new((t, n), torch.float32, W.device, stream)
     _check(lib().ft_mul_mat_vec_q(TYPES[w], _ptr(W), n, k, TYPES[act], _ptr(xq), t, _ptr(out), out.shape[-1],
                                   _stream(stream)), "ft_mul_mat_vec_q")
     return out
@@ -255,9 +267,9 @@ def moe_route(logits: torch.Tensor, topk: int, ids: torch.Tensor | None = None, 
     _dev(logits, "logits")
     t, e = logits.shape
     if ids is None:
-        ids = torch.empty((t, topk), dtype=torch.int32, device=logits.device)
+        ids = _new((t, topk), torch.int32, logits.device, stream)
     if w is None:
-        w = torch.empty((t, topk), dtype=torch.float32, device=logits.device)
+        w = _new((t, topk), torch.float32, logits.device, stream)
     _check(lib().ft_moe_route(_ptr(logits), t, e, topk, _ptr(ids), _ptr(w), _stream(stream)), "ft_moe_route")
     return ids, w
 
@@ -313,9 +325,9 @@ def moe_route_ex(logits: torch.Tensor, topk: int, score: str = "softmax", bias: 
         raise ValueError("topk, n_group, topk_group and group_top start at 1")
     dev = logits.device
     if ids is None:
-        ids = torch.empty((t, topk), dtype=torch.int32, device=dev)
+        ids = _new((t, topk), torch.int32, dev, stream)
     if w is None:
-        w = torch.empty((t, topk), dtype=torch.float32, device=dev)
+        w = _new((t, topk), torch.float32, dev, stream)
     o = _RouteOpts(score == "sigmoid", None if bias is None else _plain(bias, "bias", torch.float32, (e,), dev), n_group,
                    topk_group or 0, group_top, not renorm, scale)
     _call("ft_moe_route_ex", dev, stream, logits.data_ptr(), ty, t, e, ld if t > 1 else e, topk, ctypes.byref(o),
@@ -326,9 +338,9 @@ def moe_route_ex(logits: torch.Tensor, topk: int, score: str = "softmax", bias: 
 def moe_sort(ids: torch.Tensor, n_expert: int, stream=None):
     _dev(ids, "ids")
     t, topk = ids.shape
-    counts = torch.empty(n_expert, dtype=torch.int32, device=ids.device)
-    offsets = torch.empty(n_expert + 1, dtype=torch.int32, device=ids.device)
-    pairs = torch.empty(t * topk, dtype=torch.int32, device=ids.device)
+    counts = _new(n_expert, torch.int32, ids.device, stream)
+    offsets = _new(n_expert + 1, torch.int32, ids.device, stream)
+    pairs = _new(t * topk, torch.int32, ids.device, stream)
     _check(lib().ft_moe_sort(_ptr(ids), t, topk, n_expert, _ptr(counts), _ptr(offsets), _ptr(pairs),
                              _stream(stream)), "ft_moe_sort")
     return counts, offsets, pairs
@@ -345,7 +357,7 @@ def _moe(entry: str, w: str, w_gate, w_up, w_down, n_expert: int, hidden: int, i
     if topk is None:
         topk = ids.shape[1]
     if out is None:
-        out = torch.empty((t, hidden), dtype=torch.float32, device=x.device)
+        out = _new((t, hidden), torch.float32, x.device, stream)
     taps = taps or {}
     opts = _MoeOpts(route, direct_max_t, *(_ptr(taps.get(k)) for k in ("g", "u", "h", "hq", "down")), _ptr(in_hq),
                     _ptr(logits), _ptr(ids_out), _ptr(w_out))
@@ -384,7 +396,7 @@ def grouped_gemm_q(w: str, W: torch.Tensor, n_expert: int, n: int, k: int, act: 
     _dev(ids, "ids")
     t, topk = ids.shape
     if out is None:
-        out = torch.empty((t * topk, n), dtype=torch.float32, device=W.device)
+        out = _new((t * topk, n), torch.float32, W.device, stream)
     _check(lib().ft_grouped_gemm_q(TYPES[w], _ptr(W), n_expert, n, k, TYPES[act], _ptr(xq),
                                    1 if x_per_pair else 0, _ptr(ids), t, topk, _ptr(out), _stream(stream)),
            "ft_grouped_gemm_q")
@@ -396,7 +408,7 @@ def debug_block_dots(w: str, W: torch.Tensor, n: int, k: int, act: str, xq: torc
     _dev(W, "W")
     _dev(xq, "xq")
     sub = 16 if w in ("Q6_K", "Q2_K", "Q3_K") else 32
-    out = torch.empty((t, n, k // sub), dtype=torch.int32, device=W.device)
+    out = _new((t, n, k // sub), torch.int32, W.device, stream)
     _check(lib().ft_debug_block_dots(TYPES[w], _ptr(W), n, k, TYPES[act], _ptr(xq), t, _ptr(out),
                                      _stream(stream)), "ft_debug_block_dots")
     return out
@@ -410,7 +422,8 @@ def debug_ceiling(which: str, buf: torch.Tensor | None = None, iters: int = 0, o
     code = {"stream_read": 0, "mfma_i8": 1, "dot4": 2, "mfma_i8_k64": 3}[which]
     dev = buf.device if buf is not None else torch.device("cuda")
     if out is None:
-        out = torch.zeros(1, dtype=torch.int32, device=dev)
+        with _on(stream):
+            out = torch.zeros(1, dtype=torch.int32, device=dev)
     nbytes = 0
     if buf is not None:
         _dev(buf, "buf")
@@ -503,7 +516,7 @@ def kv_load(cache: KvCache, slots: torch.Tensor, dtype=torch.float32, k: torch.T
         dtype = (k if k is not None else v).dtype
     if dtype not in FLOATS:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
-    k, v = (torch.empty(shape, dtype=dtype, device=dev) if x is None else x for x in (k, v))
+    k, v = (_new(shape, dtype, dev, stream) if x is None else x for x in (k, v))
     ks, vs = _rows(k, "k", shape, dtype, dev), _rows(v, "v", shape, dtype, dev)
     _call("ft_kv_load", dev, stream, cache._ref, _plain(slots, "slots", torch.int64, (t,), dev), t, FLOATS[dtype],
           k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
@@ -544,7 +557,7 @@ def attn_kv(cache: KvCache, q: torch.Tensor, table: torch.Tensor, kv_len: torch.
     if scale is not None and not scale:
         raise ValueError("scale must not be 0")
     if out is None:
-        out = q.new_empty(shape)
+        out = _new(shape, q.dtype, dev, stream)
     os_ = _rows(out, "out", shape, q.dtype, dev)
     o = _AttnOpts(scale or 0.0, softcap, not causal, window,
                   None if slopes is None else _plain(slopes, "slopes", torch.float32, (n_head,), dev),
@@ -609,7 +622,7 @@ def rope_table(n_pos: int, freqs, scale: float = 1.0, device="cuda", out: torch.
     if not freqs.is_cuda:
         raise ValueError("freqs must be a list or a device tensor")
     if out is None:
-        out = torch.empty((n_pos, 2 * half), dtype=torch.float32, device=dev)
+        out = _new((n_pos, 2 * half), torch.float32, dev, stream)
     _call("ft_rope_table", dev, stream, _plain(freqs, "freqs", torch.float64, (half,), dev), half, n_pos, scale,
           _plain(out, "out", torch.float32, (n_pos, 2 * half), dev))
     return out
