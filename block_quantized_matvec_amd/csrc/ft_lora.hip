@@ -408,7 +408,7 @@ lora_expand_kernel(LoraIo io) {
     for (int i = 0; i < C; ++i) {
       if (tok[i] < 0) continue;
       float* q = io.out + tok[i] * io.ldo + at;
-      const f32x4 o = y[i] + acc[i];
+      const f32x4 o = tile.rank ? y[i] + acc[i] : y[i];   // without ranks y's own bits: -0 + 0 is +0
       if (at + 4 <= n) {
         if constexpr (STREAM) __builtin_nontemporal_store(o, (f32x4_any*)q);
         else *(f32x4_any*)q = o;
