@@ -8,11 +8,12 @@
 // and out = y + B h (lora_expand_kernel), whose workgroups first add up the shares of h.
 //
 // Both products run on v_mfma_f32_16x16x32 with the weights' rows as rows of the result and
-// the tokens as columns, so that a token's values come from its own row alone.  Accuracy is fp32's:
+// the tokens as columns, so that a token's values come from its own row alone.  Accuracy is about fp32's:
 // an fp32 operand is taken as three bf16 pieces (8 bits each, cut off, so their sum is exact), an
-// fp16 one as two, and the products of pieces down to 2^-16 of the first are summed (those left out
-// are below 2^-24 of it).  fp16 rows with fp16 weights, and bf16 with bf16, are one product.  h
-// stays in fp32 between the launches.
+// fp16 one as two, and six (or five) products of pieces are summed.  Left out are the second piece times
+// the third, both ways: as pieces are cut off these are below 2^-7 and 2^-15 of a value and have its sign, so
+// a product comes out short by up to 2^-21 of itself (2^-24.5 on average).  fp16 rows with fp16 weights, and bf16
+// with bf16, are one product and exact.  h stays in fp32 between the launches.
 //
 // Bound by memory: x, y, out and the rows of A and B that the tokens name.  4096 fp32 tokens,
 // 4096 -> 14336, rank 64, bf16 weights (540 MB): 118 us (4.6 TB/s; a 2 GiB copy 5.0), of which 99 the

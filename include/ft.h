@@ -479,7 +479,8 @@ ft_status ft_norm(ft_float type, const void* x, int64_t ldx, int64_t rows, int64
    itself (same stride).  A: [n_adapter][rank][k], B: [n_adapter][n][rank], both of w_type.  ids [t] int32:
    one outside 0 .. n_adapter-1 names no adapter, and its row of out is y's.  ranks (nullable) [n_adapter]
    int32: only that many ranks of an adapter count (0: none; at most rank), what A and B hold beyond is
-   not used.  scales (nullable: 1) [n_adapter] fp32.  About fp32 accuracy for every type; A x is held in fp32.  A
+   not used.  scales (nullable: 1) [n_adapter] fp32.  About fp32 accuracy for every type: sums and A x are held in
+   fp32, and a product with an fp32 operand (A x is one) comes out short by at most 2^-21 of itself.  A
    row of x with a NaN or an infinity gives NaN in its own row of out only.  t, k, n <= 2^20, rank 1 .. 256,
    n_adapter <= 8192.  Scratch: the stream's pool, or the caller's `workspace` (16-byte aligned,
    ft_lora_scratch_bytes). */

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from block_quantized_matvec_amd import ft
+from tests import layer_ref as ref
 from tests.gpu_util import need_gpu
 from tests.test_gpu_lora import case, check
 
@@ -100,3 +101,22 @@ def test_long_axis_of_full_tiles():
         for tx, tw, rank in (("f32", "bf16", 64), ("bf16", "bf16", 32), ("f16", "f16", 16), ("f32", "f32", 64)):
             x, a, b, y, ids, sc = case(t, k, 300, 5, rank, tx, tw, seed=k)
             some(ft.lora(x, a, b, ids, y=y, scales=sc), x, a, b, ids, y, sc)
+
+
+@pytest.mark.parametrize("t", [3, 100])
+def test_pieces_cut_off(t):
+    """Operands whose pieces are all as large as they can be, and of one sign: what the products of pieces leave out is
+    largest, and adds up.  A value's first piece holds 8 bits, so the second is below 2^-7 of the value and the third below 2^-15;
+    left out are second times third and third times second (2 * 2^-22 of the product) and third times third (2^-30).  It happens
+    twice, for A x and for B h (h has what bits it has: the bound holds for any).  Sums: k and rank roundings of 2^-24 at most."""
+    need_gpu()
+    for tw in ("f32", "f16"):
+        v = 1 + 2.0 ** -7 - 2.0 ** -23 if tw == "f32" else 1 + 2.0 ** -7 - 2.0 ** -10
+        k, n, rank = 512, 40, 8
+        x = torch.full((t, k), 1 + 2.0 ** -7 - 2.0 ** -23, device="cuda")
+        a, b = torch.full((1, rank, k), v, device="cuda").to(ref.DT[tw]), torch.full((1, n, rank), v, device="cuda").to(ref.DT[tw])
+        out = ft.lora(x, a, b, torch.zeros(t, dtype=torch.int32, device="cuda")).double()
+        w = a[0, 0, 0].double().item()
+        want = rank * w * (k * w * x[0, 0].double().item())
+        off = ((out - want).abs() / want).max().item()
+        assert off <= 2 * (2.0 ** -21 + 2.0 ** -30) + (k + rank) * 2.0 ** -24, (tw, off)
