@@ -31,17 +31,17 @@ namespace ftk {
 // grid: (token tiles, heads, 2): z = 0 the keys, 1 the values
 template <int TK, int TV, int NB>
 __global__ void __launch_bounds__(256)
-kv_store_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int64_t t, int span) {
+kv_store_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int t, int span) {
   __shared__ KvTokens s_tok;
   __shared__ __align__(16) uint8_t s_tile[NB * 32 * KV_PITCH];
-  const int64_t t0 = (int64_t)blockIdx.x * span;
+  const int t0 = blockIdx.x * span;
   t = min(t, t0 + span);
   if (blockIdx.z == 0) kv_store_side<TK, NB, false>(k, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
   else kv_store_side<TV, NB, true>(v, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
 }
 
 template <int T, int NB, bool V>
-__device__ __forceinline__ void kv_load_side(const KvIo& io, int ftype, const int64_t* slots, int64_t t, int64_t t0,
+__device__ __forceinline__ void kv_load_side(const KvIo& io, int ftype, const int64_t* slots, int t, int t0,
                                              int head, KvTokens& tk, uint8_t* s_tile) {
   constexpr int D = NB * 32;
   constexpr int ROWS = T == FT_Q8_0 ? D : D / 2;
@@ -49,36 +49,25 @@ __device__ __forceinline__ void kv_load_side(const KvIo& io, int ftype, const in
   const int tid = threadIdx.x;
   uint64_t valid;
   const int hb = kv_head_bytes(T, D, io.page), cb = kv_code_bytes(T, D, io.page);
-  const uint64_t runs = kv_runs(io, kv_slot(slots, t0, t), hb, head, tk, valid);
+  const uint64_t runs = kv_runs<V>(io, kv_slot(slots, t0, t), hb, head, tk, valid);
   __syncthreads();
-  const int nt = (int)min((int64_t)KV_TILE, t - t0);
+  const int nt = min(KV_TILE, t - t0);
   if constexpr (V) {   // the codes into the transposed tile first
-    // (both loops: four loads per thread in flight before the first is put down)
     const int n_run = __popcll(runs), n_rest = __popcll(valid & ~cover16(runs));
-    for (int i0 = tid; i0 < n_run * ROWS; i0 += 1024) {   // a row's runs side by side: often one piece of a page
-      u32x4 w[4];
+    for (int i = tid; i < n_run * ROWS; i += 256) {   // a row's runs side by side: often one piece of a page
+      const int r = i / n_run, c = i - r * n_run;
+      const int tok = nth_bit(runs, c);
+      const u32x4 w = *(const u32x4*)(io.pages + tk.at[tok] + r * io.page + tk.key[tok]);
+      uint8_t* dst = s_tile + r * KV_PITCH + tok;
+      if ((tok & 3) == 0) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = i0 + 256 * q, r = i / n_run;
-        if (i >= n_run * ROWS) continue;
-        const int tok = nth_bit(runs, i - r * n_run);
-        w[q] = *(const u32x4*)(io.pages + tk.at[tok] + r * io.page + tk.key[tok]);
-      }
+        for (int k = 0; k < 4; ++k) ((uint32_t*)dst)[k] = w[k];
+      } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = i0 + 256 * q, r = i / n_run;
-        if (i >= n_run * ROWS) continue;
-        const int tok = nth_bit(runs, i - r * n_run);
-        uint8_t* dst = s_tile + r * KV_PITCH + tok;
-        if ((tok & 3) == 0) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ((uint32_t*)dst)[k] = w[q][k];
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) dst[k] = (uint8_t)(w[q][k >> 2] >> (8 * (k & 3)));
-        }
+        for (int k = 0; k < 16; ++k) dst[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
       }
     }
+    // four loads per thread in flight before the first is put down
     for (int i0 = tid; i0 < n_rest * ROWS; i0 += 1024) {
       uint8_t b[4];
 #pragma unroll
@@ -137,17 +126,17 @@ __device__ __forceinline__ void kv_load_side(const KvIo& io, int ftype, const in
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = fmaf(df, (float)((w[n][e >> 2] >> (8 * (e & 3))) & 255u), less);
       if (u.tok < nt)
-        kv_store_n<8>(ftype, io.x, (t0 + u.tok) * io.x_token + head * io.x_head + 32 * u.b + 8 * u.l4, io.vec, x);
+        kv_store_n<8>(ftype, io.x, (int64_t)(t0 + u.tok) * io.x_token + head * io.x_head + 32 * u.b + 8 * u.l4, io.vec, x);
     }
   }
 }
 
 template <int TK, int TV, int NB>
 __global__ void __launch_bounds__(256)
-kv_load_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int64_t t, int span, int first) {
+kv_load_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int t, int span, int first) {
   __shared__ KvTokens s_tok;
   __shared__ __align__(16) uint8_t s_tile[NB * 32 * KV_PITCH];
-  const int64_t t0 = (int64_t)blockIdx.x * span;
+  const int t0 = blockIdx.x * span;
   t = min(t, t0 + span);
   if (blockIdx.z + first == 0) kv_load_side<TK, NB, false>(k, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
   else kv_load_side<TV, NB, true>(v, ftype, slots, t, t0, blockIdx.y, s_tok, s_tile);
@@ -156,13 +145,13 @@ kv_load_kernel(KvIo k, KvIo v, int ftype, const int64_t* __restrict__ slots, int
 template <int TK, int TV, int NB>
 static hipError_t kv_launch(const KvArgs& a, bool load, hipStream_t st) {
   const KvIo k = kv_io(a, false), v = kv_io(a, true);
-  const int span = kv_span(a.t, a.heads);
+  const int span = kv_span(a.t, a.heads, !load && TV == FT_Q8_0 ? 3 : 4);
   const unsigned tiles = (unsigned)((a.t + span - 1) / span);
   if (!load) {
-    kv_store_kernel<TK, TV, NB><<<dim3(tiles, a.heads, 2), 256, 0, st>>>(k, v, a.ftype, a.slots, a.t, span);
+    kv_store_kernel<TK, TV, NB><<<dim3(tiles, a.heads, 2), 256, 0, st>>>(k, v, a.ftype, a.slots, (int)a.t, span);
   } else {
     const int first = a.k ? 0 : 1;
-    kv_load_kernel<TK, TV, NB><<<dim3(tiles, a.heads, (a.k ? 1 : 0) + (a.v ? 1 : 0)), 256, 0, st>>>(k, v, a.ftype, a.slots, a.t, span,
+    kv_load_kernel<TK, TV, NB><<<dim3(tiles, a.heads, (a.k ? 1 : 0) + (a.v ? 1 : 0)), 256, 0, st>>>(k, v, a.ftype, a.slots, (int)a.t, span,
                                                                                                   first);
   }
   return hipGetLastError();

@@ -85,7 +85,7 @@ __device__ __forceinline__ uint32_t kv_quantize(const float (&v)[8], int l4, uin
 }
 
 // this lane's token's slot
-__device__ __forceinline__ int64_t kv_slot(const int64_t* slots, int64_t t0, int64_t t) {
+__device__ __forceinline__ int64_t kv_slot(const int64_t* slots, int t0, int t) {
   const int lane = threadIdx.x & 63;
   return t0 + lane < t ? slots[t0 + lane] : -1;
 }
@@ -101,8 +101,9 @@ __device__ __forceinline__ uint64_t cover16(uint64_t m) {   // bits j .. j+15 of
   return m | (m << 8);
 }
 // The tile's slots, and which of its tokens start a run that fills 16 slots from a
-// multiple of 16 on.  Every wave computes the same masks.
-template <class IO>
+// multiple of 16 on.  Every wave computes the same masks.  LIST: the tokens that no run covers are listed, where there are any
+// (unconditionally, and for keys too, it took 3 % of an aligned prompt's store).
+template <bool LIST, class IO>
 __device__ __forceinline__ uint64_t kv_runs(const IO& io, int64_t s, int head_bytes, int head, KvTokens& tk, uint64_t& valid) {
   const int lane = threadIdx.x & 63;
   if (s >= io.n_slot) s = -1;
@@ -121,7 +122,7 @@ __device__ __forceinline__ uint64_t kv_runs(const IO& io, int64_t s, int head_by
   run &= (next >> 13) & (next >> 14) & (next >> 15);
   run &= __ballot(s >= 0 && (s & 15) == 0 && lane <= 48);
   const uint64_t rest = valid & ~cover16(run);
-  if (threadIdx.x < 64 && ((rest >> lane) & 1)) tk.rest[__popcll(rest & ((1ull << lane) - 1))] = (uint8_t)lane;
+  if (LIST && rest != 0 && threadIdx.x < 64 && ((rest >> lane) & 1)) tk.rest[__popcll(rest & ((1ull << lane) - 1))] = (uint8_t)lane;
   return run;
 }
 
@@ -177,13 +178,13 @@ struct KvIo {
 };
 
 template <int T, int NB, bool V>
-__device__ __forceinline__ void kv_store_side(const KvIo& io, int ftype, const int64_t* slots, int64_t t, int64_t t0,
+__device__ __forceinline__ void kv_store_side(const KvIo& io, int ftype, const int64_t* slots, int t, int t0,
                                               int head, KvTokens& tk, uint8_t* s_tile) {
   constexpr int D = NB * 32;
   constexpr int ROWS = T == FT_Q8_0 ? D : D / 2;   // rows of the transposed tile
   constexpr int N = KV_AHEAD<NB>;
   const int tid = threadIdx.x;
-  const int nt = (int)min((int64_t)KV_TILE, t - t0);
+  const int nt = min(KV_TILE, t - t0);
   const int hb = kv_head_bytes(T, D, io.page), cb = kv_code_bytes(T, D, io.page);
   const int64_t my_slot = kv_slot(slots, t0, t);
   uint64_t valid, runs = 0;
@@ -194,11 +195,11 @@ __device__ __forceinline__ void kv_store_side(const KvIo& io, int ftype, const i
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const KvUnit u = kv_unit<NB>(it0 + n);
-      at[n] = min(t0 + u.tok, t - 1) * io.x_token + head * io.x_head + 32 * u.b + 8 * u.l4;
+      at[n] = (int64_t)min(t0 + u.tok, t - 1) * io.x_token + head * io.x_head + 32 * u.b + 8 * u.l4;
     }
     kv_load_raw<N>(ftype, io.x, at, io.vec, raw);
     if (it0 == 0) {
-      runs = kv_runs(io, my_slot, hb, head, tk, valid);
+      runs = kv_runs<V>(io, my_slot, hb, head, tk, valid);
       __syncthreads();
     }
 #pragma unroll
@@ -267,10 +268,13 @@ __device__ __forceinline__ void kv_store_side(const KvIo& io, int ftype, const i
 // Tokens that a workgroup takes.  Values of tokens that lie far apart are single bytes, and what a workgroup of 64 does
 // with them one after the other takes longer than all else: while there are CUs to spare it takes 16 or 4, at the
 // price of runs of 16 that two workgroups share (stored and read back, with queries turned: 44 tokens of one head of
-// 256 92 -> 9.7 us, 137 tokens of 4 heads of 256 56 -> 10.4, 24 of 4 heads of 128 20 -> 7.1)
-inline int kv_span(int64_t t, int heads) {
+// 256 92 -> 9.7 us, 137 tokens of 4 heads of 256 56 -> 10.4, 24 of 4 heads of 128 20 -> 7.1).  16 tokens up to
+// halves / 2 workgroups a CU: two, but one and a half where Q8_0 values are stored alone, whose single bytes cost the
+// most (first slots 0 and 5; 2000 tokens of 4 heads of 128: by 16 tokens 5.0 and 9.2 us, by 64 5.4 and 6.9; 760 of 8
+// heads: 4.6 and 7.9, 5.5 and 6.8).
+inline int kv_span(int64_t t, int heads, int halves = 4) {
   if ((t + 3) / 4 * heads <= ftk_num_cus()) return 4;
-  return (t + 15) / 16 * heads <= 2 * ftk_num_cus() ? 16 : KV_TILE;
+  return (t + 15) / 16 * heads * 2 <= (int64_t)halves * ftk_num_cus() ? 16 : KV_TILE;
 }
 
 inline KvIo kv_io(const KvArgs& a, bool v) {

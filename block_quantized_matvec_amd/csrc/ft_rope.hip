@@ -222,8 +222,8 @@ kv_store_rope_kernel(RopeTurn c, RopeRows k, RopeRows q, RopeOut out, KvIo kio, 
   const uint32_t wg = rope_group();
   if (wg < v_groups) {
     const uint32_t tile = wg / vio.heads;
-    const int64_t t0 = (int64_t)tile * span;
-    kv_store_side<TV, NB, true>(vio, c.ftype, slots, min(c.t, t0 + span), t0, (int)(wg - tile * vio.heads), s_tok, s_tile);
+    const int t0 = (int)tile * span;
+    kv_store_side<TV, NB, true>(vio, c.ftype, slots, min((int)c.t, t0 + span), t0, (int)(wg - tile * vio.heads), s_tok, s_tile);
     return;
   }
   uint32_t task = (wg - v_groups) * 4 + wave_id();
