@@ -578,12 +578,15 @@ def attn_kv(cache: KvCache, q: torch.Tensor, table: torch.Tensor, kv_len: torch.
 # rotary positions
 # ---------------------------------------------------------------------------
 def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
-               original: int = 8192, low: float = 1.0, high: float = 32.0):
+               original: int = 8192, low: float = 1.0, high: float | None = None):
     """(freqs, scale) for rope_table: the angles per position of rot_dim / 2 pairs, a list of floats, and the factor of
     their cosines and sines.  scaling stretches positions past the `original` ones that a model was trained on by
-    `factor`: "linear" (all pairs alike), "ntk" (by the base), "blend" (pairs that turn fewer than `low` times over the
-    original positions stretch, those of more than `high` times do not, linear between: by turns), "ramp" (the same,
-    linear by the pair's number, with the cosines and sines scaled by 0.1 ln(factor) + 1)."""
+    `factor`: "linear" (all pairs alike), "ntk" (by the base, NTK-aware), "blend" (pairs that turn fewer than `low` times over
+    the original positions stretch, those of more than `high` (default: 4) times do not, linear between: by turns; model
+    configurations call this form "llama3"), "ramp" (the same, `high` 32 by default, linear by the pair's number, with the
+    cosines and sines scaled by 0.1 ln(factor) + 1: YaRN, Peng et al. 2023)."""
+    if high is None:
+        high = 4.0 if scaling == "blend" else 32.0
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even")
     if not base > 1 or not factor > 0:
