@@ -8,7 +8,7 @@
 //         q = clamp(round_half_away(x / d), -8, 7)
 // (d limited to the largest finite fp16; a zero d gives zero codes.)
 //
-// A workgroup takes 64 consecutive tokens of one head and of K or V; four lanes hold a
+// A workgroup takes 64, 16 or 4 consecutive tokens (kv_span) of one head and of K or V; four lanes hold a
 // block, eight elements each, so amax (or m) meets in two DPP steps, and a wave takes four
 // tokens of each of its blocks.  K codes go straight to the page, eight at a time.  V is
 // held transposed (a row per element, the page's keys side by side: the operand order of
@@ -17,13 +17,13 @@
 // consecutive tokens fill 16 consecutive slots from a multiple of 16 on; other tokens'
 // codes are single bytes.
 //
-// At a decode step both are launch and latency (4 us each).  8192 bf16 tokens of 8 heads
-// of 128, K in Q8_0 and V in Q4_0 (33 MB of rows, 14 MB of cache): reading back 9.3 us,
-// at the rate of a copy; writing 15 us, of which vector instructions issue for 9, 170 per
+// At a decode step both are launch and latency (3.5 us each).  8192 bf16 tokens of 8 heads
+// of 128, K in Q8_0 and V in Q4_0 (33 MB of rows, 14 MB of cache), first slot a multiple of 16: reading
+// back 9.5 us, at the rate of a copy; writing 13.7 us, of which vector instructions issue for 9, 170 per
 // eight elements and wave, while the waves wait for half of their time (208 instructions, and
 // 18 us, while every value near a half-integer divided; byte writes to LDS in place of the
-// exchange between lanes: 17.6 and 12.6 us).  fp32 rows, twice the bytes: 36 us together,
-// 4.5 TB/s.
+// exchange between lanes: 17.6 and 12.6 us).  From slot 5 on, where a quarter of V leaves and
+// returns as single bytes, 15.9 and 12.0.  fp32 rows, twice the bytes, K in Q4_0 and V in Q8_0: 16 and 18.
 #include "ft_kv_store.h"
 
 namespace ftk {

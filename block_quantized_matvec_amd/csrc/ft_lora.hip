@@ -16,7 +16,7 @@
 // with bf16, are one product and exact.  h stays in fp32 between the launches.
 //
 // Bound by memory: x, y, out and the rows of A and B that the tokens name.  4096 fp32 tokens,
-// 4096 -> 14336, rank 64, bf16 weights (540 MB): 118 us (4.6 TB/s; a 2 GiB copy 5.0), of which 99 the
+// 4096 -> 14336, rank 64, bf16 weights (540 MB): 116 us (4.7 TB/s; a 2 GiB copy 5.0), of which 97 the
 // second product, 19 the first.  1500 bf16 tokens of 16 adapters in any order, 14336 -> 4096, ranks
 // 8 to 64 (110 MB): 41 us, a third of it two chains of dependent loads (tile, tokens, rows) and the sort.
 // 48 tokens of 32 adapters, ranks 8 to 64, fp16 weights, 4096 -> 14336: 25 us; B's rows of 8 to 32 ranks lie
@@ -578,7 +578,7 @@ lora_plan_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ ra
 struct LoraPlan {
   int parts, part_k, tiles, sixteens;   // tiles, and groups of 16 tokens, that there can be
   bool sorts;          // tiles from a plan, not from the ids
-  bool full;           // tiles hold more than 16 tokens on average
+  bool full;           // tiles hold more than 16 tokens on average, if every adapter is named
   int64_t likely;      // tiles that probably hold tokens
   size_t h, order, list, total;
 };

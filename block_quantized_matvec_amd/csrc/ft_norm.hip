@@ -18,8 +18,11 @@
 // Bound by memory once there are rows for the chip (a 2 GiB copy moves 5.0 TB/s here): 8192 rows of 4096,
 // bf16, both norms and the residual 46-52 us (5.2-5.8 TB/s; 91 with two chunks per thread and loads that
 // waited for each other); fp32 to Q8_K blocks 82 us (5.4); 8192 rows of 2048 fp32 41 us (64 with the registers
-// held to eight waves per SIMD, which spilled); 1500 layer-normed rows of 5002 fp16 with a gate 21 us (two
-// rounds of workgroups, the second half full).  One row of 4096: 3.3 us, the launch and two memory latencies.
+// held to eight waves per SIMD, which spilled).  1500 layer-normed rows of 5002 fp16 with a gate 21 us, 3.5 TB/s: two
+// sums one after the other, each with a barrier, and 8 us of vector issue, which the three workgroups that a CU holds do
+// not hide.  One row of 4096: 2.8 us, the launch and two memory latencies.  Wide bf16 rows with a residual, 134 MB each: 2048 of 8200
+// 29 us (two chunks a thread, half of them empty), 1024 of 16384 27, 512 of 32768 36 and 1024 of 16390 65 (four chunks, whose
+// registers spill to memory: 17 to 29 of a thread, 25 to 121 where the width is no multiple of eight).
 #include "ft_kv.h"
 #include "ft_rowstat.h"
 #include "ft_internal.h"

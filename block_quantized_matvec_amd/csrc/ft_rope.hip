@@ -19,8 +19,9 @@
 //
 // Bound by memory: 6000 bf16 tokens of 20 heads of 256 (126 MB) 25 us, 5.0 TB/s, a large copy's rate.
 // 8192 tokens of 32 query and 8 key/value heads of 128 in bf16, K to Q8_0 and V to Q4_0 (182 MB): 44 us in one
-// launch (15 for the plain store, 27 for as many queries alone); with the values' workgroups
-// spread between the others 48.  At a decode step (24 tokens, norms of every head) 3.9 us, the launch and
+// launch (14 for the plain store, 27 for as many queries alone); with the values' workgroups
+// spread between the others 48.  6000 bf16 tokens of 20 heads of 128, normed (64 MB): 18 us, the norm's 64-bit sums on top of
+// the loads.  A table of 131072 positions by 64 pairs (67 MB): 27 us, its sines and cosines in 64 bits.  At a decode step (24 tokens, norms of every head) 3.9 us, the launch and
 // three memory latencies: positions and slots, the table's row beside the values, the stores.
 #include "ft_kv_store.h"
 #include "ft_rowstat.h"
