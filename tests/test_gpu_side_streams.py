@@ -96,3 +96,35 @@ def test_a_handle_is_enough():
     got = ft.quantize_act("Q8_1", x, stream=SimpleNamespace(cuda_stream=stream.cuda_stream))
     torch.cuda.synchronize()
     assert torch.equal(got, ft.quantize_act("Q8_1", x))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_the_current_stream_stays(name):
+    """Whatever the call's stream, the default one among them, and where the call is refused."""
+    need_gpu()
+    f, default = calls()[name], torch.cuda.default_stream()
+    want = f(None)
+    torch.cuda.synchronize()
+    mine = torch.cuda.Stream()
+    with torch.cuda.stream(mine):
+        for stream in (default, SimpleNamespace(cuda_stream=default.cuda_stream, device=default.device), mine, None):
+            got = f(stream)
+            assert torch.cuda.current_stream() == mine
+            torch.cuda.synchronize()
+            for a, b in zip(*(t if isinstance(t, tuple) else (t,) for t in (want, got))):
+                assert a is b is None or torch.equal(a, b)
+        with pytest.raises((AttributeError, TypeError, ValueError)):
+            f("no stream")
+        assert torch.cuda.current_stream() == mine
+    assert torch.cuda.current_stream() == default
+
+
+def test_a_refused_call_leaves_the_stream():
+    need_gpu()
+    x, stream = some(T, W), own_stream()
+    before = torch.cuda.current_stream()
+    with pytest.raises(ft.FtError):
+        ft.norm(x, act="Q8_1", eps=-1.0, stream=stream)
+    with pytest.raises(ValueError):
+        ft.lora(x, some(3, 8, W), some(3, 96, 8), some(T, dtype=torch.int32), out=some(T, 95), stream=stream)
+    assert torch.cuda.current_stream() == before
