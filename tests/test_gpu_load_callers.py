@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from block_quantized_matvec_amd import ft
-from tests.gpu_util import need_gpu
+from tests.gpu_util import need_gpu, own_stream
 
 pytestmark = pytest.mark.gpu
 
@@ -44,7 +44,7 @@ class Handle:
 def test_a_stream_is_its_device_and_handle(stored):
     cache, slots = stored
     torch.cuda.synchronize()
-    stream = torch.cuda.Stream()
+    stream = own_stream()
     k, v = ft.kv_load(cache, slots, stream=Handle(stream))
     stream.synchronize()
     assert torch.equal(k, torch.full_like(k, 127.0)) and torch.equal(v, k)

@@ -105,7 +105,7 @@ def test_the_current_stream_stays(name):
     f, default = calls()[name], torch.cuda.default_stream()
     want = f(None)
     torch.cuda.synchronize()
-    mine = torch.cuda.Stream()
+    mine = own_stream()
     with torch.cuda.stream(mine):
         for stream in (default, SimpleNamespace(cuda_stream=default.cuda_stream, device=default.device), mine, None):
             got = f(stream)
